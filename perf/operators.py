@@ -1,0 +1,395 @@
+"""Measured cases of the paged 4-bit KV cache: writing it, reading it back, and attention over it.
+
+Cache format (what the plain forms below compute in elementary torch operations).  A row is the D channels of one
+(token, K or V, kv head), cut into groups of G channels.  Per group, in fp32, every operation rounded on its own:
+
+    lo = fp16(min x),  s = fp16((max x - min x) * fp32(1/15)),  inv = 1 / s (0 where s is 0),
+    code = clamp(round_half_even((x - lo) * inv), 0, 15),  the code stands for  lo + code * s.
+
+Codes live in pages of P tokens, uint8 [n_pages][2][H][P*D/2], K and V halves ordered for the attention that reads
+them (pack_k, pack_v); (s, lo) pairs live in fp16 [n_pages][2][H][D/G][P][2].  Slot = page * P + token in page.
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+
+# ------------------------------------------------------------------ the cases
+
+def listed():
+    bf, hf = "bf16", "f16"
+    return [
+        # one new token for each of 64 running sequences, 8 kv heads of 128 channels: pure latency
+        dict(name="write_step", kind="write", tokens=64, H=8, D=128, G=64, P=64, dtype=bf, scattered=True),
+        # one layer's K/V of a 32K prompt (the 70B-class shape, 1024 channels), arriving from prefill
+        dict(name="write_prompt", kind="write", tokens=32768, H=8, D=128, G=64, P=64, dtype=hf, scattered=False),
+        # an odd-length prefix of a small-head model with fine groups, read back to be sent away
+        dict(name="read_odd", kind="read", tokens=1001, H=5, D=64, G=32, P=16, dtype=hf),
+        # one layer of an 80,000-token context read back whole (the 34B-class shape)
+        dict(name="read_long", kind="read", tokens=80000, H=8, D=128, G=64, P=64, dtype=bf),
+        # a first reply token after a short prompt: one sequence, a few hundred keys
+        dict(name="decode_short", kind="attn", B=1, nq=1, kv=300, ragged=False, H=8, R=4, D=128, G=64, P=64,
+             window=0, softcap=0.0, dtype=bf),
+        # one user with an 80,000-token context
+        dict(name="decode_long", kind="attn", B=1, nq=1, kv=80000, ragged=False, H=8, R=8, D=128, G=64, P=64,
+             window=0, softcap=0.0, dtype=hf),
+        # a serving batch, every sequence at its own length up to 8192
+        dict(name="decode_batch", kind="attn", B=64, nq=1, kv=8192, ragged=True, H=8, R=4, D=128, G=64, P=64,
+             window=0, softcap=0.0, dtype=bf),
+        # sliding-window heads of 64 channels with fine groups and capped logits, odd batch and ratio
+        dict(name="decode_window", kind="attn", B=33, nq=1, kv=6001, ragged=True, H=4, R=7, D=64, G=32, P=16,
+             window=2047, softcap=30.0, dtype=hf),
+        # five drafted tokens checked at once for each of 16 sequences
+        dict(name="verify_draft", kind="attn", B=16, nq=5, kv=4096, ragged=True, H=8, R=4, D=128, G=128, P=32,
+             window=0, softcap=0.0, dtype=bf),
+        # a step as a serving loop makes it: the new tokens written, then attended with all before them
+        dict(name="step_joint", kind="step", B=32, nq=1, kv=16384, ragged=True, H=8, R=8, D=128, G=64, P=64,
+             window=0, softcap=0.0, dtype=bf),
+        # a 512-token piece of a prompt over the prefix already cached, fp16
+        dict(name="prefill_piece", kind="attn", B=2, nq=512, kv=4096, ragged=True, H=8, R=4, D=128, G=64, P=64,
+             window=0, softcap=0.0, dtype=hf),
+        # a 2048-token piece at the end of an 8K prompt: the most arithmetic of all
+        dict(name="prefill_long", kind="attn", B=1, nq=2048, kv=8192, ragged=False, H=8, R=4, D=128, G=64, P=64,
+             window=0, softcap=0.0, dtype=bf),
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    D = rng.choice([64, 128, 128, 256])
+    G = rng.choice([g for g in (32, 64, 128) if g <= D])
+    H, P, dtype = rng.randint(1, 8), rng.choice([16, 32, 64, 128]), rng.choice(["bf16", "f16"])
+    base = dict(H=H, D=D, G=G, P=P, dtype=dtype)
+    kind = rng.choice(["write", "read", "decode", "decode", "verify", "prefill", "step"])
+    if kind == "write":
+        T = _log(rng, 1, 32768)
+        return dict(kind="write", tokens=T, scattered=T <= 512 and rng.random() < 0.5, **base)
+    if kind == "read":
+        return dict(kind="read", tokens=_log(rng, 1, 65536), **base)
+    base.update(R=rng.choice([1, 2, 3, 4, 5, 7, 8, 12]), ragged=rng.random() < 0.7,
+                window=rng.choice([0, 0, 0, _log(rng, 1, 4096)]), softcap=rng.choice([0.0, 0.0, 30.0, 50.0]))
+    if kind in ("decode", "step"):
+        B = _log(rng, 1, 64)
+        return dict(kind="attn" if kind == "decode" else "step", B=B, nq=1,
+                    kv=_log(rng, 1, min(80000, 262144 // B)), **base)
+    if kind == "verify":
+        B = _log(rng, 1, 32)
+        return dict(kind="attn", B=B, nq=rng.randint(2, 16), kv=_log(rng, 16, 131072 // B), **base)
+    B, most = _log(rng, 1, 4), 1 << 35  # of q rows * keys * channels: below the largest listed case
+    nq = _log(rng, 17, 1024 // B)
+    return dict(kind="attn", B=B, nq=nq, kv=_log(rng, nq, max(nq, min(8192, most // (B * nq * H * base["R"] * D)))), **base)
+
+
+# --------------------------------------------------- the format, in elementary operations
+
+def group_quantise(x, G):
+    """x [..., D] -> codes uint8 [..., D], scale and lo fp16 [..., D/G]."""
+    g = x.float().clamp(-65504.0, 65504.0).unflatten(-1, (-1, G))
+    mn, mx = g.amin(-1), g.amax(-1)
+    lo = mn.half()
+    s = ((mx - mn) * (1.0 / 15.0)).half()  # the constant rounds to fp32 in an fp32 product
+    s32 = s.float()
+    inv = torch.where(s32 > 0, (1.0 / s32.double()).float(), torch.zeros_like(s32))
+    c = torch.round((g - lo.float().unsqueeze(-1)) * inv.unsqueeze(-1)).clamp(0.0, 15.0)
+    return c.to(torch.uint8).flatten(-2), s, lo
+
+
+def pack_k(c):
+    """codes [..., D] -> bytes [..., D/2]: dword (h, t) of a row holds channels 32t + 8h .. + 7, low nibble first."""
+    b = c[..., 0::2] | (c[..., 1::2] << 4)
+    return b.unflatten(-1, (-1, 4, 4)).transpose(-3, -2).flatten(-3)
+
+
+def pack_v(c):
+    """codes [..., D] -> bytes [..., 16, D/32]: piece n holds channels n*D/16 .. (four tokens' pieces lie together)."""
+    b = c[..., 0::2] | (c[..., 1::2] << 4)
+    return b.unflatten(-1, (16, -1))
+
+
+def views(codes, c):
+    """The K view [pages][H][P][D/2] and the V view [pages][H][P/4][16][4][D/32] of a code pool."""
+    n, H, P, D = codes.shape[0], c["H"], c["P"], c["D"]
+    return codes[:, 0].view(n, H, P, D // 2), codes[:, 1].view(n, H, P // 4, 16, 4, D // 32)
+
+
+def write_plain(codes, params, c, k, v, slots):
+    page, off = slots // c["P"], slots % c["P"]
+    kc, ks, kl = group_quantise(k, c["G"])
+    vc, vs, vl = group_quantise(v, c["G"])
+    K, V = views(codes, c)
+    K[page, :, off] = pack_k(kc)
+    V[page, :, off // 4, :, off % 4] = pack_v(vc)
+    params[page, 0, :, :, off] = torch.stack([ks, kl], -1)
+    params[page, 1, :, :, off] = torch.stack([vs, vl], -1)
+
+
+def nibbles(b):
+    """bytes [..., n] -> codes [..., 2n], low nibble first."""
+    return torch.stack([b & 15, b >> 4], -1).flatten(-2)
+
+
+def values(code, p, G):
+    """codes [..., D], (s, lo) [..., D/G, 2] -> fp32 values."""
+    p = p.float()
+    return (code.float().unflatten(-1, (-1, G)) * p[..., 0:1] + p[..., 1:2]).flatten(-2)
+
+
+def read_plain(codes, params, c, slots):
+    page, off = slots // c["P"], slots % c["P"]
+    K, V = views(codes, c)
+    kb = K[page, :, off].unflatten(-1, (4, -1, 4)).transpose(-3, -2).flatten(-3)
+    vb = V[page, :, off // 4, :, off % 4].flatten(-2)
+    return (values(nibbles(kb), params[page, 0, :, :, off], c["G"]),
+            values(nibbles(vb), params[page, 1, :, :, off], c["G"]))
+
+
+def attend_plain(s):
+    c = s["case"]
+    q, table, lens, cu = s["q"], s["table"], s["lens"].long(), s["cu"].long()
+    B, H, R, D, P, nq = table.shape[0], c["H"], c["R"], c["D"], c["P"], s["max_q"]
+    T = table.shape[1] * P
+    slots = (table.long().unsqueeze(-1) * P + torch.arange(P, device=q.device)).flatten()
+    k, v = read_plain(s["codes"], s["params"], c, slots)  # [B*T][H][D]
+    k, v = (t.view(B, T, H, D).transpose(1, 2) for t in (k, v))
+    n = cu[1:] - cu[:-1]
+    i = torch.arange(nq, device=q.device)
+    real = i < n.unsqueeze(1)  # [B][nq]
+    idx = torch.where(real, cu[:-1].unsqueeze(1) + i, 0)
+    qp = q.float()[idx].view(B, nq, H, R, D).permute(0, 2, 3, 1, 4).reshape(B, H, R * nq, D)
+    x = torch.matmul(qp, k.transpose(-1, -2)) * s["scale"]
+    if c["softcap"] > 0:
+        x = c["softcap"] * torch.tanh(x / c["softcap"])
+    j = torch.arange(T, device=q.device)
+    pos = (lens - n).unsqueeze(1) + i  # [B][nq]
+    ok = (j <= pos.unsqueeze(-1)) & (j < lens.view(B, 1, 1)) & real.unsqueeze(-1)
+    if c["window"] > 0:
+        ok = ok & (j > pos.unsqueeze(-1) - c["window"])
+    x = x.view(B, H, R, nq, T).masked_fill_(~ok.view(B, 1, 1, nq, T), -math.inf)
+    m = x.amax(-1, keepdim=True)
+    m = torch.where(m == -math.inf, torch.zeros_like(m), m)
+    e = x.sub_(m).exp_()
+    l = e.sum(-1, keepdim=True)
+    o = torch.matmul(e.view(B, H, R * nq, T), v).view(B, H, R, nq, D) / torch.where(l > 0, l, torch.ones_like(l))
+    lse = (m + l.log()).squeeze(-1)
+    o = o.permute(0, 3, 1, 2, 4).reshape(B, nq, H * R, D)[real]
+    return o.to(q.dtype), lse.permute(0, 3, 1, 2).reshape(B, nq, H * R)[real]
+
+
+# --------------------------------------------------------------- inputs
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def make_kv(shape, dtype, g, is_key):
+    """K has a few channels that are large in every token, V is centred: what caches look like."""
+    x = torch.randn(shape, generator=g, device="cuda", dtype=torch.float32)
+    H, D = shape[-2:]
+    if is_key:
+        mean = torch.randn((H, D), generator=g, device="cuda") * 0.5
+        big = torch.rand((H, D), generator=g, device="cuda") < 0.03
+        x = x.add_(torch.where(big, mean * 12.0, mean))
+    return x.to(dtype)
+
+
+def make_pool(c, n_pages, g):
+    """A code pool and its parameters, every token of it quantised from drawn K and V."""
+    H, D, P = c["H"], c["D"], c["P"]
+    codes = torch.empty((n_pages, 2, H, P * D // 2), dtype=torch.uint8, device="cuda")
+    params = torch.empty((n_pages, 2, H, D // c["G"], P, 2), dtype=torch.float16, device="cuda")
+    piece = max(1, (1 << 26) // (P * H * D))  # pages at a time: bounded temporaries
+    for a in range(0, n_pages, piece):
+        b = min(n_pages, a + piece)
+        slots = torch.arange(a * P, b * P, device="cuda")
+        shape = (slots.numel(), H, D)
+        write_plain(codes, params, c, make_kv(shape, DT[c["dtype"]], g, True), make_kv(shape, DT[c["dtype"]], g, False), slots)
+    return codes, params
+
+
+def lengths(c, seed):
+    """Keys a sequence holds (queries included) and its queries."""
+    B, nq, kv = c["B"], c["nq"], c["kv"]
+    if not c["ragged"]:
+        return [kv] * B, [nq] * B
+    r = np.random.default_rng(B + nq)  # the queries' counts go by the case, so that outputs keep their shapes
+    n = [int(x) for x in r.integers(max(1, nq // 2), nq + 1, B)]
+    r = np.random.default_rng(1000 + seed)
+    lens = [max(int(x), m) for x, m in zip(r.integers(max(1, kv // 4), kv + 1, B), n)]
+    lens[int(r.integers(B))] = kv
+    return lens, n
+
+
+def prepare(case, seed):
+    c = dict(case)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    H, D, P = c["H"], c["D"], c["P"]
+    s = {"case": c, "dtype": DT[c["dtype"]]}
+    if c["kind"] in ("write", "read"):
+        T = c["tokens"]
+        n_pages = T if c.get("scattered") else -(-T // P)
+        if c["kind"] == "read":
+            s["codes"], s["params"] = make_pool(c, n_pages, g)
+        else:
+            s["codes"] = torch.zeros((n_pages, 2, H, P * D // 2), dtype=torch.uint8, device="cuda")
+            s["params"] = torch.zeros((n_pages, 2, H, D // c["G"], P, 2), dtype=torch.float16, device="cuda")
+            s["k"], s["v"] = make_kv((T, H, D), s["dtype"], g, True), make_kv((T, H, D), s["dtype"], g, False)
+        pages = torch.randperm(n_pages, generator=g, device="cuda")
+        t = torch.arange(T, device="cuda")
+        if c.get("scattered"):  # each token ends another sequence's last page
+            s["slots"] = pages[t] * P + torch.randint(0, P, (T,), generator=g, device="cuda")
+        else:
+            s["slots"] = pages[t // P] * P + t % P
+    else:
+        lens, n = lengths(c, seed)
+        B, M = c["B"], -(-max(lens) // P)
+        n_pages = sum(-(-l // P) for l in lens) + 1
+        s["codes"], s["params"] = make_pool(c, n_pages, g)
+        order = torch.randperm(n_pages, generator=g, device="cuda").to(torch.int32)
+        table = torch.zeros((B, M), dtype=torch.int32, device="cuda")
+        a = 0
+        for b, l in enumerate(lens):
+            m = -(-l // P)
+            table[b, :m] = order[a:a + m]
+            a += m
+        cu = np.concatenate([[0], np.cumsum(n)])
+        s.update(table=table, lens=torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                 cu=torch.tensor(cu, dtype=torch.int32, device="cuda"), max_q=max(n), scale=1.0 / math.sqrt(D),
+                 q=torch.randn((int(cu[-1]), H * c["R"], D), generator=g, device="cuda").to(s["dtype"]))
+        if c["kind"] == "step":
+            s["k"], s["v"] = make_kv((B, H, D), s["dtype"], g, True), make_kv((B, H, D), s["dtype"], g, False)
+            last = s["lens"].long() - 1
+            s["slots"] = table.long().gather(1, (last // P).unsqueeze(1)).squeeze(1) * P + last % P
+    if own:  # the handle and the workspace that a serving program keeps
+        import entropy_coding_02_amd as kvc
+        s["cache"] = kvc.Kv4Cache(H, D, n_pages, page_tokens=P, group=c["G"], codes=s["codes"], params=s["params"])
+        if "q" in s:
+            s["work"] = torch.empty(kvc.kv4_work_bytes(s["cache"], s["q"].shape[0], H * c["R"], c["B"], M, s["max_q"]),
+                                    dtype=torch.uint8, device="cuda")
+    return s
+
+
+# ------------------------------------------------------------------- a pass
+
+def run(state):
+    s = state
+    c = s["case"]
+    if own:
+        import entropy_coding_02_amd as kvc
+        if c["kind"] == "read":
+            return kvc.kv4_read(s["cache"], s["slots"], dtype=s["dtype"])
+        if "k" in s:
+            kvc.kv4_append(s["cache"], s["k"], s["v"], s["slots"])
+        if c["kind"] == "write":
+            return kvc.kv4_read(s["cache"], s["slots"], dtype=s["dtype"])
+        return kvc.kv4_attention(s["cache"], s["q"], s["table"], s["lens"], cu_q=s["cu"], max_q=s["max_q"],
+                                 window=c["window"], softcap=c["softcap"], scale=s["scale"], return_lse=True,
+                                 work=s["work"])
+    if "k" in s:
+        write_plain(s["codes"], s["params"], c, s["k"], s["v"], s["slots"])
+    if "q" in s:
+        return attend_plain(s)
+    k, v = read_plain(s["codes"], s["params"], c, s["slots"])
+    if s["dtype"] == torch.float16:  # a value can pass its group's largest by the scale's rounding
+        k, v = k.clamp(-65504.0, 65504.0), v.clamp(-65504.0, 65504.0)
+    return k.to(s["dtype"]), v.to(s["dtype"])
+
+
+def work(case):
+    c = case
+    H, D, G = c["H"], c["D"], c["G"]
+    row = D // 2 + 4 * (D // G)  # a cached row
+    if c["kind"] in ("write", "read"):
+        n = 2 * c["tokens"] * H
+        b = n * (2 * D + row) + 8 * c["tokens"]
+        return {"bytes": 2 * b if c["kind"] == "write" else b, "flops": n * D * (10 if c["kind"] == "write" else 2)}
+    lens, nqs = lengths(c, 0)
+    W, Hq = c["window"], H * c["R"]
+    keys = pairs = 0
+    for l, n in zip(lens, nqs):
+        pos = np.arange(l - n, l)
+        first = np.maximum(0, pos - W + 1) if W else np.zeros_like(pos)
+        keys += l - int(first[0])
+        pairs += int((pos - first + 1).sum())
+    b = 2 * keys * H * row + sum(nqs) * Hq * (4 * D + 4) + 4 * sum(-(-l // c["P"]) for l in lens)
+    if c["kind"] == "step":
+        b += 2 * c["B"] * H * (2 * D + row)
+    return {"bytes": b, "flops": 4 * pairs * Hq * D}
+
+
+# ------------------------------------------- the definition in 64 bits, written apart
+
+def _r32(x):
+    return x.float().double()
+
+
+def _r16(x):
+    return x.float().half().double()  # x holds fp32 values here: one rounding
+
+
+def _decode_rows(s, page, off, kv):
+    """Values [n][H][D] in float64 of the tokens (page, off), gathered code by code from the byte layout."""
+    c = s["case"]
+    H, D, P, G = c["H"], c["D"], c["P"], c["G"]
+    ch = torch.arange(D, device="cuda")
+    if kv == 0:
+        byte = off.view(-1, 1) * (D // 2) + 4 * ((ch % 32) // 8 * (D // 32) + ch // 32) + (ch % 8) // 2
+    else:
+        w = D // 16
+        byte = (off.view(-1, 1) // 4) * (2 * D) + (ch // w) * (D // 8) + (off.view(-1, 1) % 4) * (D // 32) + (ch % w) // 2
+    pool = s["codes"][:, kv]
+    heads = torch.arange(H, device="cuda")
+    raw = pool[page.view(-1, 1, 1), heads.view(1, H, 1), byte.view(-1, 1, D)]
+    code = torch.where(ch % 2 == 0, raw & 15, raw >> 4).double()
+    sc = s["params"][:, kv][page.view(-1, 1, 1), heads.view(1, H, 1), (ch // G).view(1, 1, D), off.view(-1, 1, 1)].double()
+    return sc[..., 1] + code * sc[..., 0]
+
+
+def _quantised(x, G):
+    """The values that x [n][H][D] stands for once written: the definition's fp32 steps carried out in float64."""
+    x = x.double().clamp(-65504.0, 65504.0)
+    n, H, D = x.shape
+    g = x.reshape(n, H, D // G, G)
+    lo, hi = g.min(-1, keepdim=True).values, g.max(-1, keepdim=True).values
+    s = _r16(_r32(_r32(hi - lo) * float(np.float32(1.0) / np.float32(15.0))))
+    lo = _r16(lo)
+    inv = torch.where(s > 0, _r32(1.0 / s), 0.0)
+    code = _r32(_r32(g - lo) * inv).round().clamp(0, 15)
+    return (lo + code * s).reshape(n, H, D)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    c = s["case"]
+    if c["kind"] == "write":
+        return tuple(_quantised(s[t], c["G"]) for t in ("k", "v"))
+    P = c["P"]
+    if c["kind"] == "read":
+        return tuple(_decode_rows(s, s["slots"] // P, s["slots"] % P, kv) for kv in (0, 1))
+    H, R, W = c["H"], c["R"], c["window"]
+    cu, outs, lses = s["cu"].tolist(), [], []
+    for b, l in enumerate(s["lens"].tolist()):
+        t = torch.arange(l, device="cuda")
+        page = s["table"][b].long()[t // P]
+        k, v = (_decode_rows(s, page, t % P, kv) for kv in (0, 1))
+        if c["kind"] == "step":
+            k[-1], v[-1] = _quantised(s["k"][b:b + 1], c["G"])[0], _quantised(s["v"][b:b + 1], c["G"])[0]
+        n = cu[b + 1] - cu[b]
+        q = s["q"][cu[b]:cu[b + 1]].double()
+        pos = torch.arange(l - n, l, device="cuda").view(n, 1)
+        ok = (t <= pos) & ((t > pos - W) if W > 0 else torch.ones_like(t, dtype=torch.bool))
+        o, e = torch.empty_like(q), torch.empty((n, H * R), dtype=torch.float64, device="cuda")
+        for h in range(H * R):
+            x = (q[:, h] @ k[:, h // R].T) * s["scale"]
+            if c["softcap"] > 0:
+                x = c["softcap"] * torch.tanh(x / c["softcap"])
+            x = torch.where(ok, x, -math.inf)
+            e[:, h] = torch.logsumexp(x, -1)
+            o[:, h] = torch.exp(x - e[:, h:h + 1]) @ v[:, h // R]
+        outs.append(o)
+        lses.append(e)
+    return torch.cat(outs), torch.cat(lses)
