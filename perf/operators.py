@@ -107,15 +107,16 @@ def pack_k(c):
 
 
 def pack_v(c):
-    """codes [..., D] -> bytes [..., 16, D/32]: piece n holds channels n*D/16 .. (four tokens' pieces lie together)."""
-    b = c[..., 0::2] | (c[..., 1::2] << 4)
-    return b.unflatten(-1, (16, -1))
+    """codes [..., D] -> bytes [..., 16, D/64, 2]: two-byte piece (n, u) holds channels 64u + 16i + n, i = 0 .. 3."""
+    c = c.unflatten(-1, (-1, 4, 16)).movedim(-1, -3)
+    return c[..., 0::2] | (c[..., 1::2] << 4)
 
 
 def views(codes, c):
-    """The K view [pages][H][P][D/2] and the V view [pages][H][P/4][16][4][D/32] of a code pool."""
+    """The K view [pages][H][P][D/2] and the V view [pages][H][P/4][16][D/64][4][2] of a code pool: four tokens'
+    pieces lie side by side."""
     n, H, P, D = codes.shape[0], c["H"], c["P"], c["D"]
-    return codes[:, 0].view(n, H, P, D // 2), codes[:, 1].view(n, H, P // 4, 16, 4, D // 32)
+    return codes[:, 0].view(n, H, P, D // 2), codes[:, 1].view(n, H, P // 4, 16, D // 64, 4, 2)
 
 
 def write_plain(codes, params, c, k, v, slots):
@@ -124,7 +125,7 @@ def write_plain(codes, params, c, k, v, slots):
     vc, vs, vl = group_quantise(v, c["G"])
     K, V = views(codes, c)
     K[page, :, off] = pack_k(kc)
-    V[page, :, off // 4, :, off % 4] = pack_v(vc)
+    V[page, :, off // 4, :, :, off % 4] = pack_v(vc)
     params[page, 0, :, :, off] = torch.stack([ks, kl], -1)
     params[page, 1, :, :, off] = torch.stack([vs, vl], -1)
 
@@ -144,9 +145,9 @@ def read_plain(codes, params, c, slots):
     page, off = slots // c["P"], slots % c["P"]
     K, V = views(codes, c)
     kb = K[page, :, off].unflatten(-1, (4, -1, 4)).transpose(-3, -2).flatten(-3)
-    vb = V[page, :, off // 4, :, off % 4].flatten(-2)
+    vn = nibbles(V[page, :, off // 4, :, :, off % 4]).movedim(-3, -1).flatten(-3)
     return (values(nibbles(kb), params[page, 0, :, :, off], c["G"]),
-            values(nibbles(vb), params[page, 1, :, :, off], c["G"]))
+            values(vn, params[page, 1, :, :, off], c["G"]))
 
 
 def attend_plain(s):
@@ -337,14 +338,15 @@ def _decode_rows(s, page, off, kv):
     H, D, P, G = c["H"], c["D"], c["P"], c["G"]
     ch = torch.arange(D, device="cuda")
     if kv == 0:
+        nib = ch % 2
         byte = off.view(-1, 1) * (D // 2) + 4 * ((ch % 32) // 8 * (D // 32) + ch // 32) + (ch % 8) // 2
     else:
-        w = D // 16
-        byte = (off.view(-1, 1) // 4) * (2 * D) + (ch // w) * (D // 8) + (off.view(-1, 1) % 4) * (D // 32) + (ch % w) // 2
+        nib = (ch // 16) % 2
+        byte = (off.view(-1, 1) // 4) * (2 * D) + (ch % 16) * (D // 8) + (ch // 64) * 8 + (off.view(-1, 1) % 4) * 2 + (ch % 64) // 32
     pool = s["codes"][:, kv]
     heads = torch.arange(H, device="cuda")
     raw = pool[page.view(-1, 1, 1), heads.view(1, H, 1), byte.view(-1, 1, D)]
-    code = torch.where(ch % 2 == 0, raw & 15, raw >> 4).double()
+    code = torch.where(nib == 0, raw & 15, raw >> 4).double()
     sc = s["params"][:, kv][page.view(-1, 1, 1), heads.view(1, H, 1), (ch // G).view(1, 1, D), off.view(-1, 1, 1)].double()
     return sc[..., 1] + code * sc[..., 0]
 
