@@ -20,7 +20,8 @@ LIB_PATH = os.path.join(_PKG, "libkvc.so")
 KVC_OK, KVC_ERR_ARG, KVC_ERR_CAPACITY, KVC_ERR_HIP = 0, -1, -2, -3
 KVC_DEV_NONFINITE, KVC_DEV_CORRUPT, KVC_DEV_PAYLOAD_OVERFLOW = 1, 2, 4
 KVC_DEV_BAD_CDF, KVC_DEV_BAD_CONTAINER, KVC_DEV_BAD_SYMBOL = 8, 16, 32
-KVC_F16, KVC_F32 = 0, 1
+KVC_DEV_BAD_INDEX = 64
+KVC_F16, KVC_F32, KVC_BF16 = 0, 1, 2
 
 EXPORTED = (
     "kvc_version", "kvc_status_string", "kvc_alphabet", "kvc_n_chunks", "kvc_n_slabs",
@@ -30,6 +31,8 @@ EXPORTED = (
     "kvc_int8_quantize", "kvc_int8_dequantize", "kvc_serialize_chunk", "kvc_quantize_levels",
     "kvc_decode_lanes", "kvc_delta_forward", "kvc_delta_inverse", "kvc_encode_noalloc",
     "kvc_stream_work_bytes", "kvc_stream_encode",
+    "kvc_kv4_codes_bytes", "kvc_kv4_params_bytes", "kvc_kv4_append", "kvc_kv4_read",
+    "kvc_kv4_work_bytes", "kvc_kv4_attention",
 )
 KVC_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -42,6 +45,32 @@ class KvcDesc(ctypes.Structure):
         ("chunk_tokens", ctypes.c_int32),
         ("cdf_chunks", ctypes.c_int32),
         ("bins", ctypes.POINTER(ctypes.c_int32)),
+    ]
+
+
+class KvcKv4Desc(ctypes.Structure):
+    _fields_ = [
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("group", ctypes.c_int32),
+        ("page_tokens", ctypes.c_int32),
+        ("n_pages", ctypes.c_int64),
+    ]
+
+
+class KvcKv4Attn(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+        ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+        ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+        ("kv_len", ctypes.c_void_p), ("cu_q", ctypes.c_void_p),
+        ("n_q", ctypes.c_int64),
+        ("n_seqs", ctypes.c_int32), ("n_q_heads", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("max_q", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("causal", ctypes.c_int32), ("window", ctypes.c_int32),
+        ("softcap", ctypes.c_float), ("scale", ctypes.c_float),
+        ("work", ctypes.c_void_p), ("work_bytes", ctypes.c_int64),
     ]
 
 
@@ -118,6 +147,19 @@ def _load():
         lib.kvc_stream_encode.restype = ctypes.c_int
         lib.kvc_stream_encode.argtypes = [D, I32, P, P, P, P, I32, P, I64, P, I64, P, P, P, P,
                                           CHUNK_FN, P]
+        K = ctypes.POINTER(KvcKv4Desc)
+        lib.kvc_kv4_codes_bytes.restype = I64
+        lib.kvc_kv4_codes_bytes.argtypes = [K]
+        lib.kvc_kv4_params_bytes.restype = I64
+        lib.kvc_kv4_params_bytes.argtypes = [K]
+        lib.kvc_kv4_append.restype = ctypes.c_int
+        lib.kvc_kv4_append.argtypes = [K, P, P, I64, I64, I64, I64, I64, I32, P, P, P, P, P]
+        lib.kvc_kv4_read.restype = ctypes.c_int
+        lib.kvc_kv4_read.argtypes = [K, P, P, P, I64, P, P, I64, I64, I64, I64, I32, P, P]
+        lib.kvc_kv4_work_bytes.restype = I64
+        lib.kvc_kv4_work_bytes.argtypes = [K, I64, I32, I32, I32, I32]
+        lib.kvc_kv4_attention.restype = ctypes.c_int
+        lib.kvc_kv4_attention.argtypes = [K, ctypes.POINTER(KvcKv4Attn), P, P, P, P]
         _lib = lib
     return _lib
 
@@ -405,3 +447,157 @@ def decode(buf: Buffers, out_dtype=KVC_F16, stream=None, payload=None, payload_b
     kvc_decode(d, buf.payload if payload is None else payload, buf.slab_off, buf.stream_len, buf.cdf,
                buf.max1, buf.dec_sym, buf.out, out_dtype, buf.dev_status, stream,
                payload_bytes=payload_bytes)
+
+
+# --------------------------------------------------- the resident 4-bit cache
+
+class Kv4Cache:
+    """One layer's paged 4-bit K/V pool: a kvc_kv4_desc, its two device buffers
+    and a status word.  Layouts as in kvc.h: codes uint8
+    [n_pages][2][H][P * D/2], params float16 [n_pages][2][H][D/G][P][2] (s, lo)."""
+
+    def __init__(self, n_kv_heads: int, head_dim: int, n_pages: int, page_tokens: int = 64, group: int = 64,
+                 codes=None, params=None, dev_status=None, device="cuda"):
+        import torch
+        self.c = KvcKv4Desc(n_kv_heads, head_dim, group, page_tokens, n_pages)
+        self.ref = ctypes.byref(self.c)
+        self.n_kv_heads, self.head_dim, self.group = n_kv_heads, head_dim, group
+        self.page_tokens, self.n_pages = page_tokens, n_pages
+        sizes = []
+        for fn in ("kvc_kv4_codes_bytes", "kvc_kv4_params_bytes"):
+            v = int(getattr(_load(), fn)(self.ref))
+            if v < 0:
+                raise KvcError(fn, v)
+            sizes.append(v)
+        if codes is None:
+            codes = torch.empty((n_pages, 2, n_kv_heads, page_tokens * head_dim // 2), dtype=torch.uint8, device=device)
+        if params is None:
+            params = torch.empty((n_pages, 2, n_kv_heads, head_dim // group, page_tokens, 2), dtype=torch.float16,
+                                 device=device)
+        for name, t, dt, nb in (("codes", codes, torch.uint8, sizes[0]), ("params", params, torch.float16, sizes[1])):
+            if t.dtype != dt or t.numel() * t.element_size() != nb:
+                raise ValueError(f"kvc: {name} must be {dt} of {nb} bytes")
+            _ptr(t)
+        if dev_status is None:
+            dev_status = torch.zeros(1, dtype=torch.int32, device=codes.device)
+        self.codes, self.params, self.dev_status = codes, params, dev_status
+
+
+def _kv4_dtype(dt):
+    import torch
+    try:
+        return {torch.float16: KVC_F16, torch.float32: KVC_F32, torch.bfloat16: KVC_BF16}[dt]
+    except KeyError:
+        raise ValueError(f"kvc: float16, bfloat16 or float32, not {dt}") from None
+
+
+def _rows(cache: Kv4Cache, name: str, t, heads: int, n: int):
+    """Pointer and strides of a [n][heads][D] tensor whose channels are contiguous."""
+    if not t.is_cuda:
+        raise ValueError("kvc: device tensors only (there is no CPU path)")
+    if t.dim() != 3 or t.shape[0] != n or t.shape[1] != heads or t.shape[2] != cache.head_dim:
+        raise ValueError(f"kvc: {name} must be [{n}][{heads}][{cache.head_dim}], not {list(t.shape)}")
+    if t.stride(2) != 1:
+        raise ValueError(f"kvc: the channels of {name} must be contiguous")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _ints(name: str, t, dt, shape):
+    if t.dtype != dt or tuple(t.shape) != shape:
+        raise ValueError(f"kvc: {name} must be {dt} of shape {list(shape)}, not {t.dtype} {list(t.shape)}")
+    return _ptr(t)
+
+
+def kv4_append(cache: Kv4Cache, k, v, slots, stream=None):
+    """Quantise k, v [T][H][D] (float16, bfloat16 or float32) into the slots
+    int64 [T] (page * page_tokens + token in page; negative: skipped)."""
+    import torch
+    n = k.shape[0]
+    if v.dtype != k.dtype:
+        raise ValueError("kvc: k and v must have one dtype")
+    kp, kts, khs = _rows(cache, "k", k, cache.n_kv_heads, n)
+    vp, vts, vhs = _rows(cache, "v", v, cache.n_kv_heads, n)
+    _check("kvc_kv4_append", _load().kvc_kv4_append(
+        cache.ref, kp, vp, n, kts, khs, vts, vhs, _kv4_dtype(k.dtype), _ints("slots", slots, torch.int64, (n,)),
+        cache.codes.data_ptr(), cache.params.data_ptr(), cache.dev_status.data_ptr(), _stream(stream)))
+
+
+def kv4_read(cache: Kv4Cache, slots, dtype=None, k=None, v=None, stream=None):
+    """The values at slots int64 [T], as (k, v) [T][H][D] of `dtype` (float16
+    unless given) or written into k and v (one dtype, channels contiguous)."""
+    import torch
+    if slots.dim() != 1:
+        raise ValueError("kvc: slots must be int64 [T]")
+    n = slots.shape[0]
+    if dtype is None:
+        dtype = torch.float16 if k is None and v is None else (v if k is None else k).dtype
+    shape = (n, cache.n_kv_heads, cache.head_dim)
+    k = torch.empty(shape, dtype=dtype, device=slots.device) if k is None else k
+    v = torch.empty(shape, dtype=dtype, device=slots.device) if v is None else v
+    if k.dtype != dtype or v.dtype != dtype:
+        raise ValueError("kvc: k and v must have one dtype")
+    kp, kts, khs = _rows(cache, "k", k, cache.n_kv_heads, n)
+    vp, vts, vhs = _rows(cache, "v", v, cache.n_kv_heads, n)
+    _check("kvc_kv4_read", _load().kvc_kv4_read(
+        cache.ref, cache.codes.data_ptr(), cache.params.data_ptr(), _ints("slots", slots, torch.int64, (n,)), n,
+        kp, vp, kts, khs, vts, vhs, _kv4_dtype(dtype), cache.dev_status.data_ptr(), _stream(stream)))
+    return k, v
+
+
+def kv4_work_bytes(cache: Kv4Cache, n_q: int, n_q_heads: int, n_seqs: int, max_pages: int, max_q: int) -> int:
+    """Workspace of a kv4_attention call: n_q query tokens in all, at most
+    max_q of one sequence, page tables of max_pages entries."""
+    v = int(_load().kvc_kv4_work_bytes(cache.ref, n_q, n_seqs, n_q_heads, max_pages, max_q))
+    if v < 0:
+        raise KvcError("kvc_kv4_work_bytes", v)
+    return v
+
+
+def kv4_attention(cache: Kv4Cache, q, page_table, kv_len, cu_q=None, max_q: Optional[int] = None, causal: bool = True,
+                  window: int = 0, softcap: float = 0.0, scale: Optional[float] = None, out=None,
+                  return_lse: bool = False, lse=None, work=None, stream=None):
+    """Attention of q [n_q][Hq][D] (float16 or bfloat16) over the cached keys:
+    the last query of sequence b stands at its last key.  page_table int32
+    [B][max_pages], kv_len int32 [B]; cu_q int32 [B + 1] bounds each
+    sequence's queries (at most max_q; n_q if not given), without it every
+    sequence has n_q / B.  `work`: uint8 of kv4_work_bytes, allocated if not
+    given.  Returns out, or (out, lse float32 [n_q][Hq])."""
+    import torch
+    if q.dim() != 3 or page_table.dim() != 2:
+        raise ValueError("kvc: q must be [n_q][Hq][D], page_table [B][max_pages]")
+    n_q, n_heads, _ = q.shape
+    B, max_pages = page_table.shape
+    if page_table.dtype != torch.int32 or not page_table.is_cuda or (max_pages > 1 and page_table.stride(1) != 1):
+        raise ValueError("kvc: page_table must be a device int32 tensor with contiguous rows")
+    if cu_q is None:
+        if B == 0 or n_q % B:
+            raise ValueError("kvc: without cu_q every sequence has the same number of queries")
+        if max_q is not None and max_q != n_q // B:
+            raise ValueError("kvc: without cu_q max_q is n_q / B")
+        max_q = n_q // B
+    elif max_q is None:
+        max_q = n_q
+    if out is None:
+        out = torch.empty((n_q, n_heads, cache.head_dim), dtype=q.dtype, device=q.device)
+    elif out.dtype != q.dtype:
+        raise ValueError("kvc: out must have q's dtype")
+    if lse is not None:
+        return_lse = True
+        if lse.dtype != torch.float32 or tuple(lse.shape) != (n_q, n_heads):
+            raise ValueError("kvc: lse must be float32 [n_q][Hq]")
+    elif return_lse:
+        lse = torch.empty((n_q, n_heads), dtype=torch.float32, device=q.device)
+    if work is None:
+        nb = kv4_work_bytes(cache, n_q, n_heads, B, max_pages, max_q)
+        work = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
+    qp, qts, qhs = _rows(cache, "q", q, n_heads, n_q)
+    op, ots, ohs = _rows(cache, "out", out, n_heads, n_q)
+    args = KvcKv4Attn(
+        qp, op, _ptr(lse), qts, qhs, ots, ohs, page_table.data_ptr(), page_table.stride(0),
+        _ints("kv_len", kv_len, torch.int32, (B,)), None if cu_q is None else _ints("cu_q", cu_q, torch.int32, (B + 1,)),
+        n_q, B, n_heads, max_pages, max_q, _kv4_dtype(q.dtype), causal, window, softcap,
+        cache.head_dim ** -0.5 if scale is None else scale, _ptr(work), 0 if work is None else work.numel() * work.element_size())
+    _check("kvc_kv4_attention", _load().kvc_kv4_attention(
+        cache.ref, ctypes.byref(args), cache.codes.data_ptr(), cache.params.data_ptr(), cache.dev_status.data_ptr(),
+        _stream(stream)))
+    return (out, lse) if return_lse else out

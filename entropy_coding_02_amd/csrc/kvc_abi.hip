@@ -8,6 +8,7 @@
 
 #include "kvc_common.h"
 #include "kvc_kernels.h"
+#include "kvc_kv4.h"
 
 // Encoder workspace of kvc_encode_noalloc: one array per GPU the library runs
 // on, held until the process ends, shared by every call on that GPU.  In host
@@ -72,6 +73,48 @@ int make_geometry(const kvc_desc *d, Geometry &g)
 }
 
 bool aligned(const void *ptr, uintptr_t a) { return ((uintptr_t)ptr & (a - 1)) == 0; }
+
+// Validate a 4-bit pool's descriptor; KVC_OK or KVC_ERR_ARG.
+int make_pool(const kvc_kv4_desc *d, Kv4Pool &p)
+{
+    if (!d || d->n_kv_heads < 1 || d->n_kv_heads > 1024) return KVC_ERR_ARG;
+    if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256) return KVC_ERR_ARG;
+    if ((d->group != 32 && d->group != 64 && d->group != 128) || d->group > d->head_dim) return KVC_ERR_ARG;
+    if (d->n_pages < 1 || d->n_pages > INT32_MAX) return KVC_ERR_ARG;
+    memset(&p, 0, sizeof(p));
+    for (p.pshift = 4; p.pshift <= 8 && d->page_tokens != 1 << p.pshift; ++p.pshift) {}
+    if (p.pshift > 8) return KVC_ERR_ARG;
+    p.n_pages = d->n_pages;
+    p.H = d->n_kv_heads;
+    p.D = d->head_dim;
+    p.G = d->group;
+    return KVC_OK;
+}
+
+bool kv4_dtype(int32_t dt) { return dt == KVC_F16 || dt == KVC_F32 || dt == KVC_BF16; }
+
+// The rows of one side of kvc_kv4_append / kvc_kv4_read.
+bool make_rows(Kv4Rows &r, const void *src, void *dst, int64_t ts, int64_t hs, int32_t dt)
+{
+    const void *ptr = src ? src : dst;
+    if (!aligned(ptr, dt == KVC_F32 ? 4 : 2)) return false;
+    const int per16 = dt == KVC_F32 ? 4 : 8;  // elements of a 16-byte piece
+    r.src = src;
+    r.dst = dst;
+    r.token_stride = ts;
+    r.head_stride = hs;
+    r.vec = aligned(ptr, 16) && ts % per16 == 0 && hs % per16 == 0;
+    return true;
+}
+
+// Sizes an attention call may have: tiles and positions are counted in 32 bits.
+bool kv4_attn_sizes(const Kv4Pool &p, int64_t n_q, int64_t n_seqs, int64_t n_q_heads, int64_t max_pages, int64_t max_q)
+{
+    return n_q >= 0 && n_q <= INT32_MAX && n_seqs >= 0 && max_q >= 0 && max_pages >= 0 && n_q_heads >= p.H &&
+           n_q_heads % p.H == 0 && (max_pages << p.pshift) <= ((int64_t)1 << 30) &&
+           max_q * (n_q_heads / p.H) <= ((int64_t)1 << 30) && n_q * n_q_heads <= ((int64_t)1 << 32) &&
+           n_seqs * p.H * ((max_q * (n_q_heads / p.H) + 15) / 16) < ((int64_t)1 << 30);
+}
 
 // The tensor as the CDF producers see it: its tables as chunks of S * Tc
 // tokens, one table each (the tables are the per-chunk CDFs of that coarser
@@ -696,6 +739,136 @@ int kvc_delta_inverse(const kvc_desc *desc, int32_t anchor_tokens, uint16_t *y, 
     if (!y || !aligned(y, 2)) return KVC_ERR_ARG;
     const bool vec = g.p.C % 8 == 0 && g.p.C <= 1024 && aligned(y, 16);
     return launch_status(launch_delta_inverse(y, g.p, anchor_tokens, vec, (hipStream_t)stream));
+}
+
+int64_t kvc_kv4_codes_bytes(const kvc_kv4_desc *desc)
+{
+    Kv4Pool p;
+    const int rc = make_pool(desc, p);
+    return rc != KVC_OK ? rc : (p.n_pages << p.pshift) * p.H * p.D;  // 2 x D/2 bytes a token and head
+}
+
+int64_t kvc_kv4_params_bytes(const kvc_kv4_desc *desc)
+{
+    Kv4Pool p;
+    const int rc = make_pool(desc, p);
+    return rc != KVC_OK ? rc : (p.n_pages << p.pshift) * p.H * (p.D / p.G) * 8;
+}
+
+int kvc_kv4_append(const kvc_kv4_desc *desc, const void *k, const void *v, int64_t n_tokens,
+                   int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                   int64_t v_head_stride, int32_t dtype, const int64_t *slots, uint8_t *codes,
+                   uint16_t *params, int32_t *dev_status, void *stream)
+{
+    Kv4Pool p;
+    const int rc = make_pool(desc, p);
+    if (rc != KVC_OK) return rc;
+    if (!kv4_dtype(dtype) || n_tokens < 0 || n_tokens > ((int64_t)1 << 40)) return KVC_ERR_ARG;
+    if (n_tokens == 0) return KVC_OK;
+    Kv4Rows kr, vr;
+    if (!k || !v || !slots || !codes || !params || !aligned(slots, 8) || !aligned(codes, 16) ||
+        !aligned(params, 16) || (dev_status && !aligned(dev_status, 4)) ||
+        !make_rows(kr, k, nullptr, k_token_stride, k_head_stride, dtype) ||
+        !make_rows(vr, v, nullptr, v_token_stride, v_head_stride, dtype))
+        return KVC_ERR_ARG;
+    p.codes = codes;
+    p.params = (uint32_t *)params;
+    p.status = dev_status;
+    return launch_status(launch_kv4_append(p, kr, vr, n_tokens, dtype, slots, (hipStream_t)stream));
+}
+
+int kvc_kv4_read(const kvc_kv4_desc *desc, const uint8_t *codes, const uint16_t *params,
+                 const int64_t *slots, int64_t n_tokens, void *k, void *v, int64_t k_token_stride,
+                 int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                 int32_t out_dtype, int32_t *dev_status, void *stream)
+{
+    Kv4Pool p;
+    const int rc = make_pool(desc, p);
+    if (rc != KVC_OK) return rc;
+    if (!kv4_dtype(out_dtype) || n_tokens < 0 || n_tokens > ((int64_t)1 << 40)) return KVC_ERR_ARG;
+    if (n_tokens == 0) return KVC_OK;
+    Kv4Rows kr = {}, vr = {};
+    if ((!k && !v) || !slots || !codes || !params || !aligned(slots, 8) || !aligned(codes, 16) ||
+        !aligned(params, 16) || (dev_status && !aligned(dev_status, 4)) ||
+        (k && !make_rows(kr, nullptr, k, k_token_stride, k_head_stride, out_dtype)) ||
+        (v && !make_rows(vr, nullptr, v, v_token_stride, v_head_stride, out_dtype)))
+        return KVC_ERR_ARG;
+    p.codes = (uint8_t *)codes;
+    p.params = (uint32_t *)params;
+    p.status = dev_status;
+    return launch_status(launch_kv4_read(p, kr, vr, n_tokens, out_dtype, slots, (hipStream_t)stream));
+}
+
+int64_t kvc_kv4_work_bytes(const kvc_kv4_desc *desc, int64_t n_q, int32_t n_seqs, int32_t n_q_heads,
+                           int32_t max_pages, int32_t max_q)
+{
+    Kv4Pool p;
+    const int rc = make_pool(desc, p);
+    if (rc != KVC_OK) return rc;
+    if (!kv4_attn_sizes(p, n_q, n_seqs, n_q_heads, max_pages, max_q)) return KVC_ERR_ARG;
+    const Kv4Plan plan = kv4_plan(n_seqs, p.H, n_q_heads / p.H, max_q, (int64_t)max_pages << p.pshift);
+    return plan.ns > 1 ? plan.ns * n_q * n_q_heads * (p.D + 2) * 4 : 0;
+}
+
+int kvc_kv4_attention(const kvc_kv4_desc *desc, const kvc_kv4_attn *args, const uint8_t *codes,
+                      const uint16_t *params, int32_t *dev_status, void *stream)
+{
+    Kv4Attn a;
+    memset(&a, 0, sizeof(a));
+    const int rc = make_pool(desc, a.pool);
+    if (rc != KVC_OK) return rc;
+    if (!args || !kv4_attn_sizes(a.pool, args->n_q, args->n_seqs, args->n_q_heads, args->max_pages, args->max_q))
+        return KVC_ERR_ARG;
+    if ((args->dtype != KVC_F16 && args->dtype != KVC_BF16) || args->window < 0 || (args->window && !args->causal) ||
+        !(args->softcap >= 0.0f) || args->softcap > 3.0e38f || !(args->scale == args->scale) ||
+        args->scale > 1.0e37f || args->scale < -1.0e37f)
+        return KVC_ERR_ARG;
+    if (args->n_q == 0 || args->n_seqs == 0 || args->max_q == 0) return KVC_OK;
+    if (!args->q || !args->out || !args->kv_len || !codes || !params || (!args->page_table && args->max_pages) ||
+        !aligned(args->q, 2) || !aligned(args->out, 2) || !aligned(args->lse, 4) || !aligned(args->kv_len, 4) ||
+        !aligned(args->page_table, 4) || !aligned(args->cu_q, 4) || !aligned(codes, 16) || !aligned(params, 16) ||
+        (dev_status && !aligned(dev_status, 4)))
+        return KVC_ERR_ARG;
+    if (!args->cu_q && (int64_t)args->n_seqs * args->max_q != args->n_q) return KVC_ERR_ARG;
+    const Kv4Plan plan = kv4_plan(args->n_seqs, a.pool.H, args->n_q_heads / a.pool.H, args->max_q,
+                                  (int64_t)args->max_pages << a.pool.pshift);
+    const int64_t part = plan.ns > 1 ? plan.ns * args->n_q * args->n_q_heads : 0;
+    if (part) {
+        if (!args->work || !aligned(args->work, 16)) return KVC_ERR_ARG;
+        if (args->work_bytes < part * (a.pool.D + 2) * 4) return KVC_ERR_CAPACITY;
+        a.part_o = (float *)args->work;
+        a.part_ml = a.part_o + part * a.pool.D;
+    }
+    a.pool.codes = (uint8_t *)codes;
+    a.pool.params = (uint32_t *)params;
+    a.pool.status = dev_status;
+    a.q = (const uint16_t *)args->q;
+    a.out = (uint16_t *)args->out;
+    a.lse = args->lse;
+    a.q_ts = args->q_token_stride;
+    a.q_hs = args->q_head_stride;
+    a.o_ts = args->out_token_stride;
+    a.o_hs = args->out_head_stride;
+    a.q_vec = aligned(a.q, 16) && a.q_ts % 8 == 0 && a.q_hs % 8 == 0;
+    a.o_vec = aligned(a.out, 8) && a.o_ts % 4 == 0 && a.o_hs % 4 == 0;
+    a.table = args->page_table;
+    a.table_stride = args->table_stride;
+    a.kv_len = args->kv_len;
+    a.cu_q = args->cu_q;
+    a.n_q = args->n_q;
+    a.B = args->n_seqs;
+    a.Hq = args->n_q_heads;
+    a.R = args->n_q_heads / a.pool.H;
+    a.max_pages = args->max_pages;
+    a.max_q = args->max_q;
+    a.causal = args->causal != 0;
+    // a window that reaches past every key is none
+    a.window = args->window >= (int64_t)args->max_pages << a.pool.pshift ? 0 : args->window;
+    a.softcap = args->softcap;
+    a.scale = args->scale;
+    a.ns = plan.ns;
+    a.tiles = plan.tiles;
+    return launch_status(launch_kv4_attention(a, args->dtype == KVC_BF16, (hipStream_t)stream));
 }
 
 }  // extern "C"

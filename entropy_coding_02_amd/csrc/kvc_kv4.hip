@@ -1,0 +1,407 @@
+// kvc_kv4.hip - writing tokens into the resident 4-bit cache and reading them
+// back.  Both are bound by memory: a row of D channels is 2D (16-bit) or 4D
+// bytes outside and D/2 + 4D/G bytes in the cache.
+//
+// Work is cut into quads of four consecutive tokens of one head, because four
+// tokens' V pieces lie side by side in a page: a quad whose slots are four
+// consecutive ones at a multiple of four (any run of a prompt) moves its V
+// codes 8 bytes at a time, any other quad 2 bytes at a time.
+#include "kvc_kernels.h"
+#include "kvc_kv4.h"
+
+namespace {
+
+typedef _Float16 half1;
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x)
+{
+    const int i = __builtin_bit_cast(int, x);
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, CTRL, 0xF, 0xF, false));
+}
+
+// Max over aligned runs of LANES lanes (4, 8 or 16), within a row of 16:
+// neighbours and pairs by quad_perm, then mirrored halves (whose quads
+// already agree).
+template <int LANES>
+__device__ __forceinline__ float run_max(float v)
+{
+    v = fmaxf(v, dpp<0xB1>(v));
+    v = fmaxf(v, dpp<0x4E>(v));
+    if (LANES >= 8) v = fmaxf(v, dpp<0x141>(v));
+    if (LANES >= 16) v = fmaxf(v, dpp<0x140>(v));
+    return v;
+}
+
+__device__ __forceinline__ float load1(const uint16_t *p, int64_t i, int dtype)
+{
+    if (dtype == KVC_F32) return ((const float *)p)[i];
+    const uint32_t b = p[i];
+    return dtype == KVC_F16 ? kvc_h2f(b) : __builtin_bit_cast(float, b << 16);
+}
+
+template <int DT>
+__device__ __forceinline__ void load8(const void *src, int64_t i, bool vec, float *x)
+{
+    if (!vec) {
+        for (int j = 0; j < 8; ++j) x[j] = load1((const uint16_t *)src, i + j, DT);
+    } else if (DT == KVC_F32) {
+        const float4 a = *(const float4 *)((const float *)src + i), b = *(const float4 *)((const float *)src + i + 4);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+        const u32x4 w = *(const u32x4 *)((const uint16_t *)src + i);
+        for (int j = 0; j < 4; ++j) {
+            x[2 * j] = DT == KVC_F16 ? kvc_h2f(w[j] & 0xFFFF) : __builtin_bit_cast(float, w[j] << 16);
+            x[2 * j + 1] = DT == KVC_F16 ? kvc_h2f(w[j] >> 16) : __builtin_bit_cast(float, w[j] & 0xFFFF0000u);
+        }
+    }
+}
+
+// A channel's part in its group's extremes: x clamped to the fp16 range, and
+// for a non-finite x an infinity that no clamped x reaches.
+__device__ __forceinline__ void clamp_in(float &x, float &hi, float &nlo)
+{
+    const bool fin = __builtin_fabsf(x) < __builtin_inff();
+    x = fminf(fmaxf(x, -65504.0f), 65504.0f);
+    hi = fmaxf(hi, fin ? x : __builtin_inff());
+    nlo = fmaxf(nlo, -x);
+}
+
+struct GroupScale {
+    uint32_t bits;  // s | lo << 16
+    float lo, inv;
+    bool bad;
+};
+
+__device__ __forceinline__ GroupScale group_scale(float hi, float nlo)
+{
+    GroupScale g;
+    g.bad = hi > 65504.0f;
+    const float d = hi + nlo;                     // max - min, one rounding
+    const uint32_t lob = kvc_f2h(-nlo), sb = kvc_f2h(d * (1.0f / 15.0f));
+    g.lo = kvc_h2f(lob);
+    const float s = kvc_h2f(sb);
+    g.inv = s > 0.0f ? 1.0f / s : 0.0f;
+    g.bits = sb | (lob << 16);
+    if (g.bad) {
+        g.bits = 0x7E00u << 16;
+        g.lo = g.inv = 0.0f;
+    }
+    return g;
+}
+
+__device__ __forceinline__ uint32_t code4(float x, const GroupScale &g)
+{
+    const float r = __builtin_rintf((x - g.lo) * g.inv);
+    return g.bad ? 0u : (uint32_t)fminf(fmaxf(r, 0.0f), 15.0f);
+}
+
+// The slots of a quad; a token that is past the end, skipped or out of the
+// pool has slot -1.
+struct Quad {
+    int64_t slot[4];
+    bool run;  // four consecutive slots from a multiple of four: one page, one V piece row
+};
+
+__device__ __forceinline__ Quad load_quad(const Kv4Pool &p, const int64_t *slots, int64_t t0, int64_t n, bool flag)
+{
+    Quad q;
+    const int64_t end = p.n_pages << p.pshift;
+    bool bad = false;
+    for (int i = 0; i < 4; ++i) {
+        int64_t s = t0 + i < n ? slots[t0 + i] : -1;
+        if (s >= end) bad = true, s = -1;
+        q.slot[i] = s;
+    }
+    if (bad && flag) kvc_flag(p.status, KVC_DEV_BAD_INDEX);
+    q.run = q.slot[0] >= 0 && (q.slot[0] & 3) == 0 && q.slot[1] == q.slot[0] + 1 && q.slot[2] == q.slot[0] + 2 &&
+            q.slot[3] == q.slot[0] + 3;
+    return q;
+}
+
+// K: a lane quantises 8 contiguous channels of one token into one dword; a
+// group is G/8 neighbouring lanes.
+template <int D, int G, int DT>
+__device__ __forceinline__ void append_k(const Kv4Pool &p, const Kv4Rows &r, int64_t n, const int64_t *slots, uint32_t item)
+{
+    const int i = item % (D / 8), tok = item / (D / 8) % 4;
+    const uint32_t qh = item / (D / 2);
+    const int head = qh % p.H;
+    const int64_t t = (int64_t)(qh / p.H) * 4 + tok;
+    if (t >= n) return;  // the D/8 lanes of a token leave together
+    const int64_t slot = slots[t];
+    if (slot < 0 || slot >= p.n_pages << p.pshift) {
+        if (slot >= 0 && i == 0) kvc_flag(p.status, KVC_DEV_BAD_INDEX);
+        return;
+    }
+    float x[8], hi = -__builtin_inff(), nlo = -__builtin_inff();
+    load8<DT>(r.src, t * r.token_stride + head * r.head_stride + 8 * i, r.vec, x);
+    for (int j = 0; j < 8; ++j) clamp_in(x[j], hi, nlo);
+    const GroupScale g = group_scale(run_max<G / 8>(hi), run_max<G / 8>(nlo));
+    uint32_t w = 0;
+    for (int j = 0; j < 8; ++j) w |= code4(x[j], g) << (4 * j);
+    const int P = 1 << p.pshift, off = (int)(slot & (P - 1));
+    const int64_t blk = kv4_block(p, slot >> p.pshift, 0, head);
+    *(uint32_t *)(p.codes + blk * (P * (D / 2)) + off * (D / 2) + 4 * ((i % 4) * (D / 32) + i / 4)) = w;
+    if (i % (G / 8) == 0) {
+        p.params[(blk * (D / G) + i / (G / 8)) * P + off] = g.bits;
+        if (g.bad) kvc_flag(p.status, KVC_DEV_NONFINITE);
+    }
+}
+
+// V: a lane quantises channels 64u + n + {0, 16, 32, 48} of the quad's four
+// tokens into four 16-bit pieces; a group of 64 is 16 lanes (the n), one of
+// 32 half of each lane's channels, one of 128 two runs of 16 lanes.
+template <int D, int G, int DT>
+__device__ __forceinline__ void append_v(const Kv4Pool &p, const Kv4Rows &r, int64_t n, const int64_t *slots, uint32_t item)
+{
+    constexpr int HALVES = G == 32 ? 2 : 1;
+    const int nn = item % 16, u = item / 16 % (D / 64);
+    const uint32_t qh = item / (D / 4);
+    const int head = qh % p.H;
+    const int64_t t0 = (int64_t)(qh / p.H) * 4;
+    if (t0 >= n) return;
+    const Quad q = load_quad(p, slots, t0, n, nn == 0 && u == 0);
+    uint32_t piece[4], bits[HALVES][4];
+    float x[4][4];
+    for (int k = 0; k < 4; ++k)
+        for (int j = 0; j < 4; ++j)
+            x[k][j] = q.slot[k] < 0 ? 0.0f
+                                    : load1((const uint16_t *)r.src, (t0 + k) * r.token_stride + head * r.head_stride + 64 * u + 16 * j + nn, DT);
+    bool bad = false;
+    for (int k = 0; k < 4; ++k) {
+        piece[k] = 0;
+        for (int f = 0; f < HALVES; ++f) {
+            float hi = -__builtin_inff(), nlo = -__builtin_inff();
+            for (int j = f * 4 / HALVES; j < (f + 1) * 4 / HALVES; ++j) clamp_in(x[k][j], hi, nlo);
+            hi = run_max<16>(hi), nlo = run_max<16>(nlo);
+            if (G == 128) {
+                hi = fmaxf(hi, __shfl_xor(hi, 16, 64));
+                nlo = fmaxf(nlo, __shfl_xor(nlo, 16, 64));
+            }
+            const GroupScale g = group_scale(hi, nlo);
+            for (int j = f * 4 / HALVES; j < (f + 1) * 4 / HALVES; ++j) piece[k] |= code4(x[k][j], g) << (4 * j);
+            bits[f][k] = g.bits;
+            bad |= g.bad;
+        }
+    }
+    const int P = 1 << p.pshift;
+    const bool owner = nn == 0 && (G < 128 || u % 2 == 0);
+    if (bad && owner) kvc_flag(p.status, KVC_DEV_NONFINITE);
+    const int grp = 64 * u / G;
+    if (q.run) {
+        const int off = (int)(q.slot[0] & (P - 1));
+        const int64_t blk = kv4_block(p, q.slot[0] >> p.pshift, 1, head);
+        const u32x2 w = {piece[0] | piece[1] << 16, piece[2] | piece[3] << 16};
+        *(u32x2 *)(p.codes + blk * (P * (D / 2)) + (off / 4) * (2 * D) + nn * (D / 8) + u * 8) = w;
+        if (owner)
+            for (int f = 0; f < HALVES; ++f) {
+                const u32x4 b = {bits[f][0], bits[f][1], bits[f][2], bits[f][3]};
+                *(u32x4 *)(p.params + (blk * (D / G) + grp + f) * P + off) = b;
+            }
+        return;
+    }
+    for (int k = 0; k < 4; ++k) {
+        if (q.slot[k] < 0) continue;
+        const int off = (int)(q.slot[k] & (P - 1));
+        const int64_t blk = kv4_block(p, q.slot[k] >> p.pshift, 1, head);
+        *(uint16_t *)(p.codes + blk * (P * (D / 2)) + (off / 4) * (2 * D) + nn * (D / 8) + u * 8 + (off % 4) * 2) =
+            (uint16_t)piece[k];
+        if (owner)
+            for (int f = 0; f < HALVES; ++f) p.params[(blk * (D / G) + grp + f) * P + off] = bits[f][k];
+    }
+}
+
+// Blocks 0 .. k_blocks - 1 write K, the rest V.
+template <int D, int G, int DT>
+__global__ __launch_bounds__(256) void k_kv4_append(Kv4Pool p, Kv4Rows k, Kv4Rows v, int64_t n, const int64_t *slots, uint32_t k_blocks)
+{
+    if (blockIdx.x < k_blocks)
+        append_k<D, G, DT>(p, k, n, slots, blockIdx.x * 256 + threadIdx.x);
+    else
+        append_v<D, G, DT>(p, v, n, slots, (blockIdx.x - k_blocks) * 256 + threadIdx.x);
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(void *dst, int64_t i, bool vec, const float *y)
+{
+    if (DT == KVC_F32) {
+        float *d = (float *)dst + i;
+        if (vec) {
+            *(float4 *)d = make_float4(y[0], y[1], y[2], y[3]);
+            *(float4 *)(d + 4) = make_float4(y[4], y[5], y[6], y[7]);
+        } else {
+            for (int j = 0; j < 8; ++j) d[j] = y[j];
+        }
+        return;
+    }
+    u32x4 w;
+    for (int j = 0; j < 4; ++j) {
+        float a = y[2 * j], b = y[2 * j + 1];
+        if (DT == KVC_F16) {
+            // a value past the fp16 range becomes its largest; NaN stays NaN
+            a = a > 65504.0f ? 65504.0f : (a < -65504.0f ? -65504.0f : a);
+            b = b > 65504.0f ? 65504.0f : (b < -65504.0f ? -65504.0f : b);
+            w[j] = kvc_f2h2(a, b);
+        } else {
+            w[j] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16;
+        }
+    }
+    uint16_t *d = (uint16_t *)dst + i;
+    if (vec) {
+        *(u32x4 *)d = w;
+    } else {
+        for (int j = 0; j < 8; ++j) d[j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+    }
+}
+
+// fp32(lo + code * s): the product of a 4-bit and an 11-bit integer is exact.
+__device__ __forceinline__ float value4(uint32_t code, uint32_t bits)
+{
+    return __builtin_fmaf((float)code, kvc_h2f(bits & 0xFFFF), kvc_h2f(bits >> 16));
+}
+
+template <int D, int G, int DT>
+__device__ __forceinline__ void read_k(const Kv4Pool &p, const Kv4Rows &r, int64_t n, const int64_t *slots, uint32_t item)
+{
+    const int i = item % (D / 8), tok = item / (D / 8) % 4;
+    const uint32_t qh = item / (D / 2);
+    const int head = qh % p.H;
+    const int64_t t = (int64_t)(qh / p.H) * 4 + tok;
+    if (t >= n) return;
+    const int64_t slot = slots[t];
+    float y[8] = {};
+    if (slot >= 0 && slot < p.n_pages << p.pshift) {
+        const int P = 1 << p.pshift, off = (int)(slot & (P - 1));
+        const int64_t blk = kv4_block(p, slot >> p.pshift, 0, head);
+        const uint32_t w = *(const uint32_t *)(p.codes + blk * (P * (D / 2)) + off * (D / 2) + 4 * ((i % 4) * (D / 32) + i / 4));
+        const uint32_t b = p.params[(blk * (D / G) + i / (G / 8)) * P + off];
+        for (int j = 0; j < 8; ++j) y[j] = value4(w >> (4 * j) & 15, b);
+    } else if (slot >= 0 && i == 0) {
+        kvc_flag(p.status, KVC_DEV_BAD_INDEX);
+    }
+    store8<DT>(r.dst, t * r.token_stride + head * r.head_stride + 8 * i, r.vec, y);
+}
+
+// A lane writes channels 8i .. 8i + 7 of the quad's four tokens: one nibble of
+// the pieces n = 8 (i % 2) .. + 7, which its neighbours read too (from L1).
+template <int D, int G, int DT>
+__device__ __forceinline__ void read_v(const Kv4Pool &p, const Kv4Rows &r, int64_t n, const int64_t *slots, uint32_t item)
+{
+    const int i = item % (D / 8);
+    const uint32_t qh = item / (D / 8);
+    const int head = qh % p.H;
+    const int64_t t0 = (int64_t)(qh / p.H) * 4;
+    if (t0 >= n) return;
+    const Quad q = load_quad(p, slots, t0, n, i == 0);
+    const int c = i / 2, u = c / 4, sh = 4 * (c % 4), grp = 8 * i / G;
+    const int P = 1 << p.pshift;
+    const int in_piece = 8 * (i % 2) * (D / 8) + u * 8;
+    uint32_t w[4][8], bits[4];
+    if (q.run) {
+        const int off = (int)(q.slot[0] & (P - 1));
+        const int64_t blk = kv4_block(p, q.slot[0] >> p.pshift, 1, head);
+        const uint8_t *src = p.codes + blk * (P * (D / 2)) + (off / 4) * (2 * D) + in_piece;
+        for (int j = 0; j < 8; ++j) {
+            const u32x2 d = *(const u32x2 *)(src + j * (D / 8));
+            for (int k = 0; k < 4; ++k) w[k][j] = d[k / 2] >> (16 * (k & 1) + sh) & 15;
+        }
+        const u32x4 b = *(const u32x4 *)(p.params + (blk * (D / G) + grp) * P + off);
+        for (int k = 0; k < 4; ++k) bits[k] = b[k];
+    } else {
+        for (int k = 0; k < 4; ++k) {
+            bits[k] = 0;
+            for (int j = 0; j < 8; ++j) w[k][j] = 0;
+            if (q.slot[k] < 0) continue;
+            const int off = (int)(q.slot[k] & (P - 1));
+            const int64_t blk = kv4_block(p, q.slot[k] >> p.pshift, 1, head);
+            const uint8_t *src = p.codes + blk * (P * (D / 2)) + (off / 4) * (2 * D) + in_piece + (off % 4) * 2;
+            for (int j = 0; j < 8; ++j) w[k][j] = *(const uint16_t *)(src + j * (D / 8)) >> sh & 15;
+            bits[k] = p.params[(blk * (D / G) + grp) * P + off];
+        }
+    }
+    for (int k = 0; k < 4; ++k) {
+        if (t0 + k >= n) break;
+        float y[8];
+        for (int j = 0; j < 8; ++j) y[j] = value4(w[k][j], bits[k]);
+        store8<DT>(r.dst, (t0 + k) * r.token_stride + head * r.head_stride + 8 * i, r.vec, y);
+    }
+}
+
+template <int D, int G, int DT>
+__global__ __launch_bounds__(256) void k_kv4_read(Kv4Pool p, Kv4Rows k, Kv4Rows v, int64_t n, const int64_t *slots, uint32_t k_blocks)
+{
+    if (blockIdx.x < k_blocks)
+        read_k<D, G, DT>(p, k, n, slots, blockIdx.x * 256 + threadIdx.x);
+    else
+        read_v<D, G, DT>(p, v, n, slots, (blockIdx.x - k_blocks) * 256 + threadIdx.x);
+}
+
+template <int D, int G>
+hipError_t move_rows(bool append, const Kv4Pool &p, const Kv4Rows &k, const Kv4Rows &v, int64_t n, int dt,
+                     const int64_t *slots, hipStream_t s)
+{
+    const uint32_t qh = (uint32_t)((n + 3) / 4 * p.H);
+    const uint32_t kb = append || k.dst ? (qh * (D / 2) + 255) / 256 : 0;
+    const uint32_t vb = append ? (qh * (D / 4) + 255) / 256 : (v.dst ? (qh * (D / 8) + 255) / 256 : 0);
+    const dim3 grid(kb + vb), block(256);
+#define KV4_CASE(KERNEL)                                                                       \
+    if (dt == KVC_F16) KERNEL<D, G, KVC_F16><<<grid, block, 0, s>>>(p, k, v, n, slots, kb);      \
+    else if (dt == KVC_BF16) KERNEL<D, G, KVC_BF16><<<grid, block, 0, s>>>(p, k, v, n, slots, kb); \
+    else KERNEL<D, G, KVC_F32><<<grid, block, 0, s>>>(p, k, v, n, slots, kb);
+    if (append) { KV4_CASE(k_kv4_append) } else { KV4_CASE(k_kv4_read) }
+#undef KV4_CASE
+    return hipGetLastError();
+}
+
+hipError_t move_piece(bool append, const Kv4Pool &p, const Kv4Rows &k, const Kv4Rows &v, int64_t n, int dt,
+                      const int64_t *slots, hipStream_t s)
+{
+    switch (p.D * 1000 + p.G) {
+    case 64032: return move_rows<64, 32>(append, p, k, v, n, dt, slots, s);
+    case 64064: return move_rows<64, 64>(append, p, k, v, n, dt, slots, s);
+    case 128032: return move_rows<128, 32>(append, p, k, v, n, dt, slots, s);
+    case 128064: return move_rows<128, 64>(append, p, k, v, n, dt, slots, s);
+    case 128128: return move_rows<128, 128>(append, p, k, v, n, dt, slots, s);
+    case 256032: return move_rows<256, 32>(append, p, k, v, n, dt, slots, s);
+    case 256064: return move_rows<256, 64>(append, p, k, v, n, dt, slots, s);
+    default: return move_rows<256, 128>(append, p, k, v, n, dt, slots, s);
+    }
+}
+
+// Rows from token t on.
+Kv4Rows rows_from(Kv4Rows r, int64_t t, int dt)
+{
+    const int64_t off = t * r.token_stride * (dt == KVC_F32 ? 4 : 2);
+    if (r.src) r.src = (const char *)r.src + off;
+    if (r.dst) r.dst = (char *)r.dst + off;
+    return r;
+}
+
+// A launch counts its items (at most n/4 * H * D/2) in 32 bits; more tokens
+// than that take several.
+hipError_t move_any(bool append, const Kv4Pool &p, const Kv4Rows &k, const Kv4Rows &v, int64_t n, int dt,
+                    const int64_t *slots, hipStream_t s)
+{
+    const int64_t most = ((int64_t)1 << 31) / ((int64_t)p.H * (p.D / 2)) * 4;
+    for (int64_t t = 0; t < n; t += most) {
+        const hipError_t e = move_piece(append, p, rows_from(k, t, dt), rows_from(v, t, dt),
+                                        n - t < most ? n - t : most, dt, slots + t, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_kv4_append(const Kv4Pool &pool, const Kv4Rows &k, const Kv4Rows &v, int64_t n_tokens,
+                             int dtype, const int64_t *slots, hipStream_t stream)
+{
+    return move_any(true, pool, k, v, n_tokens, dtype, slots, stream);
+}
+
+hipError_t launch_kv4_read(const Kv4Pool &pool, const Kv4Rows &k, const Kv4Rows &v, int64_t n_tokens,
+                           int dtype, const int64_t *slots, hipStream_t stream)
+{
+    return move_any(false, pool, k, v, n_tokens, dtype, slots, stream);
+}

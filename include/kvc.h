@@ -74,10 +74,11 @@ enum kvc_status {
 #define KVC_DEV_BAD_CDF 8          /* a CDF row the container cannot carry (kvc_serialize) */
 #define KVC_DEV_BAD_CONTAINER 16   /* a container that does not match the descriptor (kvc_deserialize) */
 #define KVC_DEV_BAD_SYMBOL 32      /* a symbol >= A, outside every CDF row (kvc_cdf, kvc_encode) */
+#define KVC_DEV_BAD_INDEX 64       /* a slot, page, length or query outside its buffer (kvc_kv4_*) */
 /* Bit 30 is used within a kvc_encode call (set and cleared on its stream); no
  * call leaves it set. */
 
-enum kvc_dtype { KVC_F16 = 0, KVC_F32 = 1 };
+enum kvc_dtype { KVC_F16 = 0, KVC_F32 = 1, KVC_BF16 = 2 /* the kvc_kv4 calls only */ };
 
 typedef struct kvc_desc {
     int32_t n_layers;     /* L, 1..256 */
@@ -426,6 +427,110 @@ int kvc_int8_quantize(const kvc_desc *desc, int32_t group, const uint16_t *kv, u
                       float *scale, uint8_t *zero_point, int32_t *dev_status, void *stream);
 int kvc_int8_dequantize(const kvc_desc *desc, int32_t group, const uint8_t *q, const float *scale,
                         const uint8_t *zero_point, void *out, int32_t out_dtype, void *stream);
+
+/*
+ * The resident 4-bit cache: what a serving loop attends over once a cache has
+ * arrived (kvc_decode) and while it grows.  Tokens are quantised to 4 bits as
+ * they are written into pages, read back as values when they are to be coded
+ * and sent again, and attended over in place.
+ *
+ * Format.  A row is the D = head_dim channels of one (token, K|V, kv head),
+ * cut into groups of G = group channels.  Per group, in fp32 with every
+ * operation rounded on its own and round half to even, x clamped to +-65504:
+ *   lo = fp16(min x),  s = fp16((max x - min x) * fp32(1/15)),  inv = 1 / s (0 if s = 0),
+ *   code = clamp(round((x - lo) * inv), 0, 15);  it stands for the value lo + code * s.
+ * A group holding Inf or NaN is stored as lo = NaN, s = 0 (its values read
+ * back as NaN, and only rows that attend to it see them) and sets
+ * KVC_DEV_NONFINITE.
+ *
+ * Layout (device memory, 16-byte aligned; H = n_kv_heads, P = page_tokens):
+ *   codes   [n_pages][2][H] blocks of P * D/2 bytes
+ *           K block: [P] rows of D/2 bytes; dword h * D/32 + t (h = 0..3) holds
+ *             channels 32t + 8h .. 32t + 8h + 7, the lowest in the low bits;
+ *           V block: [P/4][16][D/64][4] 16-bit pieces; piece (a, n, u, i) holds
+ *             channels 64u + n, + 16, + 32, + 48 of token 4a + i, lowest first
+ *   params  [n_pages][2][H][D/G][P] pairs of fp16 (s, lo)
+ * so that a wave's matrix operands are whole 8- or 16-byte loads and no two
+ * tokens share a byte.  A slot is page * P + (token within the page).
+ */
+typedef struct kvc_kv4_desc {
+    int32_t n_kv_heads;  /* H, 1..1024 */
+    int32_t head_dim;    /* D: 64, 128 or 256 */
+    int32_t group;       /* G: 32, 64 or 128, at most D */
+    int32_t page_tokens; /* P: 16, 32, 64, 128 or 256 */
+    int64_t n_pages;     /* 1..2^31 - 1 */
+} kvc_kv4_desc;
+
+/* Bytes of the two buffers; negative kvc_status if the descriptor is invalid. */
+int64_t kvc_kv4_codes_bytes(const kvc_kv4_desc *desc);
+int64_t kvc_kv4_params_bytes(const kvc_kv4_desc *desc);
+
+/*
+ * Write n_tokens tokens' K and V into their slots.
+ *   k, v    [n_tokens][H][D] of dtype (KVC_F16, KVC_F32 or KVC_BF16; device, read), the
+ *           channels of a row contiguous, tokens and heads at the strides given (in
+ *           elements, any sign); 16-byte aligned rows are loaded in wide pieces
+ *   slots   int64 [n_tokens] (device, read); a negative slot skips its token (padding of a
+ *           captured batch); a slot past the pool skips it and sets KVC_DEV_BAD_INDEX
+ * Two tokens of one call with the same slot leave an unspecified mix of both.
+ */
+int kvc_kv4_append(const kvc_kv4_desc *desc, const void *k, const void *v, int64_t n_tokens,
+                   int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                   int64_t v_head_stride, int32_t dtype, const int64_t *slots, uint8_t *codes,
+                   uint16_t *params, int32_t *dev_status, void *stream);
+
+/*
+ * Read slots back as values: fp32(lo + code * s), rounded to out_dtype (for
+ * KVC_F16 clamped to +-65504 first: a value can pass its group's largest by
+ * the rounding of s).
+ *   k, v    [n_tokens][H][D] of out_dtype (KVC_F16, KVC_F32 or KVC_BF16; device, written),
+ *           strides as kvc_kv4_append; either may be NULL
+ *   slots   as kvc_kv4_append; the rows of a negative or bad slot are written as zeros
+ */
+int kvc_kv4_read(const kvc_kv4_desc *desc, const uint8_t *codes, const uint16_t *params,
+                 const int64_t *slots, int64_t n_tokens, void *k, void *v, int64_t k_token_stride,
+                 int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                 int32_t out_dtype, int32_t *dev_status, void *stream);
+
+/*
+ * Attention of new tokens over the cached ones (their own among them, written
+ * before).  Query i of sequence b, one of nq_b = cu_q[b+1] - cu_q[b], stands at
+ * position pos = kv_len[b] - nq_b + i and sees the keys j < kv_len[b] with, if
+ * causal, j <= pos and, if window > 0, j > pos - window.  Its heads, R = n_q_heads / H for each kv
+ * head, compute over those keys, from the values the codes stand for,
+ *   x_j = scale * q.k_j  (softcap > 0: softcap * tanh(x_j / softcap)),
+ *   out = sum_j softmax(x)_j v_j,  lse = ln sum_j exp(x_j).
+ * A row without a key gives out = 0, lse = -inf.  Logits, maxima, sums and
+ * accumulators are fp32; out is rounded once.
+ */
+typedef struct kvc_kv4_attn {
+    const void *q;             /* [n_q][n_q_heads][D] of dtype (KVC_F16 or KVC_BF16), channels contiguous */
+    void *out;                 /* as q (written); must not overlap q */
+    float *lse;                /* NULL, or [n_q][n_q_heads] (written) */
+    int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride; /* elements */
+    const int32_t *page_table; /* [n_seqs][max_pages], rows table_stride entries apart: the page of
+                                  each P tokens of a sequence; entries past its length are not read */
+    int64_t table_stride;
+    const int32_t *kv_len;     /* [n_seqs]; below 0 is taken as 0 */
+    const int32_t *cu_q;       /* [n_seqs + 1] rising from 0 to n_q, or NULL: max_q queries each */
+    int64_t n_q;               /* query tokens in all */
+    int32_t n_seqs, n_q_heads, max_pages;
+    int32_t max_q;             /* the most queries of one sequence */
+    int32_t dtype, causal, window; /* window > 0 needs causal */
+    float softcap, scale;
+    void *work;                /* work_bytes >= kvc_kv4_work_bytes, 16-byte aligned (NULL if that is 0) */
+    int64_t work_bytes;
+} kvc_kv4_attn;
+
+/* Workspace of a call with these sizes (0 when no row's keys are split). */
+int64_t kvc_kv4_work_bytes(const kvc_kv4_desc *desc, int64_t n_q, int32_t n_seqs, int32_t n_q_heads,
+                           int32_t max_pages, int32_t max_q);
+
+/* A page outside the pool, a length past the table or queries outside
+ * [0, n_q) set KVC_DEV_BAD_INDEX; the sequence's outputs are then unspecified
+ * (the kernels stay inside their buffers). */
+int kvc_kv4_attention(const kvc_kv4_desc *desc, const kvc_kv4_attn *args, const uint8_t *codes,
+                      const uint16_t *params, int32_t *dev_status, void *stream);
 
 #ifdef __cplusplus
 }
