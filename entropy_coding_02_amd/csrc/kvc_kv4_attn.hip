@@ -40,22 +40,30 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c)
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// Nibble I of both halves of w as a pair of 1 + n/16.
-template <bool BF, int I>
-__device__ __forceinline__ uint32_t unit_pair(uint32_t w)
-{
-    constexpr int at = BF ? 3 : 6;  // the code's place below the exponent
-    constexpr uint32_t mask = 0x000F000Fu << at, one = BF ? 0x3F803F80u : 0x3C003C00u;
-    const uint32_t x = 4 * I <= at ? w << (at - 4 * I) : w >> (4 * I - at);
-    return (x & mask) | one;
-}
-
-// A K dword (8 channels of a key) as 8 operands in the order 0,4,1,5,2,6,3,7.
+// The mask and the constant exponent that make pairs of 1 + n/16, held in
+// registers: as literals they cost a second instruction at every use.
 template <bool BF>
-__device__ __forceinline__ u32x4 k_operand(uint32_t w)
-{
-    return u32x4{unit_pair<BF, 0>(w), unit_pair<BF, 1>(w), unit_pair<BF, 2>(w), unit_pair<BF, 3>(w)};
-}
+struct Unit {
+    static constexpr int at = BF ? 3 : 6;  // the code's place below the exponent
+    uint32_t mask, one;
+    static __device__ __forceinline__ Unit make()
+    {
+        uint32_t mask = 0x000F000Fu << at, one = BF ? 0x3F803F80u : 0x3C003C00u;
+        __asm__("" : "+s"(mask), "+v"(one));
+        return Unit{mask, one};
+    }
+    // nibble i of both halves of w
+    __device__ __forceinline__ uint32_t pair(uint32_t w, int i) const
+    {
+        const uint32_t x = 4 * i <= at ? w << (at - 4 * i) : w >> (4 * i - at);
+        return (x & mask) | one;
+    }
+    // a K dword (8 channels of a key) as 8 operands in the order 0,4,1,5,2,6,3,7
+    __device__ __forceinline__ u32x4 octet(uint32_t w) const
+    {
+        return u32x4{pair(w, 0), pair(w, 1), pair(w, 2), pair(w, 3)};
+    }
+};
 
 __device__ __forceinline__ float s_of(uint32_t w) { return kvc_h2f(w & 0xFFFF); }
 __device__ __forceinline__ float lo_of(uint32_t w) { return kvc_h2f(w >> 16); }
@@ -68,11 +76,17 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b)
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Over the four lanes (16 apart) of a query row.
+// Over the four lanes (16 apart) of a query row: swapping rows of 16, then
+// halves, of a value with itself leaves both operands of the reduction.
 __device__ __forceinline__ float row_max(float v)
 {
-    v = fmaxf(v, __shfl_xor(v, 16, 64));
-    return fmaxf(v, __shfl_xor(v, 32, 64));
+    uint32_t b = __builtin_bit_cast(uint32_t, v);
+    const auto x = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    const uint32_t x0 = x[0], x1 = x[1];
+    b = __builtin_bit_cast(uint32_t, fmaxf(__builtin_bit_cast(float, x0), __builtin_bit_cast(float, x1)));
+    const auto y = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    const uint32_t y0 = y[0], y1 = y[1];
+    return fmaxf(__builtin_bit_cast(float, y0), __builtin_bit_cast(float, y1));
 }
 __device__ __forceinline__ float row_sum(float v)
 {
@@ -87,12 +101,15 @@ __device__ __forceinline__ float lse_of(float M, float L)
     return L == 0.0f ? -__builtin_inff() : (M + __builtin_amdgcn_logf(L)) * kLn2;
 }
 
-// What a wave loads for 32 keys: two tiles of 16.
+// What a wave loads for 32 keys: two tiles of 16.  A lane holds the codes it
+// multiplies, but of the parameters only its share (a dword for each 64 of
+// them): it works with those of four keys that 15 other lanes want too, so
+// they pass through LDS rather than lie in 16 lanes' registers.
 template <int D, int G>
 struct Stage {
-    static constexpr int NW = D / 32, NG = D / G;
+    static constexpr int NW = D / 32, NG = D / G, NP = (NG + 3) / 4;
     uint32_t k[2][NW], v[2][NW];
-    u32x4 kp[2][NG], vp[2][NG];
+    uint32_t kp[2][NP], vp[2][NP];
 };
 
 template <int D, int G>
@@ -103,8 +120,10 @@ __device__ __forceinline__ void load_words(uint32_t *dst, const uint8_t *src)
         const u32x2 w = *(const u32x2 *)src;
         dst[0] = w[0], dst[1] = w[1];
     } else {
+#pragma unroll
         for (int i = 0; i < NW / 4; ++i) {
             const u32x4 w = *(const u32x4 *)(src + 16 * i);
+#pragma unroll
             for (int j = 0; j < 4; ++j) dst[4 * i + j] = w[j];
         }
     }
@@ -127,8 +146,9 @@ __device__ __forceinline__ bool make_job(const Kv4Attn &a, Job &j)
     j.b = id % a.B;
     j.tile = id / a.B;
     bool bad = false;
-    int64_t c0 = a.cu_q ? a.cu_q[j.b] : (int64_t)j.b * a.max_q;
-    int64_t c1 = a.cu_q ? a.cu_q[j.b + 1] : c0 + a.max_q;
+    // the same for the whole block, which the compiler cannot see of a load
+    int64_t c0 = a.cu_q ? __builtin_amdgcn_readfirstlane(a.cu_q[j.b]) : (int64_t)j.b * a.max_q;
+    int64_t c1 = a.cu_q ? __builtin_amdgcn_readfirstlane(a.cu_q[j.b + 1]) : c0 + a.max_q;
     if (c0 < 0 || c0 > a.n_q) bad = true, c0 = c0 < 0 ? 0 : a.n_q;
     if (c1 < c0 || c1 > a.n_q || c1 - c0 > a.max_q) {
         bad = true;
@@ -139,7 +159,7 @@ __device__ __forceinline__ bool make_job(const Kv4Attn &a, Job &j)
     j.q0 = (int)c0;
     j.nq = (int)(c1 - c0);
     const int cap = a.max_pages << a.pool.pshift;
-    j.len = a.kv_len[j.b];
+    j.len = __builtin_amdgcn_readfirstlane(a.kv_len[j.b]);
     if (j.len > cap) bad = true, j.len = cap;
     if (j.len < 0) j.len = 0;
     if (bad && j.tile == 0 && threadIdx.x == 0) kvc_flag(a.pool.status, KVC_DEV_BAD_INDEX);
@@ -161,37 +181,205 @@ __device__ __forceinline__ bool make_job(const Kv4Attn &a, Job &j)
     return true;
 }
 
+// Where a lane reads within a tile's blocks (bytes); the tiles' own places are
+// the same for the whole wave.
 template <int D, int G>
-__device__ __forceinline__ void load_stage(const Kv4Attn &a, const Job &j, int blk, int lane, Stage<D, G> &st)
+struct LaneAt {
+    static constexpr int NG = D / G, NP = (NG + 3) / 4;
+    uint32_t k, v, p[NP];
+    __device__ __forceinline__ LaneAt(int lane, int pshift)
+    {
+        const int r = lane & 15, h = lane >> 4;
+        k = r * (D / 2) + h * (D / 8);
+        v = h * (2 * D) + r * (D / 8);
+        // group h (+ 4), key r; with fewer than four groups lanes repeat one
+#pragma unroll
+        for (int i = 0; i < NP; ++i) p[i] = (((uint32_t)((h + 4 * i) % NG) << pshift) + r) * 4;
+    }
+};
+
+// The table entries of a block's two tiles (a tile that no row sees is read
+// from one that some row does).
+__device__ __forceinline__ void load_pages(const Kv4Attn &a, const Job &j, int blk, int32_t *page)
 {
-    constexpr int NG = D / G;
-    const int r = lane & 15, h = lane >> 4;
-    const int P = 1 << a.pool.pshift;
     const int t_lo = j.kbeg >> 4, t_hi = (j.kend - 1) >> 4;
+#pragma unroll
     for (int t = 0; t < 2; ++t) {
-        // a tile that no row sees is read from one that some row does
         const int kt = min(max(blk * 2 + t, t_lo), t_hi);
-        int64_t page = a.table[j.b * a.table_stride + (kt >> (a.pool.pshift - 4))];
-        if (page < 0 || page >= a.pool.n_pages) {
-            if (lane == 0) kvc_flag(a.pool.status, KVC_DEV_BAD_INDEX);
-            page = 0;
-        }
-        const int off = (kt << 4) & (P - 1);
-        const int64_t kb = kv4_block(a.pool, page, 0, j.h), vb = kb + a.pool.H;
-        load_words<D, G>(st.k[t], a.pool.codes + kb * (P * (D / 2)) + (off + r) * (D / 2) + h * (D / 8));
-        load_words<D, G>(st.v[t], a.pool.codes + vb * (P * (D / 2)) + (off / 4 + h) * (2 * D) + r * (D / 8));
-        for (int g = 0; g < NG; ++g) {
-            st.kp[t][g] = *(const u32x4 *)(a.pool.params + (kb * NG + g) * P + off + 4 * h);
-            st.vp[t][g] = *(const u32x4 *)(a.pool.params + (vb * NG + g) * P + off + 4 * h);
-        }
+        page[t] = a.table[j.b * a.table_stride + (kt >> (a.pool.pshift - 4))];
     }
 }
 
+template <int D, int G>
+__device__ __forceinline__ void load_stage(const Kv4Attn &a, const Job &j, int blk, const int32_t *pages,
+                                           const LaneAt<D, G> &at, Stage<D, G> &st)
+{
+    constexpr int NG = D / G;
+    const int P = 1 << a.pool.pshift;
+    const int t_lo = j.kbeg >> 4, t_hi = (j.kend - 1) >> 4;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int kt = min(max(blk * 2 + t, t_lo), t_hi);
+        const int32_t entry = __builtin_amdgcn_readfirstlane(pages[t]);
+        const bool bad = (uint32_t)entry >= (uint32_t)a.pool.n_pages;
+        const int32_t page = __builtin_amdgcn_readfirstlane(bad ? 0 : entry);
+        if (bad && (threadIdx.x & 63) == 0) kvc_flag(a.pool.status, KVC_DEV_BAD_INDEX);
+        const int off = (kt << 4) & (P - 1);
+        const int64_t kb = kv4_block(a.pool, page, 0, j.h), vb = kb + a.pool.H;
+        const uint8_t *kc = a.pool.codes + (kb * P + off) * (D / 2), *vc = a.pool.codes + (vb * P + off) * (D / 2);
+        const uint8_t *kp = (const uint8_t *)(a.pool.params + kb * NG * P + off);
+        const uint8_t *vp = (const uint8_t *)(a.pool.params + vb * NG * P + off);
+        load_words<D, G>(st.k[t], kc + at.k);
+#pragma unroll
+        for (int i = 0; i < at.NP; ++i) st.kp[t][i] = *(const uint32_t *)(kp + at.p[i]);
+        load_words<D, G>(st.v[t], vc + at.v);
+#pragma unroll
+        for (int i = 0; i < at.NP; ++i) st.vp[t][i] = *(const uint32_t *)(vp + at.p[i]);
+    }
+}
+
+// One wave's running state over 16 query rows, and what of the rows the steps
+// need: a lane stands for row `lane & 15` and for four keys of each tile.
 template <int D, int G, bool BF>
-__global__ __launch_bounds__(64 * kWaves) void k_kv4_attn(Kv4Attn a)
+struct Rows16 {
+    static constexpr int NW = D / 32, NG = D / G, NT = D / 16;
+    Unit<BF> uk;
+    Unit<true> uv;
+    u32x4 q[NW];
+    f32x4 neg_qs[NG], o[NT], ps[NG];  // ps: sum of the p s that went into o
+    float qs16[NG], z[NG], m, l;
+    int h, k_lo, k_hi, all_lo, all_hi;
+    float c2, cap;
+
+    // lds: this wave's [K|V][tile][group][16 keys] parameters
+    __device__ __forceinline__ void step(const Stage<D, G> &st, int key0, uint32_t *lds, int lane)
+    {
+        constexpr int NP = Stage<D, G>::NP, TILE = 64 * NP;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                lds[t * TILE + 64 * i + lane] = st.kp[t][i];
+                lds[(2 + t) * TILE + 64 * i + lane] = st.vp[t][i];
+            }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        float x[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            f32x4 s4 = {0, 0, 0, 0};
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                f32x4 c = neg_qs[g];
+#pragma unroll
+                for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) c = mfma<BF>(uk.octet(st.k[t][s]), q[s], c);
+                const u32x4 kp = *(const u32x4 *)&lds[t * TILE + 16 * g + 4 * h];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s4[i] = __builtin_fmaf(lo_of(kp[i]), qs16[g], __builtin_fmaf(s_of(kp[i]), c[i], s4[i]));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[t][i] = s4[i];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        float mul = c2;
+        if (cap > 0.0f) {
+            // or the compiler computes this for every call
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) __asm__ volatile("" : "+v"(x[t][i]));
+            // c tanh(y / c) = c - 2c / (exp(2y / c) + 1), in powers of 2
+            const float in = c2 * 2.0f * kLog2e / cap, top = cap * kLog2e;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[t][i] = top - 2.0f * top * __builtin_amdgcn_rcpf(exp2_fast(x[t][i] * in) + 1.0f);
+            mul = 1.0f;
+        }
+        const bool partial = key0 + 32 > all_hi || key0 < all_lo;
+        if (partial)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = key0 + 16 * t + 4 * h + i;
+                    if (key < k_lo || key >= k_hi) x[t][i] = -__builtin_inff();
+                }
+        float mx = x[0][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[i / 4][i % 4]);
+        mx = row_max(mx);
+        mx = mx == -__builtin_inff() ? mx : mx * mul;
+        if (__any(mx > m)) {
+            const float mn = fmaxf(m, mx);
+            const float f = mn == -__builtin_inff() ? 1.0f : exp2_fast(m - mn);
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) z[g] *= f, ps[g] *= f;
+#pragma unroll
+            for (int c = 0; c < NT; ++c) o[c] *= f;
+        }
+        const float mu = m == -__builtin_inff() ? 0.0f : m;
+        float p[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                p[t][i] = exp2_fast(__builtin_fmaf(x[t][i], mul, -mu));
+                l += p[t][i];
+            }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            u32x4 hi, lo;
+            u32x4 vp[2] = {*(const u32x4 *)&lds[2 * TILE + 16 * g + 4 * h], *(const u32x4 *)&lds[3 * TILE + 16 * g + 4 * h]};
+            if (partial) {
+                __asm__ volatile("");
+                // what lies at a key that the row does not see may be anything, NaN too
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (x[t][i] == -__builtin_inff()) vp[t][i] = 0;
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    const uint32_t w0 = vp[t][i], w1 = vp[t][i + 1];
+                    const float a0 = p[t][i] * s_of(w0), a1 = p[t][i + 1] * s_of(w1);
+                    z[g] = __builtin_fmaf(p[t][i], lo_of(w0), z[g]);
+                    z[g] = __builtin_fmaf(p[t][i + 1], lo_of(w1), z[g]);
+                    const uint32_t hp = bf16_pair(a0, a1);
+                    hi[2 * t + i / 2] = hp;
+                    lo[2 * t + i / 2] = bf16_pair(a0 - __builtin_bit_cast(float, hp << 16),
+                                                  a1 - __builtin_bit_cast(float, hp & 0xFFFF0000u));
+                }
+            const u32x4 ones = {uv.one, uv.one, uv.one, uv.one};
+            ps[g] = mfma<true>(ones, hi, ps[g]);
+            ps[g] = mfma<true>(ones, lo, ps[g]);
+#pragma unroll
+            for (int c = g * (G / 16); c < (g + 1) * (G / 16); ++c) {
+                if (c % 4 == 0) __builtin_amdgcn_sched_barrier(0);
+                const int w = 2 * (c / 4);
+                const u32x4 va = {uv.pair(st.v[0][w], c & 3), uv.pair(st.v[0][w + 1], c & 3),
+                                  uv.pair(st.v[1][w], c & 3), uv.pair(st.v[1][w + 1], c & 3)};
+                o[c] = mfma<true>(va, hi, o[c]);
+                o[c] = mfma<true>(va, lo, o[c]);
+            }
+        }
+    }
+};
+
+template <int D, int G, bool BF>
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv4_attn(Kv4Attn a)
 {
     constexpr int NW = D / 32, NG = D / G, NT = D / 16;
-    __shared__ float lds_o[kWaves][16][D];
+    // the waves' parameters while they run, their results after
+    constexpr int kLdsP = 4 * 64 * Stage<D, G>::NP;
+    __shared__ __align__(16) uint32_t lds_p[kWaves][kLdsP];
+    __shared__ __align__(16) float lds_o[kWaves][16][D];
     __shared__ float lds_ml[kWaves][2][16];
     Job j;
     if (!make_job(a, j)) return;
@@ -200,134 +388,90 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv4_attn(Kv4Attn a)
     const int row = j.row0 + col, qi = row / a.R;
     const bool real = row < j.rows;
     const int pos = j.pos0 + qi;
-    const int k_hi = a.causal ? min(j.len, pos + 1) : j.len;      // keys k_lo <= key < k_hi
-    const int k_lo = a.window ? max(0, pos - a.window + 1) : 0;
+    Rows16<D, G, BF> r;
+    r.uk = Unit<BF>::make();
+    r.uv = Unit<true>::make();
+    r.h = h;
+    r.k_hi = a.causal ? min(j.len, pos + 1) : j.len;      // keys k_lo <= key < k_hi
+    r.k_lo = a.window ? max(0, pos - a.window + 1) : 0;
     // keys that every row of the tile sees
-    const int all_hi = a.causal ? min(j.len, j.pos0 + j.row0 / a.R + 1) : j.len;
-    const int all_lo = a.window ? j.pos0 + min(j.row0 + 15, j.rows - 1) / a.R - a.window + 1 : 0;
+    r.all_hi = a.causal ? min(j.len, j.pos0 + j.row0 / a.R + 1) : j.len;
+    r.all_lo = a.window ? j.pos0 + min(j.row0 + 15, j.rows - 1) / a.R - a.window + 1 : 0;
+    // a negative scale becomes a positive one of -q, so that the largest logit
+    // is found before scaling, and 0 one too small to tell (0 times the -inf of
+    // a masked key would be NaN)
+    r.c2 = 16.0f * fmaxf(__builtin_fabsf(a.scale), 1.0e-30f) * (a.softcap > 0.0f ? 1.0f : kLog2e);
+    r.cap = a.softcap;
+    r.m = -__builtin_inff();
+    r.l = 0.0f;
+
+    const LaneAt<D, G> at(lane, a.pool.pshift);
+    const int b_end = min(j.u1 * 4, (j.kend + 31) / 32);
+    Stage<D, G> cur, next;
+    int32_t pages[2] = {0, 0};
+    int blk = j.u0 * 4 + wave;
+    if (blk < b_end) {
+        load_pages(a, j, blk, pages);
+        load_stage<D, G>(a, j, blk, pages, at, cur);
+        load_pages(a, j, blk + kWaves, pages);  // clamped to the last tile
+    }
 
     // query operands in the codes' order, and the group sums of q as accumulators
-    u32x4 q[NW];
-    f32x4 neg_qs[NG];
-    float qs16[NG];
     {
         const uint16_t *src = a.q + (int64_t)(j.q0 + qi) * a.q_ts + (int64_t)(j.h * a.R + row % a.R) * a.q_hs + 8 * h;
+        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
         for (int s = 0; s < NW; ++s) {
             u32x4 w = {0, 0, 0, 0};
             if (real) {
                 if (a.q_vec)
                     w = *(const u32x4 *)(src + 32 * s);
                 else
+#pragma unroll
                     for (int i = 0; i < 4; ++i) w[i] = src[32 * s + 2 * i] | (uint32_t)src[32 * s + 2 * i + 1] << 16;
             }
-            q[s] = u32x4{(w[0] & 0xFFFF) | w[2] << 16, w[0] >> 16 | (w[2] & 0xFFFF0000u),
-                         (w[1] & 0xFFFF) | w[3] << 16, w[1] >> 16 | (w[3] & 0xFFFF0000u)};
+            r.q[s] = u32x4{(w[0] & 0xFFFF) | w[2] << 16, w[0] >> 16 | (w[2] & 0xFFFF0000u),
+                           (w[1] & 0xFFFF) | w[3] << 16, w[1] >> 16 | (w[3] & 0xFFFF0000u)} ^ flip;
         }
         constexpr uint32_t one = BF ? 0xBF80BF80u : 0xBC00BC00u;  // -1
         const u32x4 ones = {one, one, one, one};
+#pragma unroll
         for (int g = 0; g < NG; ++g) {
             f32x4 c = {0, 0, 0, 0};
-            for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) c = mfma<BF>(ones, q[s], c);
-            neg_qs[g] = c;
-            qs16[g] = -c[0] * (1.0f / 16.0f);
+#pragma unroll
+            for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) c = mfma<BF>(ones, r.q[s], c);
+            r.neg_qs[g] = c;
+            r.qs16[g] = -c[0] * (1.0f / 16.0f);
         }
     }
-    const float c2 = 16.0f * a.scale * (a.softcap > 0.0f ? 1.0f : kLog2e);
+#pragma unroll
+    for (int c = 0; c < NT; ++c) r.o[c] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int g = 0; g < NG; ++g) r.z[g] = 0.0f, r.ps[g] = f32x4{0, 0, 0, 0};
 
-    f32x4 o[NT];
-    float z[NG], m = -__builtin_inff(), l = 0.0f;
-    for (int c = 0; c < NT; ++c) o[c] = f32x4{0, 0, 0, 0};
-    for (int g = 0; g < NG; ++g) z[g] = 0.0f;
-
-    const int b_end = min(j.u1 * 4, (j.kend + 31) / 32);
-    Stage<D, G> cur, nxt;
-    int blk = j.u0 * 4 + wave;
-    if (blk < b_end) load_stage<D, G>(a, j, blk, lane, cur);
+    // A block's codes are on their way while the one before is worked on, and
+    // its pages one block earlier still.
     for (; blk < b_end; blk += kWaves) {
-        if (blk + kWaves < b_end) load_stage<D, G>(a, j, blk + kWaves, lane, nxt);
-        const int key0 = blk * 32;
-        float x[2][4];
-        for (int t = 0; t < 2; ++t) {
-            f32x4 s4 = {0, 0, 0, 0};
-            for (int g = 0; g < NG; ++g) {
-                f32x4 c = neg_qs[g];
-                for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) c = mfma<BF>(k_operand<BF>(cur.k[t][s]), q[s], c);
-                for (int i = 0; i < 4; ++i)
-                    s4[i] = __builtin_fmaf(lo_of(cur.kp[t][g][i]), qs16[g], __builtin_fmaf(s_of(cur.kp[t][g][i]), c[i], s4[i]));
-            }
-            for (int i = 0; i < 4; ++i) x[t][i] = s4[i] * c2;
+        if (blk + kWaves < b_end) {
+            load_stage<D, G>(a, j, blk + kWaves, pages, at, next);
+            load_pages(a, j, blk + 2 * kWaves, pages);
         }
-        if (a.softcap > 0.0f) {
-            // tanh(y) = 1 - 2 / (exp(2y) + 1)
-            const float c = 2.0f * kLog2e / a.softcap, top = a.softcap * kLog2e;
-            for (int t = 0; t < 2; ++t)
-                for (int i = 0; i < 4; ++i) x[t][i] = top - 2.0f * top * __builtin_amdgcn_rcpf(exp2_fast(x[t][i] * c) + 1.0f);
-        }
-        if (key0 + 32 > all_hi || key0 < all_lo) {
-            for (int t = 0; t < 2; ++t)
-                for (int i = 0; i < 4; ++i) {
-                    const int key = key0 + 16 * t + 4 * h + i;
-                    if (key < k_lo || key >= k_hi) {
-                        x[t][i] = -__builtin_inff();
-                        // what lies there may be anything, NaN too
-                        for (int g = 0; g < NG; ++g) cur.vp[t][g][i] = 0;
-                    }
-                }
-        }
-        float mx = x[0][0];
-        for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[i / 4][i % 4]);
-        mx = row_max(mx);
-        if (__any(mx > m)) {
-            const float mn = fmaxf(m, mx);
-            const float f = mn == -__builtin_inff() ? 1.0f : exp2_fast(m - mn);
-            m = mn;
-            l *= f;
-            for (int g = 0; g < NG; ++g) z[g] *= f;
-            for (int c = 0; c < NT; ++c) o[c] *= f;
-        }
-        const float mu = m == -__builtin_inff() ? 0.0f : m;
-        float p[2][4];
-        for (int t = 0; t < 2; ++t)
-            for (int i = 0; i < 4; ++i) {
-                p[t][i] = exp2_fast(x[t][i] - mu);
-                l += p[t][i];
-            }
-        for (int g = 0; g < NG; ++g) {
-            u32x4 hi, lo;
-            for (int t = 0; t < 2; ++t)
-                for (int i = 0; i < 4; i += 2) {
-                    const uint32_t w0 = cur.vp[t][g][i], w1 = cur.vp[t][g][i + 1];
-                    const float a0 = p[t][i] * s_of(w0), a1 = p[t][i + 1] * s_of(w1);
-                    z[g] = __builtin_fmaf(p[t][i], lo_of(w0), z[g]);
-                    z[g] = __builtin_fmaf(p[t][i + 1], lo_of(w1), z[g]);
-                    z[g] = __builtin_fmaf(-16.0f, a0, z[g]);
-                    z[g] = __builtin_fmaf(-16.0f, a1, z[g]);
-                    const uint32_t hp = bf16_pair(a0, a1);
-                    hi[2 * t + i / 2] = hp;
-                    lo[2 * t + i / 2] = bf16_pair(a0 - __builtin_bit_cast(float, hp << 16),
-                                                  a1 - __builtin_bit_cast(float, hp & 0xFFFF0000u));
-                }
-            for (int c = g * (G / 16); c < (g + 1) * (G / 16); ++c) {
-                const int w = 2 * (c / 4);
-                u32x4 va;
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t d = cur.v[i / 2][w + (i & 1)];
-                    va[i] = (c & 3) == 0 ? unit_pair<true, 0>(d) : (c & 3) == 1 ? unit_pair<true, 1>(d)
-                          : (c & 3) == 2 ? unit_pair<true, 2>(d) : unit_pair<true, 3>(d);
-                }
-                o[c] = mfma<true>(va, hi, o[c]);
-                o[c] = mfma<true>(va, lo, o[c]);
-            }
-        }
-        cur = nxt;
+        r.step(cur, blk * 32, lds_p[wave], lane);
+        cur = next;
     }
+    float m = r.m, l = r.l, z[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) z[g] = __builtin_fmaf(-4.0f, r.ps[g][0], r.z[g]);  // a quarter in each of the row's lanes
 
     // the four waves' parts: out = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w
     l = row_sum(l);
+#pragma unroll
     for (int g = 0; g < NG; ++g) z[g] = row_sum(z[g]);
+#pragma unroll
     for (int c = 0; c < NT; ++c) {
         f32x4 y;
-        for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(16.0f, o[c][i], z[16 * c / G]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(16.0f, r.o[c][i], z[16 * c / G]);
         *(f32x4 *)&lds_o[wave][col][16 * c + 4 * h] = y;
     }
     if (h == 0) {
@@ -340,7 +484,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv4_attn(Kv4Attn a)
     const int orow = j.row0 + mr;
     if (orow >= j.rows) return;
     float M = -__builtin_inff(), L = 0.0f, wgt[kWaves];
+#pragma unroll
     for (int w = 0; w < kWaves; ++w) M = fmaxf(M, lds_ml[w][0][mr]);
+#pragma unroll
     for (int w = 0; w < kWaves; ++w) {
         wgt[w] = M == -__builtin_inff() ? 0.0f : exp2_fast(lds_ml[w][0][mr] - M);
         L += wgt[w] * lds_ml[w][1][mr];
@@ -351,6 +497,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv4_attn(Kv4Attn a)
     const float inv = a.ns > 1 ? 1.0f : (L == 0.0f ? 0.0f : 1.0f / L);
     for (int c = part * 4; c < D; c += 64) {
         f32x4 y = {0, 0, 0, 0};
+#pragma unroll
         for (int w = 0; w < kWaves; ++w) y += wgt[w] * *(const f32x4 *)&lds_o[w][mr][c];
         y *= inv;
         if (a.ns > 1) {
@@ -361,6 +508,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv4_attn(Kv4Attn a)
             if (a.o_vec) {
                 *(u32x2 *)dst = w;
             } else {
+#pragma unroll
                 for (int i = 0; i < 4; ++i) dst[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
             }
         }
@@ -375,33 +523,50 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv4_attn(Kv4Attn a)
     }
 }
 
-// Joins the splits of a row: one wave a row, D/64 channels a lane.
-template <int D, bool BF>
-__global__ __launch_bounds__(256) void k_kv4_join(Kv4Attn a)
+// Joins the splits of a row: D/4 lanes a split, as many splits at a time as
+// fill the block, then their sums through LDS.
+template <int D, bool BF, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_kv4_join(Kv4Attn a)
 {
-    const int64_t rows = a.n_q * a.Hq, row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63;
-    if (row >= rows) return;
+    constexpr int LANES = D / 4, AT_ONCE = THREADS / LANES;
+    __shared__ f32x4 lds_y[AT_ONCE][LANES];
+    __shared__ float lds_l[AT_ONCE];
+    const int64_t rows = a.n_q * a.Hq, row = blockIdx.x;
+    const int part = threadIdx.x % LANES, first = threadIdx.x / LANES;
     float M = -__builtin_inff();
-    for (int s = lane; s < a.ns; s += 64) M = fmaxf(M, a.part_ml[(s * rows + row) * 2]);
+    for (int s = threadIdx.x & 63; s < a.ns; s += 64) M = fmaxf(M, a.part_ml[(s * rows + row) * 2]);
     for (int off = 32; off; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, 64));
-    float y[D / 64] = {}, L = 0.0f;
-    for (int s = 0; s < a.ns; ++s) {
+    f32x4 y = {0, 0, 0, 0};
+    float L = 0.0f;
+#pragma unroll 4
+    for (int s = first; s < a.ns; s += AT_ONCE) {
         const float ms = a.part_ml[(s * rows + row) * 2], ls = a.part_ml[(s * rows + row) * 2 + 1];
-        if (ls == 0.0f) continue;  // no keys
-        const float w = exp2_fast(ms - M);
+        const f32x4 ys = *(const f32x4 *)(a.part_o + (s * rows + row) * D + 4 * part);
+        const float w = ls == 0.0f ? 0.0f : exp2_fast(ms - M);  // 0: no keys
         L += w * ls;
-        for (int i = 0; i < D / 64; ++i) y[i] += w * a.part_o[(s * rows + row) * D + lane + 64 * i];
+        y += w * ys;
+    }
+    lds_y[first][part] = y;
+    if (part == 0) lds_l[first] = L;
+    __syncthreads();
+    if (first) return;
+    L = lds_l[0];
+    for (int i = 1; i < AT_ONCE; ++i) {
+        y += lds_y[i][part];
+        L += lds_l[i];
     }
     const int64_t tok = row / a.Hq;
     const int head = (int)(row % a.Hq);
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    for (int i = 0; i < D / 64; ++i) {
-        const float v = y[i] * inv;
-        a.out[tok * a.o_ts + head * a.o_hs + lane + 64 * i] =
-            BF ? __builtin_bit_cast(uint16_t, (__bf16)v) : (uint16_t)kvc_f2h(v);
+    y *= L == 0.0f ? 0.0f : 1.0f / L;
+    uint16_t *dst = a.out + tok * a.o_ts + head * a.o_hs + 4 * part;
+    const u32x2 w = {BF ? bf16_pair(y[0], y[1]) : kvc_f2h2(y[0], y[1]), BF ? bf16_pair(y[2], y[3]) : kvc_f2h2(y[2], y[3])};
+    if (a.o_vec) {
+        *(u32x2 *)dst = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dst[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
     }
-    if (a.lse && lane == 0) a.lse[row] = lse_of(M, L);
+    if (a.lse && part == 0) a.lse[row] = lse_of(M, L);
 }
 
 template <int D, int G, bool BF>
@@ -411,7 +576,11 @@ hipError_t attend(const Kv4Attn &a, hipStream_t s)
     k_kv4_attn<D, G, BF><<<dim3((uint32_t)blocks), dim3(64 * kWaves), 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && a.ns > 1) {
-        k_kv4_join<D, BF><<<dim3((uint32_t)((a.n_q * a.Hq + 3) / 4)), dim3(256), 0, s>>>(a);
+        const dim3 rows((uint32_t)(a.n_q * a.Hq));
+        if (a.ns <= 8)
+            k_kv4_join<D, BF, 64><<<rows, dim3(64), 0, s>>>(a);
+        else
+            k_kv4_join<D, BF, 256><<<rows, dim3(256), 0, s>>>(a);
         e = hipGetLastError();
     }
     return e;
