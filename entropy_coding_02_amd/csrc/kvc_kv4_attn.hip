@@ -29,6 +29,11 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
+// Arrays that no kernel here writes, read through the scalar cache: they
+// neither occupy vector registers nor wait in line behind the codes.
+typedef const int32_t __attribute__((address_space(4))) const_i32;
+__device__ __forceinline__ int32_t scalar_load(const int32_t *p, int64_t i) { return ((const_i32 *)(uintptr_t)p)[i]; }
+
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kWaves = 4;
 
@@ -94,6 +99,10 @@ __device__ __forceinline__ float row_sum(float v)
     return v + __shfl_xor(v, 32, 64);
 }
 
+// A barrier for LDS alone: __syncthreads also waits for every load on its way
+// from memory, which here are the first codes.
+__device__ __forceinline__ void lds_barrier() { __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // From a row's maximum and sum in powers of 2; a row without keys has L = 0, a
 // row that met a NaN has L = NaN (its maximum may be -inf).
 __device__ __forceinline__ float lse_of(float M, float L)
@@ -146,9 +155,8 @@ __device__ __forceinline__ bool make_job(const Kv4Attn &a, Job &j)
     j.b = id % a.B;
     j.tile = id / a.B;
     bool bad = false;
-    // the same for the whole block, which the compiler cannot see of a load
-    int64_t c0 = a.cu_q ? __builtin_amdgcn_readfirstlane(a.cu_q[j.b]) : (int64_t)j.b * a.max_q;
-    int64_t c1 = a.cu_q ? __builtin_amdgcn_readfirstlane(a.cu_q[j.b + 1]) : c0 + a.max_q;
+    int64_t c0 = a.cu_q ? scalar_load(a.cu_q, j.b) : (int64_t)j.b * a.max_q;
+    int64_t c1 = a.cu_q ? scalar_load(a.cu_q, j.b + 1) : c0 + a.max_q;
     if (c0 < 0 || c0 > a.n_q) bad = true, c0 = c0 < 0 ? 0 : a.n_q;
     if (c1 < c0 || c1 > a.n_q || c1 - c0 > a.max_q) {
         bad = true;
@@ -159,7 +167,7 @@ __device__ __forceinline__ bool make_job(const Kv4Attn &a, Job &j)
     j.q0 = (int)c0;
     j.nq = (int)(c1 - c0);
     const int cap = a.max_pages << a.pool.pshift;
-    j.len = __builtin_amdgcn_readfirstlane(a.kv_len[j.b]);
+    j.len = scalar_load(a.kv_len, j.b);
     if (j.len > cap) bad = true, j.len = cap;
     if (j.len < 0) j.len = 0;
     if (bad && j.tile == 0 && threadIdx.x == 0) kvc_flag(a.pool.status, KVC_DEV_BAD_INDEX);
@@ -212,7 +220,7 @@ __device__ __forceinline__ void load_pages(const Kv4Attn &a, const Job &j, int b
 
 template <int D, int G>
 __device__ __forceinline__ void load_stage(const Kv4Attn &a, const Job &j, int blk, const int32_t *pages,
-                                           const LaneAt<D, G> &at, Stage<D, G> &st)
+                                           const LaneAt<D, G> &at, Stage<D, G> &st, bool &bad_page)
 {
     constexpr int NG = D / G;
     const int P = 1 << a.pool.pshift;
@@ -222,8 +230,8 @@ __device__ __forceinline__ void load_stage(const Kv4Attn &a, const Job &j, int b
         const int kt = min(max(blk * 2 + t, t_lo), t_hi);
         const int32_t entry = __builtin_amdgcn_readfirstlane(pages[t]);
         const bool bad = (uint32_t)entry >= (uint32_t)a.pool.n_pages;
-        const int32_t page = __builtin_amdgcn_readfirstlane(bad ? 0 : entry);
-        if (bad && (threadIdx.x & 63) == 0) kvc_flag(a.pool.status, KVC_DEV_BAD_INDEX);
+        const int32_t page = bad ? 0 : entry;
+        bad_page |= bad;
         const int off = (kt << 4) & (P - 1);
         const int64_t kb = kv4_block(a.pool, page, 0, j.h), vb = kb + a.pool.H;
         const uint8_t *kc = a.pool.codes + (kb * P + off) * (D / 2), *vc = a.pool.codes + (vb * P + off) * (D / 2);
@@ -238,240 +246,228 @@ __device__ __forceinline__ void load_stage(const Kv4Attn &a, const Job &j, int b
     }
 }
 
-// One wave's running state over 16 query rows, and what of the rows the steps
-// need: a lane stands for row `lane & 15` and for four keys of each tile.
 template <int D, int G, bool BF>
-struct Rows16 {
-    static constexpr int NW = D / 32, NG = D / G, NT = D / 16;
-    Unit<BF> uk;
-    Unit<true> uv;
-    u32x4 q[NW];
-    f32x4 neg_qs[NG], o[NT], ps[NG];  // ps: sum of the p s that went into o
-    float qs16[NG], z[NG], m, l;
-    int h, k_lo, k_hi, all_lo, all_hi;
-    float c2, cap;
-
-    // lds: this wave's [K|V][tile][group][16 keys] parameters
-    __device__ __forceinline__ void step(const Stage<D, G> &st, int key0, uint32_t *lds, int lane)
-    {
-        constexpr int NP = Stage<D, G>::NP, TILE = 64 * NP;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                lds[t * TILE + 64 * i + lane] = st.kp[t][i];
-                lds[(2 + t) * TILE + 64 * i + lane] = st.vp[t][i];
-            }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        float x[2][4];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            f32x4 s4 = {0, 0, 0, 0};
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                f32x4 c = neg_qs[g];
-#pragma unroll
-                for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) c = mfma<BF>(uk.octet(st.k[t][s]), q[s], c);
-                const u32x4 kp = *(const u32x4 *)&lds[t * TILE + 16 * g + 4 * h];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    s4[i] = __builtin_fmaf(lo_of(kp[i]), qs16[g], __builtin_fmaf(s_of(kp[i]), c[i], s4[i]));
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[t][i] = s4[i];
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        float mul = c2;
-        if (cap > 0.0f) {
-            // or the compiler computes this for every call
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) __asm__ volatile("" : "+v"(x[t][i]));
-            // c tanh(y / c) = c - 2c / (exp(2y / c) + 1), in powers of 2
-            const float in = c2 * 2.0f * kLog2e / cap, top = cap * kLog2e;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[t][i] = top - 2.0f * top * __builtin_amdgcn_rcpf(exp2_fast(x[t][i] * in) + 1.0f);
-            mul = 1.0f;
-        }
-        const bool partial = key0 + 32 > all_hi || key0 < all_lo;
-        if (partial)
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int key = key0 + 16 * t + 4 * h + i;
-                    if (key < k_lo || key >= k_hi) x[t][i] = -__builtin_inff();
-                }
-        float mx = x[0][0];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[i / 4][i % 4]);
-        mx = row_max(mx);
-        mx = mx == -__builtin_inff() ? mx : mx * mul;
-        if (__any(mx > m)) {
-            const float mn = fmaxf(m, mx);
-            const float f = mn == -__builtin_inff() ? 1.0f : exp2_fast(m - mn);
-            m = mn;
-            l *= f;
-#pragma unroll
-            for (int g = 0; g < NG; ++g) z[g] *= f, ps[g] *= f;
-#pragma unroll
-            for (int c = 0; c < NT; ++c) o[c] *= f;
-        }
-        const float mu = m == -__builtin_inff() ? 0.0f : m;
-        float p[2][4];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                p[t][i] = exp2_fast(__builtin_fmaf(x[t][i], mul, -mu));
-                l += p[t][i];
-            }
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            u32x4 hi, lo;
-            u32x4 vp[2] = {*(const u32x4 *)&lds[2 * TILE + 16 * g + 4 * h], *(const u32x4 *)&lds[3 * TILE + 16 * g + 4 * h]};
-            if (partial) {
-                __asm__ volatile("");
-                // what lies at a key that the row does not see may be anything, NaN too
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (x[t][i] == -__builtin_inff()) vp[t][i] = 0;
-            }
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    const uint32_t w0 = vp[t][i], w1 = vp[t][i + 1];
-                    const float a0 = p[t][i] * s_of(w0), a1 = p[t][i + 1] * s_of(w1);
-                    z[g] = __builtin_fmaf(p[t][i], lo_of(w0), z[g]);
-                    z[g] = __builtin_fmaf(p[t][i + 1], lo_of(w1), z[g]);
-                    const uint32_t hp = bf16_pair(a0, a1);
-                    hi[2 * t + i / 2] = hp;
-                    lo[2 * t + i / 2] = bf16_pair(a0 - __builtin_bit_cast(float, hp << 16),
-                                                  a1 - __builtin_bit_cast(float, hp & 0xFFFF0000u));
-                }
-            const u32x4 ones = {uv.one, uv.one, uv.one, uv.one};
-            ps[g] = mfma<true>(ones, hi, ps[g]);
-            ps[g] = mfma<true>(ones, lo, ps[g]);
-#pragma unroll
-            for (int c = g * (G / 16); c < (g + 1) * (G / 16); ++c) {
-                if (c % 4 == 0) __builtin_amdgcn_sched_barrier(0);
-                const int w = 2 * (c / 4);
-                const u32x4 va = {uv.pair(st.v[0][w], c & 3), uv.pair(st.v[0][w + 1], c & 3),
-                                  uv.pair(st.v[1][w], c & 3), uv.pair(st.v[1][w + 1], c & 3)};
-                o[c] = mfma<true>(va, hi, o[c]);
-                o[c] = mfma<true>(va, lo, o[c]);
-            }
-        }
-    }
-};
-
-template <int D, int G, bool BF>
-__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv4_attn(Kv4Attn a)
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2 : 3) : 4) void k_kv4_attn(Kv4Attn a)
 {
-    constexpr int NW = D / 32, NG = D / G, NT = D / 16;
-    // the waves' parameters while they run, their results after
-    constexpr int kLdsP = 4 * 64 * Stage<D, G>::NP;
-    __shared__ __align__(16) uint32_t lds_p[kWaves][kLdsP];
+    constexpr int NW = D / 32, NG = D / G, NT = D / 16, NP = Stage<D, G>::NP, TILE = 64 * NP, NQ = (NW + kWaves - 1) / kWaves;
+    // Each wave's results; while it runs, its [K|V][tile][group][16 keys] parameters.
     __shared__ __align__(16) float lds_o[kWaves][16][D];
     __shared__ float lds_ml[kWaves][2][16];
+    // The query operands, which as registers would cost a wave a SIMD.
+    __shared__ u32x4 lds_q[NW][64];
     Job j;
     if (!make_job(a, j)) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int col = lane & 15, h = lane >> 4;
+    const int col = lane & 15, h = lane >> 4;  // this lane's query row, and its four keys of each tile
+    uint32_t *const prm = (uint32_t *)&lds_o[wave][0][0];
     const int row = j.row0 + col, qi = row / a.R;
-    const bool real = row < j.rows;
-    const int pos = j.pos0 + qi;
-    Rows16<D, G, BF> r;
-    r.uk = Unit<BF>::make();
-    r.uv = Unit<true>::make();
-    r.h = h;
-    r.k_hi = a.causal ? min(j.len, pos + 1) : j.len;      // keys k_lo <= key < k_hi
-    r.k_lo = a.window ? max(0, pos - a.window + 1) : 0;
-    // keys that every row of the tile sees
-    r.all_hi = a.causal ? min(j.len, j.pos0 + j.row0 / a.R + 1) : j.len;
-    r.all_lo = a.window ? j.pos0 + min(j.row0 + 15, j.rows - 1) / a.R - a.window + 1 : 0;
-    // a negative scale becomes a positive one of -q, so that the largest logit
-    // is found before scaling, and 0 one too small to tell (0 times the -inf of
-    // a masked key would be NaN)
-    r.c2 = 16.0f * fmaxf(__builtin_fabsf(a.scale), 1.0e-30f) * (a.softcap > 0.0f ? 1.0f : kLog2e);
-    r.cap = a.softcap;
-    r.m = -__builtin_inff();
-    r.l = 0.0f;
-
-    const LaneAt<D, G> at(lane, a.pool.pshift);
     const int b_end = min(j.u1 * 4, (j.kend + 31) / 32);
-    Stage<D, G> cur, next;
-    int32_t pages[2] = {0, 0};
     int blk = j.u0 * 4 + wave;
-    if (blk < b_end) {
-        load_pages(a, j, blk, pages);
-        load_stage<D, G>(a, j, blk, pages, at, cur);
-        load_pages(a, j, blk + kWaves, pages);  // clamped to the last tile
-    }
+    const bool work = blk < b_end;
 
-    // query operands in the codes' order, and the group sums of q as accumulators
+    // Query operands in the codes' order, each wave a part, and the pages of
+    // its first two blocks.
+    int32_t first[2] = {0, 0}, pages[2] = {0, 0};
+    u32x4 qw[NQ];
     {
+        const bool real = row < j.rows;
         const uint16_t *src = a.q + (int64_t)(j.q0 + qi) * a.q_ts + (int64_t)(j.h * a.R + row % a.R) * a.q_hs + 8 * h;
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            const int s = wave + i * kWaves;
+            qw[i] = u32x4{0, 0, 0, 0};
+            if (!real || s >= NW) continue;
+            if (a.q_vec)
+                qw[i] = *(const u32x4 *)(src + 32 * s);
+            else
+                for (int k = 0; k < 4; ++k) qw[i][k] = src[32 * s + 2 * k] | (uint32_t)src[32 * s + 2 * k + 1] << 16;
+        }
+        if (work) {
+            load_pages(a, j, blk, first);
+            load_pages(a, j, blk + kWaves, pages);
+        }
+        // a negative scale becomes a positive one of -q, so that the largest
+        // logit is found before scaling
         const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
-        for (int s = 0; s < NW; ++s) {
-            u32x4 w = {0, 0, 0, 0};
-            if (real) {
-                if (a.q_vec)
-                    w = *(const u32x4 *)(src + 32 * s);
-                else
+        for (int i = 0; i < NQ; ++i) {
+            const u32x4 w = qw[i];
+            if (wave + i * kWaves < NW)
+                lds_q[wave + i * kWaves][lane] = u32x4{(w[0] & 0xFFFF) | w[2] << 16, w[0] >> 16 | (w[2] & 0xFFFF0000u),
+                                                       (w[1] & 0xFFFF) | w[3] << 16, w[1] >> 16 | (w[3] & 0xFFFF0000u)} ^ flip;
+        }
+        lds_barrier();
+    }
+
+    const Unit<BF> uk = Unit<BF>::make();
+    const Unit<true> uv = Unit<true>::make();
+    f32x4 o[NT], ps[NG];  // ps: the sums of the p s that went into o
+    float z[NG], m = -__builtin_inff(), l = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = src[32 * s + 2 * i] | (uint32_t)src[32 * s + 2 * i + 1] << 16;
+    for (int c = 0; c < NT; ++c) o[c] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int g = 0; g < NG; ++g) z[g] = 0.0f, ps[g] = f32x4{0, 0, 0, 0};
+    if (work) {
+        const LaneAt<D, G> at(lane, a.pool.pshift);
+        Stage<D, G> cur, next;
+        bool bad_page = false;
+        load_stage<D, G>(a, j, blk, first, at, cur, bad_page);
+
+        // the group sums of q as accumulators
+        f32x4 neg_qs[NG];
+        float qs16[NG];
+        {
+            constexpr uint32_t one = BF ? 0xBF80BF80u : 0xBC00BC00u;  // -1
+            const u32x4 ones = {one, one, one, one};
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                f32x4 c = {0, 0, 0, 0};
+#pragma unroll
+                for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) c = mfma<BF>(ones, lds_q[s][lane], c);
+                neg_qs[g] = c;
+                qs16[g] = -c[0] * (1.0f / 16.0f);
             }
-            r.q[s] = u32x4{(w[0] & 0xFFFF) | w[2] << 16, w[0] >> 16 | (w[2] & 0xFFFF0000u),
-                           (w[1] & 0xFFFF) | w[3] << 16, w[1] >> 16 | (w[3] & 0xFFFF0000u)} ^ flip;
         }
-        constexpr uint32_t one = BF ? 0xBF80BF80u : 0xBC00BC00u;  // -1
-        const u32x4 ones = {one, one, one, one};
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            f32x4 c = {0, 0, 0, 0};
-#pragma unroll
-            for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) c = mfma<BF>(ones, r.q[s], c);
-            r.neg_qs[g] = c;
-            r.qs16[g] = -c[0] * (1.0f / 16.0f);
-        }
-    }
-#pragma unroll
-    for (int c = 0; c < NT; ++c) r.o[c] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int g = 0; g < NG; ++g) r.z[g] = 0.0f, r.ps[g] = f32x4{0, 0, 0, 0};
+        const int pos = j.pos0 + qi;
+        const int k_hi = a.causal ? min(j.len, pos + 1) : j.len;  // keys k_lo <= key < k_hi
+        const int k_lo = a.window ? max(0, pos - a.window + 1) : 0;
+        // keys that every row of the tile sees
+        const int all_hi = a.causal ? min(j.len, j.pos0 + j.row0 / a.R + 1) : j.len;
+        const int all_lo = a.window ? j.pos0 + min(j.row0 + 15, j.rows - 1) / a.R - a.window + 1 : 0;
+        // a scale of 0 becomes one too small to tell: 0 times the -inf of a
+        // masked key would be NaN
+        const float c2 = 16.0f * fmaxf(__builtin_fabsf(a.scale), 1.0e-30f) * (a.softcap > 0.0f ? 1.0f : kLog2e);
 
-    // A block's codes are on their way while the one before is worked on, and
-    // its pages one block earlier still.
-    for (; blk < b_end; blk += kWaves) {
-        if (blk + kWaves < b_end) {
-            load_stage<D, G>(a, j, blk + kWaves, pages, at, next);
-            load_pages(a, j, blk + 2 * kWaves, pages);
-        }
-        r.step(cur, blk * 32, lds_p[wave], lane);
-        cur = next;
-    }
-    float m = r.m, l = r.l, z[NG];
-#pragma unroll
-    for (int g = 0; g < NG; ++g) z[g] = __builtin_fmaf(-4.0f, r.ps[g][0], r.z[g]);  // a quarter in each of the row's lanes
+        // A block's codes are on their way while the one before is worked on,
+        // and its pages one block earlier still.  The last turns load the last
+        // tile again rather than branch: where a load may or may not have been
+        // issued, the wait for an older one is a wait for all.
+        for (; blk < b_end; blk += kWaves) {
+            int32_t after[2];  // loads return in order: before the codes, or they would wait for them
+            load_pages(a, j, blk + 2 * kWaves, after);
+            load_stage<D, G>(a, j, blk + kWaves, pages, at, next, bad_page);
+            pages[0] = after[0], pages[1] = after[1];
 
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    prm[t * TILE + 64 * i + lane] = cur.kp[t][i];
+                    prm[(2 + t) * TILE + 64 * i + lane] = cur.vp[t][i];
+                }
+            float x[2][4] = {};
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                f32x4 c[2] = {neg_qs[g], neg_qs[g]};
+#pragma unroll
+                for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) {
+                    const u32x4 q = lds_q[s][lane];
+                    c[0] = mfma<BF>(uk.octet(cur.k[0][s]), q, c[0]);
+                    c[1] = mfma<BF>(uk.octet(cur.k[1][s]), q, c[1]);
+                }
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const u32x4 kp = *(const u32x4 *)&prm[t * TILE + 16 * g + 4 * h];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[t][i] = __builtin_fmaf(lo_of(kp[i]), qs16[g], __builtin_fmaf(s_of(kp[i]), c[t][i], x[t][i]));
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            float mul = c2;
+            if (a.softcap > 0.0f) {
+                // or the compiler computes this for every call
+#pragma unroll
+                for (int i = 0; i < 8; ++i) __asm__ volatile("" : "+v"(x[i / 4][i % 4]));
+                // c tanh(y / c) = c - 2c / (exp(2y / c) + 1), in powers of 2
+                const float in = c2 * 2.0f * kLog2e / a.softcap, top = a.softcap * kLog2e;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float &y = x[i / 4][i % 4];
+                    y = top - 2.0f * top * __builtin_amdgcn_rcpf(exp2_fast(y * in) + 1.0f);
+                }
+                mul = 1.0f;
+            }
+            const int key0 = blk * 32;
+            const bool partial = key0 + 32 > all_hi || key0 < all_lo;
+            if (partial)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int key = key0 + 16 * (i / 4) + 4 * h + i % 4;
+                    if (key < k_lo || key >= k_hi) x[i / 4][i % 4] = -__builtin_inff();
+                }
+            float mx = x[0][0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[i / 4][i % 4]);
+            mx = row_max(mx);
+            mx = mx == -__builtin_inff() ? mx : mx * mul;
+            if (__any(mx > m)) {
+                const float mn = fmaxf(m, mx);
+                const float f = mn == -__builtin_inff() ? 1.0f : exp2_fast(m - mn);
+                m = mn;
+                l *= f;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) z[g] *= f, ps[g] *= f;
+#pragma unroll
+                for (int c = 0; c < NT; ++c) o[c] *= f;
+            }
+            const float mu = m == -__builtin_inff() ? 0.0f : m;
+            float p[2][4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                p[i / 4][i % 4] = exp2_fast(__builtin_fmaf(x[i / 4][i % 4], mul, -mu));
+                l += p[i / 4][i % 4];
+            }
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                u32x4 hi, lo;
+                u32x4 vp[2] = {*(const u32x4 *)&prm[2 * TILE + 16 * g + 4 * h], *(const u32x4 *)&prm[3 * TILE + 16 * g + 4 * h]};
+                if (partial) {
+                    // what lies at a key that the row does not see may be anything, NaN too
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (x[i / 4][i % 4] == -__builtin_inff()) vp[i / 4][i % 4] = 0;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const uint32_t w0 = vp[i / 4][i % 4], w1 = vp[i / 4][i % 4 + 1];
+                    const float p0 = p[i / 4][i % 4], p1 = p[i / 4][i % 4 + 1];
+                    const float a0 = p0 * s_of(w0), a1 = p1 * s_of(w1);
+                    z[g] = __builtin_fmaf(p0, lo_of(w0), z[g]);
+                    z[g] = __builtin_fmaf(p1, lo_of(w1), z[g]);
+                    const uint32_t hp = bf16_pair(a0, a1);
+                    hi[i / 2] = hp;
+                    lo[i / 2] = bf16_pair(a0 - __builtin_bit_cast(float, hp << 16),
+                                          a1 - __builtin_bit_cast(float, hp & 0xFFFF0000u));
+                }
+                const u32x4 ones = {uv.one, uv.one, uv.one, uv.one};
+                ps[g] = mfma<true>(ones, hi, ps[g]);
+                ps[g] = mfma<true>(ones, lo, ps[g]);
+#pragma unroll
+                for (int c = g * (G / 16); c < (g + 1) * (G / 16); ++c) {
+                    if (c % 4 == 0) __builtin_amdgcn_sched_barrier(0);
+                    const int w = 2 * (c / 4);
+                    const u32x4 va = {uv.pair(cur.v[0][w], c & 3), uv.pair(cur.v[0][w + 1], c & 3),
+                                      uv.pair(cur.v[1][w], c & 3), uv.pair(cur.v[1][w + 1], c & 3)};
+                    o[c] = mfma<true>(va, hi, o[c]);
+                    o[c] = mfma<true>(va, lo, o[c]);
+                }
+            }
+            cur = next;
+        }
+        if (bad_page && lane == 0) kvc_flag(a.pool.status, KVC_DEV_BAD_INDEX);
+    }
+
+    __asm__ volatile("" ::: "memory");  // parameters are read, results may take their place
     // the four waves' parts: out = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w
     l = row_sum(l);
 #pragma unroll
-    for (int g = 0; g < NG; ++g) z[g] = row_sum(z[g]);
+    for (int g = 0; g < NG; ++g) z[g] = row_sum(z[g]) - 16.0f * ps[g][0];
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
         f32x4 y;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(16.0f, r.o[c][i], z[16 * c / G]);
+        for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(16.0f, o[c][i], z[16 * c / G]);
         *(f32x4 *)&lds_o[wave][col][16 * c + 4 * h] = y;
     }
     if (h == 0) {
@@ -600,7 +596,7 @@ Kv4Plan kv4_plan(int64_t n_seqs, int H, int R, int64_t max_q, int64_t max_keys)
     p.tiles = (int32_t)((max_q * R + 15) / 16);
     const int64_t blocks = n_seqs * H * p.tiles;
     const int64_t units = (max_keys + 127) / 128;
-    int64_t ns = blocks ? 1024 / blocks : 1;
+    int64_t ns = blocks ? 2048 / blocks : 1;
     ns = ns < units ? ns : units;
     ns = ns < 128 ? ns : 128;
     p.ns = (int32_t)(ns < 1 ? 1 : ns);
