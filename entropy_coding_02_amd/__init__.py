@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -159,7 +160,7 @@ def _load():
         lib.kvc_kv4_work_bytes.restype = I64
         lib.kvc_kv4_work_bytes.argtypes = [K, I64, I32, I32, I32, I32]
         lib.kvc_kv4_attention.restype = ctypes.c_int
-        lib.kvc_kv4_attention.argtypes = [K, ctypes.POINTER(KvcKv4Attn), P, P, P, P]
+        lib.kvc_kv4_attention.argtypes = [K, P, P, P, P, P]  # the kvc_kv4_attn as bytes or a reference
         _lib = lib
     return _lib
 
@@ -481,29 +482,54 @@ class Kv4Cache:
         if dev_status is None:
             dev_status = torch.zeros(1, dtype=torch.int32, device=codes.device)
         self.codes, self.params, self.dev_status = codes, params, dev_status
+        # what every call needs of them
+        self.codes_ptr, self.params_ptr, self.status_ptr = codes.data_ptr(), params.data_ptr(), dev_status.data_ptr()
+        self.int32, self.int64, self.float32 = torch.int32, torch.int64, torch.float32
+
+
+_KV4_DTYPES = {}  # torch.dtype -> KVC_* (filled on first use: torch is imported late)
+_ATTN = struct.Struct("@PPPqqqqPqPPqiiiiiiiffPq")  # kvc_kv4_attn, field by field as KvcKv4Attn
+_RAW_STREAM = None
 
 
 def _kv4_dtype(dt):
-    import torch
-    try:
-        return {torch.float16: KVC_F16, torch.float32: KVC_F32, torch.bfloat16: KVC_BF16}[dt]
-    except KeyError:
-        raise ValueError(f"kvc: float16, bfloat16 or float32, not {dt}") from None
+    v = _KV4_DTYPES.get(dt)
+    if v is None:
+        import torch
+        _KV4_DTYPES.update({torch.float16: KVC_F16, torch.float32: KVC_F32, torch.bfloat16: KVC_BF16})
+        v = _KV4_DTYPES.get(dt)
+        if v is None:
+            raise ValueError(f"kvc: float16, bfloat16 or float32, not {dt}")
+    return v
 
 
-def _rows(cache: Kv4Cache, name: str, t, heads: int, n: int):
-    """Pointer and strides of a [n][heads][D] tensor whose channels are contiguous."""
+def _kv4_stream(stream, t):
+    """The caller's stream, or the current one of t's device (without building
+    a torch.cuda.Stream: these calls are a few microseconds long)."""
+    global _RAW_STREAM
+    if stream is not None:
+        return _stream(stream)
+    if _RAW_STREAM is None:
+        import torch
+        _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _RAW_STREAM(t.get_device())
+
+
+def _rows(name: str, t, shape):
+    """Pointer and strides of a device tensor [n][heads][D] whose channels are contiguous."""
+    if t.shape != shape or t.dim() != 3:
+        raise ValueError(f"kvc: {name} must be {list(shape)}, not {list(t.shape)}")
     if not t.is_cuda:
         raise ValueError("kvc: device tensors only (there is no CPU path)")
-    if t.dim() != 3 or t.shape[0] != n or t.shape[1] != heads or t.shape[2] != cache.head_dim:
-        raise ValueError(f"kvc: {name} must be [{n}][{heads}][{cache.head_dim}], not {list(t.shape)}")
-    if t.stride(2) != 1:
+    ts, hs, cs = t.stride()
+    if cs != 1:
         raise ValueError(f"kvc: the channels of {name} must be contiguous")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+    return t.data_ptr(), ts, hs
 
 
 def _ints(name: str, t, dt, shape):
-    if t.dtype != dt or tuple(t.shape) != shape:
+    if t.dtype != dt or t.shape != shape:
         raise ValueError(f"kvc: {name} must be {dt} of shape {list(shape)}, not {t.dtype} {list(t.shape)}")
     return _ptr(t)
 
@@ -511,36 +537,36 @@ def _ints(name: str, t, dt, shape):
 def kv4_append(cache: Kv4Cache, k, v, slots, stream=None):
     """Quantise k, v [T][H][D] (float16, bfloat16 or float32) into the slots
     int64 [T] (page * page_tokens + token in page; negative: skipped)."""
-    import torch
     n = k.shape[0]
     if v.dtype != k.dtype:
         raise ValueError("kvc: k and v must have one dtype")
-    kp, kts, khs = _rows(cache, "k", k, cache.n_kv_heads, n)
-    vp, vts, vhs = _rows(cache, "v", v, cache.n_kv_heads, n)
-    _check("kvc_kv4_append", _load().kvc_kv4_append(
-        cache.ref, kp, vp, n, kts, khs, vts, vhs, _kv4_dtype(k.dtype), _ints("slots", slots, torch.int64, (n,)),
-        cache.codes.data_ptr(), cache.params.data_ptr(), cache.dev_status.data_ptr(), _stream(stream)))
+    shape = (n, cache.n_kv_heads, cache.head_dim)
+    kp, kts, khs = _rows("k", k, shape)
+    vp, vts, vhs = _rows("v", v, shape)
+    rc = _load().kvc_kv4_append(cache.ref, kp, vp, n, kts, khs, vts, vhs, _kv4_dtype(k.dtype),
+                                _ints("slots", slots, cache.int64, (n,)), cache.codes_ptr, cache.params_ptr,
+                                cache.status_ptr, _kv4_stream(stream, k))
+    _check("kvc_kv4_append", rc)
 
 
 def kv4_read(cache: Kv4Cache, slots, dtype=None, k=None, v=None, stream=None):
     """The values at slots int64 [T], as (k, v) [T][H][D] of `dtype` (float16
     unless given) or written into k and v (one dtype, channels contiguous)."""
-    import torch
     if slots.dim() != 1:
         raise ValueError("kvc: slots must be int64 [T]")
     n = slots.shape[0]
     if dtype is None:
-        dtype = torch.float16 if k is None and v is None else (v if k is None else k).dtype
+        dtype = cache.params.dtype if k is None and v is None else (v if k is None else k).dtype
     shape = (n, cache.n_kv_heads, cache.head_dim)
-    k = torch.empty(shape, dtype=dtype, device=slots.device) if k is None else k
-    v = torch.empty(shape, dtype=dtype, device=slots.device) if v is None else v
+    k = slots.new_empty(shape, dtype=dtype) if k is None else k
+    v = slots.new_empty(shape, dtype=dtype) if v is None else v
     if k.dtype != dtype or v.dtype != dtype:
         raise ValueError("kvc: k and v must have one dtype")
-    kp, kts, khs = _rows(cache, "k", k, cache.n_kv_heads, n)
-    vp, vts, vhs = _rows(cache, "v", v, cache.n_kv_heads, n)
-    _check("kvc_kv4_read", _load().kvc_kv4_read(
-        cache.ref, cache.codes.data_ptr(), cache.params.data_ptr(), _ints("slots", slots, torch.int64, (n,)), n,
-        kp, vp, kts, khs, vts, vhs, _kv4_dtype(dtype), cache.dev_status.data_ptr(), _stream(stream)))
+    kp, kts, khs = _rows("k", k, shape)
+    vp, vts, vhs = _rows("v", v, shape)
+    rc = _load().kvc_kv4_read(cache.ref, cache.codes_ptr, cache.params_ptr, _ints("slots", slots, cache.int64, (n,)), n,
+                              kp, vp, kts, khs, vts, vhs, _kv4_dtype(dtype), cache.status_ptr, _kv4_stream(stream, k))
+    _check("kvc_kv4_read", rc)
     return k, v
 
 
@@ -562,12 +588,13 @@ def kv4_attention(cache: Kv4Cache, q, page_table, kv_len, cu_q=None, max_q: Opti
     sequence's queries (at most max_q; n_q if not given), without it every
     sequence has n_q / B.  `work`: uint8 of kv4_work_bytes, allocated if not
     given.  Returns out, or (out, lse float32 [n_q][Hq])."""
-    import torch
     if q.dim() != 3 or page_table.dim() != 2:
         raise ValueError("kvc: q must be [n_q][Hq][D], page_table [B][max_pages]")
     n_q, n_heads, _ = q.shape
+    shape = (n_q, n_heads, cache.head_dim)
     B, max_pages = page_table.shape
-    if page_table.dtype != torch.int32 or not page_table.is_cuda or (max_pages > 1 and page_table.stride(1) != 1):
+    i32, dtype = cache.int32, q.dtype
+    if page_table.dtype != i32 or not page_table.is_cuda or (max_pages > 1 and page_table.stride(1) != 1):
         raise ValueError("kvc: page_table must be a device int32 tensor with contiguous rows")
     if cu_q is None:
         if B == 0 or n_q % B:
@@ -578,26 +605,27 @@ def kv4_attention(cache: Kv4Cache, q, page_table, kv_len, cu_q=None, max_q: Opti
     elif max_q is None:
         max_q = n_q
     if out is None:
-        out = torch.empty((n_q, n_heads, cache.head_dim), dtype=q.dtype, device=q.device)
-    elif out.dtype != q.dtype:
+        out = q.new_empty(shape)
+    elif out.dtype != dtype:
         raise ValueError("kvc: out must have q's dtype")
     if lse is not None:
         return_lse = True
-        if lse.dtype != torch.float32 or tuple(lse.shape) != (n_q, n_heads):
+        if lse.dtype != cache.float32 or lse.shape != shape[:2]:
             raise ValueError("kvc: lse must be float32 [n_q][Hq]")
     elif return_lse:
-        lse = torch.empty((n_q, n_heads), dtype=torch.float32, device=q.device)
+        lse = q.new_empty(shape[:2], dtype=cache.float32)
     if work is None:
         nb = kv4_work_bytes(cache, n_q, n_heads, B, max_pages, max_q)
-        work = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
-    qp, qts, qhs = _rows(cache, "q", q, n_heads, n_q)
-    op, ots, ohs = _rows(cache, "out", out, n_heads, n_q)
-    args = KvcKv4Attn(
-        qp, op, _ptr(lse), qts, qhs, ots, ohs, page_table.data_ptr(), page_table.stride(0),
-        _ints("kv_len", kv_len, torch.int32, (B,)), None if cu_q is None else _ints("cu_q", cu_q, torch.int32, (B + 1,)),
-        n_q, B, n_heads, max_pages, max_q, _kv4_dtype(q.dtype), causal, window, softcap,
-        cache.head_dim ** -0.5 if scale is None else scale, _ptr(work), 0 if work is None else work.numel() * work.element_size())
-    _check("kvc_kv4_attention", _load().kvc_kv4_attention(
-        cache.ref, ctypes.byref(args), cache.codes.data_ptr(), cache.params.data_ptr(), cache.dev_status.data_ptr(),
-        _stream(stream)))
+        work = q.new_empty(nb, dtype=cache.codes.dtype) if nb else None
+    qp, qts, qhs = _rows("q", q, shape)
+    op, ots, ohs = _rows("out", out, shape)
+    args = _ATTN.pack(
+        qp, op, 0 if lse is None else _ptr(lse), qts, qhs, ots, ohs, page_table.data_ptr(), page_table.stride(0),
+        _ints("kv_len", kv_len, i32, (B,)), 0 if cu_q is None else _ints("cu_q", cu_q, i32, (B + 1,)),
+        n_q, B, n_heads, max_pages, max_q, _kv4_dtype(dtype), bool(causal), window, softcap,
+        cache.head_dim ** -0.5 if scale is None else scale, 0 if work is None else _ptr(work),
+        0 if work is None else work.numel() * work.element_size())
+    rc = _load().kvc_kv4_attention(cache.ref, args, cache.codes_ptr, cache.params_ptr, cache.status_ptr,
+                                   _kv4_stream(stream, q))
+    _check("kvc_kv4_attention", rc)
     return (out, lse) if return_lse else out

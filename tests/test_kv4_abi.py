@@ -134,3 +134,12 @@ def test_reference_layouts_are_permutations():
         assert len(seen) == 16 * D and max(b for b, _ in seen) == 16 * D // 2 - 1
         code = np.arange(D) % 16
         assert sorted(np.concatenate([kv4_ref.pack_k(code) & 15, kv4_ref.pack_k(code) >> 4])) == sorted(code)
+
+
+def test_packed_arguments_match_the_structure():
+    """The binding packs kvc_kv4_attn itself: same size, and every field where the structure has it."""
+    fields = [n for n, _ in kvc.KvcKv4Attn._fields_]
+    assert kvc._ATTN.size == ctypes.sizeof(kvc.KvcKv4Attn)
+    vals = [0.5 + i if n in ("softcap", "scale") else i + 1 for i, n in enumerate(fields)]
+    got = kvc.KvcKv4Attn.from_buffer_copy(kvc._ATTN.pack(*vals))
+    assert [getattr(got, n) for n in fields] == vals
