@@ -806,7 +806,7 @@ int64_t kvc_kv4_work_bytes(const kvc_kv4_desc *desc, int64_t n_q, int32_t n_seqs
     const int rc = make_pool(desc, p);
     if (rc != KVC_OK) return rc;
     if (!kv4_attn_sizes(p, n_q, n_seqs, n_q_heads, max_pages, max_q)) return KVC_ERR_ARG;
-    const Kv4Plan plan = kv4_plan(n_seqs, p.H, n_q_heads / p.H, max_q, (int64_t)max_pages << p.pshift);
+    const Kv4Plan plan = kv4_plan(p, n_seqs, n_q_heads / p.H, max_q, (int64_t)max_pages << p.pshift, 0);
     return plan.ns > 1 ? plan.ns * n_q * n_q_heads * (p.D + 2) * 4 : 0;
 }
 
@@ -830,8 +830,9 @@ int kvc_kv4_attention(const kvc_kv4_desc *desc, const kvc_kv4_attn *args, const 
         (dev_status && !aligned(dev_status, 4)))
         return KVC_ERR_ARG;
     if (!args->cu_q && (int64_t)args->n_seqs * args->max_q != args->n_q) return KVC_ERR_ARG;
-    const Kv4Plan plan = kv4_plan(args->n_seqs, a.pool.H, args->n_q_heads / a.pool.H, args->max_q,
-                                  (int64_t)args->max_pages << a.pool.pshift);
+    const int64_t most_keys = (int64_t)args->max_pages << a.pool.pshift;
+    a.window = args->window >= most_keys ? 0 : args->window;  // one that reaches past every key is none
+    const Kv4Plan plan = kv4_plan(a.pool, args->n_seqs, args->n_q_heads / a.pool.H, args->max_q, most_keys, a.window);
     const int64_t part = plan.ns > 1 ? plan.ns * args->n_q * args->n_q_heads : 0;
     if (part) {
         if (!args->work || !aligned(args->work, 16)) return KVC_ERR_ARG;
@@ -862,8 +863,6 @@ int kvc_kv4_attention(const kvc_kv4_desc *desc, const kvc_kv4_attn *args, const 
     a.max_pages = args->max_pages;
     a.max_q = args->max_q;
     a.causal = args->causal != 0;
-    // a window that reaches past every key is none
-    a.window = args->window >= (int64_t)args->max_pages << a.pool.pshift ? 0 : args->window;
     a.softcap = args->softcap;
     a.scale = args->scale;
     a.ns = plan.ns;

@@ -18,6 +18,8 @@
 // k indices): probabilities never cross lanes, the terms with lo and the row
 // sums are plain fp32 sums per lane, added over the four lanes of a row once
 // at the end.
+#include <algorithm>
+
 #include "kvc_kernels.h"
 #include "kvc_kv4.h"
 
@@ -590,17 +592,26 @@ hipError_t attend_dt(const Kv4Attn &a, bool bf16, hipStream_t s)
 
 }  // namespace
 
-Kv4Plan kv4_plan(int64_t n_seqs, int H, int R, int64_t max_q, int64_t max_keys)
+// How many ways a row's keys are split.  A split costs a block's start and its
+// part of the join, so it gets at least 256 keys while the blocks are fewer
+// than the compute units, 512 up to two blocks a unit (D = 256: a unit holds
+// one), 1024 beyond, up to eight a unit, which even out unequal sequences.
+// Measured with 8 kv heads of 128 (us a call, this rule against its
+// neighbours): 1 x 4000 keys 11.4 (at least 512: 14.4, 1024: 19.0), 1 x 16000
+// 15.4 (256: 18.5, 1024: 19.5), 64 x up to 8192 100 (1024 blocks 114, 4096 108),
+// 64 x up to 1000 21 (split in two 27.5).
+Kv4Plan kv4_plan(const Kv4Pool &p, int64_t n_seqs, int R, int64_t max_q, int64_t max_keys, int64_t window)
 {
-    Kv4Plan p;
-    p.tiles = (int32_t)((max_q * R + 15) / 16);
-    const int64_t blocks = n_seqs * H * p.tiles;
-    const int64_t units = (max_keys + 127) / 128;
-    int64_t ns = blocks ? 2048 / blocks : 1;
-    ns = ns < units ? ns : units;
-    ns = ns < 128 ? ns : 128;
-    p.ns = (int32_t)(ns < 1 ? 1 : ns);
-    return p;
+    Kv4Plan plan;
+    plan.tiles = (int32_t)((max_q * R + 15) / 16);
+    const int64_t blocks = n_seqs * p.H * plan.tiles;
+    if (window && window + max_q < max_keys) max_keys = window + max_q;
+    int64_t ns = 1;
+    const int64_t level[3][2] = {{256, 256}, {p.D == 256 ? 256 : 512, 512}, {2048, 1024}};  // blocks, keys
+    for (int i = 0; i < 3 && blocks; ++i)
+        ns = std::max(ns, std::min(level[i][0] / blocks, (max_keys + level[i][1] - 1) / level[i][1]));
+    plan.ns = (int32_t)std::min<int64_t>(ns, 128);
+    return plan;
 }
 
 hipError_t launch_kv4_attention(const Kv4Attn &a, bool bf16, hipStream_t stream)
