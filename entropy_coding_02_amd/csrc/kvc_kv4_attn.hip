@@ -1,16 +1,20 @@
 // kvc_kv4_attn.hip - attention over the resident 4-bit cache.
 //
-// With n a code (0..15) and m = 1 + n/16, a cached value is y = lo + 16 s (m - 1).
-// m has at most 5 significant bits and its bits are the code's under a constant
-// exponent, so one shift and one and-or turn two codes into two exact 16-bit
-// matrix operands, and (s, lo) never touch them:
-//   logits   q.k = sum_g s_g * 16 (sum_{c in g} q_c m_c - qs_g) + lo_g * qs_g,  qs_g = sum_{c in g} q_c;
-//            the products are exact, -qs_g is the accumulator's start;
-//   output   o_c = 16 sum_j (p_j s_jg) m_jc + sum_j p_j (lo_jg - 16 s_jg),  c in group g.
-// p_j s_jg goes into the matrix product as two bf16 terms (17 bits; bf16
-// because s spans the fp16 range), whatever the type of q: one rounding to 8
-// or 11 bits would be an error of the output's own size, since m is up to
-// four times the value it stands for.
+// A cached value is y = lo + s n, n = 0..15.  A code within the mantissa of an
+// fp16 whose exponent is zero is the subnormal n 2^-24 (or, four bits up,
+// n 2^-20), exactly, and the matrix instructions take subnormals as they are:
+// one mask turns two codes into two matrix operands, and (s, lo) never touch
+// them:
+//   logits   q.k = sum_g s_g (sum_{c in g} q_c n_c) + lo_g (sum_{c in g} q_c);
+//            a query row is scaled by a power of two to just under 2^15 (an
+//            fp16 then holds every bit of it that fp32 sums would), so the
+//            products are exact;
+//   output   o_c = sum_j (p_j s_jg) n_jc + sum_j p_j lo_jg,  c in group g.
+// p_j s_jg enters the matrix product as two fp16 terms (22 bits): one would
+// be an error of the output's own size, since n s is up to twice the value it
+// belongs to.  They keep those bits because p is taken relative not to the
+// row's maximum alone but also to a power of two above every s met so far:
+// p s lies just under 2^15 at its largest.
 //
 // Orientation: S^T = K q^T (16 keys x 16 query rows), so a lane holds one
 // query row and four keys of a tile, which is just what P^T needs as the
@@ -27,7 +31,7 @@ namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
@@ -39,38 +43,23 @@ __device__ __forceinline__ int32_t scalar_load(const int32_t *p, int64_t i) { re
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kWaves = 4;
 
-template <bool BF>
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c)
 {
-    if (BF)
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// The mask and the constant exponent that make pairs of 1 + n/16, held in
-// registers: as literals they cost a second instruction at every use.
-template <bool BF>
-struct Unit {
-    static constexpr int at = BF ? 3 : 6;  // the code's place below the exponent
-    uint32_t mask, one;
-    static __device__ __forceinline__ Unit make()
-    {
-        uint32_t mask = 0x000F000Fu << at, one = BF ? 0x3F803F80u : 0x3C003C00u;
-        __asm__("" : "+s"(mask), "+v"(one));
-        return Unit{mask, one};
-    }
-    // nibble i of both halves of w
-    __device__ __forceinline__ uint32_t pair(uint32_t w, int i) const
-    {
-        const uint32_t x = 4 * i <= at ? w << (at - 4 * i) : w >> (4 * i - at);
-        return (x & mask) | one;
-    }
-    // a K dword (8 channels of a key) as 8 operands in the order 0,4,1,5,2,6,3,7
-    __device__ __forceinline__ u32x4 octet(uint32_t w) const
-    {
-        return u32x4{pair(w, 0), pair(w, 1), pair(w, 2), pair(w, 3)};
-    }
-};
+// Nibble i of both halves of w as a pair of subnormals, n 2^-24 for an even i
+// and n 2^-20 for an odd one.
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int i)
+{
+    return (i < 2 ? w : w >> 8) & (i & 1 ? 0x00F000F0u : 0x000F000Fu);
+}
+// A K dword (8 channels of a key) as 8 operands in the order 0,4,1,5,2,6,3,7,
+// of which the odd pairs count 16 times (q has 1/16 of itself there).
+__device__ __forceinline__ u32x4 code_octet(uint32_t w)
+{
+    return u32x4{code_pair(w, 0), code_pair(w, 1), code_pair(w, 2), code_pair(w, 3)};
+}
 
 __device__ __forceinline__ float s_of(uint32_t w) { return kvc_h2f(w & 0xFFFF); }
 __device__ __forceinline__ float lo_of(uint32_t w) { return kvc_h2f(w >> 16); }
@@ -79,6 +68,12 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b)
 {
     const f32x2 v = {a, b};
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+__device__ __forceinline__ uint32_t f16_pair(float a, float b)
+{
+    const f16x2 v = {(_Float16)a, (_Float16)b};
+    return __builtin_bit_cast(uint32_t, v);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -191,60 +186,79 @@ __device__ __forceinline__ bool make_job(const Kv4Attn &a, Job &j)
     return true;
 }
 
-// Where a lane reads within a tile's blocks (bytes); the tiles' own places are
-// the same for the whole wave.
+// Where a lane reads, in bytes from a tile's place in its page's K block or K
+// parameters: V lies a fixed distance on.  (A page's codes are at most
+// 2 * 1024 heads * 256 tokens * 128 bytes.)
 template <int D, int G>
 struct LaneAt {
     static constexpr int NG = D / G, NP = (NG + 3) / 4;
-    uint32_t k, v, p[NP];
-    __device__ __forceinline__ LaneAt(int lane, int pshift)
+    uint32_t k, v, kp[NP], vp[NP];
+    __device__ __forceinline__ LaneAt(int lane, const Kv4Pool &p)
     {
         const int r = lane & 15, h = lane >> 4;
         k = r * (D / 2) + h * (D / 8);
-        v = h * (2 * D) + r * (D / 8);
+        v = h * (2 * D) + r * (D / 8) + ((uint32_t)p.H << p.pshift) * (D / 2);
         // group h (+ 4), key r; with fewer than four groups lanes repeat one
-#pragma unroll
-        for (int i = 0; i < NP; ++i) p[i] = (((uint32_t)((h + 4 * i) % NG) << pshift) + r) * 4;
+        for (int i = 0; i < NP; ++i) {
+            kp[i] = (((uint32_t)((h + 4 * i) % NG) << p.pshift) + r) * 4;
+            vp[i] = kp[i] + ((uint32_t)(p.H * NG) << p.pshift) * 4;
+        }
     }
 };
 
-// The table entries of a block's two tiles (a tile that no row sees is read
-// from one that some row does).
-__device__ __forceinline__ void load_pages(const Kv4Attn &a, const Job &j, int blk, int32_t *page)
-{
-    const int t_lo = j.kbeg >> 4, t_hi = (j.kend - 1) >> 4;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int kt = min(max(blk * 2 + t, t_lo), t_hi);
-        page[t] = a.table[j.b * a.table_stride + (kt >> (a.pool.pshift - 4))];
+// The same for the whole wave, kept in scalar registers: this (sequence, head)
+// and what a page number is multiplied by.
+template <int D, int G>
+struct WaveAt {
+    const int32_t *table;
+    const uint8_t *codes, *params;
+    uint32_t page_codes, page_params;  // bytes of a page
+    int t_lo, t_hi, shift, mask;       // tiles that some row sees; a tile's page and its place there
+    uint32_t n_pages;
+    __device__ __forceinline__ WaveAt(const Kv4Attn &a, const Job &j)
+    {
+        const int P = 1 << a.pool.pshift;
+        table = a.table + j.b * a.table_stride;
+        codes = a.pool.codes + (int64_t)j.h * (P * (D / 2));
+        params = (const uint8_t *)a.pool.params + (int64_t)j.h * (D / G * P * 4);
+        page_codes = (uint32_t)a.pool.H * P * D;
+        page_params = (uint32_t)a.pool.H * P * (D / G) * 8;
+        t_lo = j.kbeg >> 4;
+        t_hi = (j.kend - 1) >> 4;
+        shift = a.pool.pshift - 4;
+        mask = (P >> 4) - 1;
+        n_pages = (uint32_t)a.pool.n_pages;
     }
+    // A tile that no row sees is read from one that some row does.
+    __device__ __forceinline__ int tile(int blk, int t) const { return min(max(blk * 2 + t, t_lo), t_hi); }
+};
+
+// The table entries of a block's two tiles.
+template <int D, int G>
+__device__ __forceinline__ void load_pages(const WaveAt<D, G> &w, int blk, int32_t *page)
+{
+#pragma unroll
+    for (int t = 0; t < 2; ++t) page[t] = w.table[w.tile(blk, t) >> w.shift];
 }
 
 template <int D, int G>
-__device__ __forceinline__ void load_stage(const Kv4Attn &a, const Job &j, int blk, const int32_t *pages,
-                                           const LaneAt<D, G> &at, Stage<D, G> &st, bool &bad_page)
+__device__ __forceinline__ void load_stage(const WaveAt<D, G> &w, int blk, const int32_t *pages, const LaneAt<D, G> &at,
+                                           Stage<D, G> &st, bool &bad_page)
 {
-    constexpr int NG = D / G;
-    const int P = 1 << a.pool.pshift;
-    const int t_lo = j.kbeg >> 4, t_hi = (j.kend - 1) >> 4;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        const int kt = min(max(blk * 2 + t, t_lo), t_hi);
-        const int32_t entry = __builtin_amdgcn_readfirstlane(pages[t]);
-        const bool bad = (uint32_t)entry >= (uint32_t)a.pool.n_pages;
-        const int32_t page = bad ? 0 : entry;
-        bad_page |= bad;
-        const int off = (kt << 4) & (P - 1);
-        const int64_t kb = kv4_block(a.pool, page, 0, j.h), vb = kb + a.pool.H;
-        const uint8_t *kc = a.pool.codes + (kb * P + off) * (D / 2), *vc = a.pool.codes + (vb * P + off) * (D / 2);
-        const uint8_t *kp = (const uint8_t *)(a.pool.params + kb * NG * P + off);
-        const uint8_t *vp = (const uint8_t *)(a.pool.params + vb * NG * P + off);
-        load_words<D, G>(st.k[t], kc + at.k);
+        const uint32_t entry = (uint32_t)__builtin_amdgcn_readfirstlane(pages[t]);
+        bad_page |= entry >= w.n_pages;
+        const uint32_t page = entry < w.n_pages ? entry : 0;
+        const uint32_t in = (uint32_t)(w.tile(blk, t) & w.mask);
+        const uint8_t *codes = w.codes + (uint64_t)page * w.page_codes + in * (8 * D);
+        const uint8_t *params = w.params + (uint64_t)page * w.page_params + in * 64;
+        load_words<D, G>(st.k[t], codes + at.k);
 #pragma unroll
-        for (int i = 0; i < at.NP; ++i) st.kp[t][i] = *(const uint32_t *)(kp + at.p[i]);
-        load_words<D, G>(st.v[t], vc + at.v);
+        for (int i = 0; i < at.NP; ++i) st.kp[t][i] = *(const uint32_t *)(params + at.kp[i]);
+        load_words<D, G>(st.v[t], codes + at.v);
 #pragma unroll
-        for (int i = 0; i < at.NP; ++i) st.vp[t][i] = *(const uint32_t *)(vp + at.p[i]);
+        for (int i = 0; i < at.NP; ++i) st.vp[t][i] = *(const uint32_t *)(params + at.vp[i]);
     }
 }
 
@@ -266,88 +280,107 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
     const int b_end = min(j.u1 * 4, (j.kend + 31) / 32);
     int blk = j.u0 * 4 + wave;
     const bool work = blk < b_end;
+    const WaveAt<D, G> wat(a, j);
 
-    // Query operands in the codes' order, each wave a part, and the pages of
-    // its first two blocks.
+    // The pages of this wave's first two blocks, and its row of q (all of it,
+    // for the row's largest; every wave then stores a part of the operands).
     int32_t first[2] = {0, 0}, pages[2] = {0, 0};
-    u32x4 qw[NQ];
+    float up;  // what the lane's row of logits is to be multiplied by
     {
         const bool real = row < j.rows;
         const uint16_t *src = a.q + (int64_t)(j.q0 + qi) * a.q_ts + (int64_t)(j.h * a.R + row % a.R) * a.q_hs + 8 * h;
+        u32x4 qw[NW];
 #pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-            const int s = wave + i * kWaves;
-            qw[i] = u32x4{0, 0, 0, 0};
-            if (!real || s >= NW) continue;
+        for (int s = 0; s < NW; ++s) {
+            qw[s] = u32x4{0, 0, 0, 0};
+            if (!real) continue;
             if (a.q_vec)
-                qw[i] = *(const u32x4 *)(src + 32 * s);
+                qw[s] = *(const u32x4 *)(src + 32 * s);
             else
-                for (int k = 0; k < 4; ++k) qw[i][k] = src[32 * s + 2 * k] | (uint32_t)src[32 * s + 2 * k + 1] << 16;
+                for (int k = 0; k < 4; ++k) qw[s][k] = src[32 * s + 2 * k] | (uint32_t)src[32 * s + 2 * k + 1] << 16;
         }
         if (work) {
-            load_pages(a, j, blk, first);
-            load_pages(a, j, blk + kWaves, pages);
+            load_pages(wat, blk, first);
+            load_pages(wat, blk + kWaves, pages);
         }
-        // a negative scale becomes a positive one of -q, so that the largest
-        // logit is found before scaling
-        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+        uint32_t top = 0;  // the largest magnitude, by its bits
+#pragma unroll
+        for (int s = 0; s < NW; ++s)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = max(top, max(qw[s][k] & 0x7FFFu, qw[s][k] >> 16 & 0x7FFFu));
+        const float big = row_max(BF ? __builtin_bit_cast(float, top << 16) : kvc_h2f(top));
+        // 2^(14 - e) for a largest of 2^e (a row of zeros and one of Inf or
+        // NaN, taken for 0 here, stay as they are)
+        const int e = big > 0.0f && big < __builtin_inff() ? max((int)(__builtin_bit_cast(uint32_t, big) >> 23) - 127, -100) : 14;
+        const float f = __builtin_bit_cast(float, (uint32_t)(127 + 14 - e) << 23);
+        // A negative scale becomes a positive one of -q, so that the largest
+        // logit is found before scaling, and 0 one too small to tell (0 times
+        // the -inf of a masked key would be NaN).
+        const float sign = a.scale < 0.0f ? -f : f;
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
-            const u32x4 w = qw[i];
+            float y[8];
+            u32x4 w = qw[i * kWaves];
+#pragma unroll
+            for (int k = 1; k < kWaves; ++k)
+                if (k < NW && wave == k) w = qw[(i * kWaves + k) % NW];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t b = w[k / 2] >> (16 * (k & 1)) & 0xFFFFu;
+                y[k] = (BF ? __builtin_bit_cast(float, b << 16) : kvc_h2f(b)) * sign;
+            }
             if (wave + i * kWaves < NW)
-                lds_q[wave + i * kWaves][lane] = u32x4{(w[0] & 0xFFFF) | w[2] << 16, w[0] >> 16 | (w[2] & 0xFFFF0000u),
-                                                       (w[1] & 0xFFFF) | w[3] << 16, w[1] >> 16 | (w[3] & 0xFFFF0000u)} ^ flip;
+                lds_q[wave + i * kWaves][lane] =
+                    u32x4{f16_pair(y[0], y[4]), f16_pair(y[1] * 0.0625f, y[5] * 0.0625f), f16_pair(y[2], y[6]),
+                          f16_pair(y[3] * 0.0625f, y[7] * 0.0625f)};
         }
+        // 2^24 for the codes, 2^(e - 14) for q
+        up = fmaxf(__builtin_fabsf(a.scale), 1.0e-30f) * (a.softcap > 0.0f ? 1.0f : kLog2e);
+        up = fmaxf(up * __builtin_bit_cast(float, (uint32_t)(127 + min(24 - 14 + e, 127)) << 23), 1.0e-37f);
         lds_barrier();
     }
 
-    const Unit<BF> uk = Unit<BF>::make();
-    const Unit<true> uv = Unit<true>::make();
-    f32x4 o[NT], ps[NG];  // ps: the sums of the p s that went into o
-    float z[NG], m = -__builtin_inff(), l = 0.0f;
+    f32x4 o[NT];
+    // ref: the row's largest logit and 2^15 below the bound of s, in powers of 2
+    float z[NG], m = -__builtin_inff(), ref = -__builtin_inff(), l = 0.0f;
 #pragma unroll
     for (int c = 0; c < NT; ++c) o[c] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int g = 0; g < NG; ++g) z[g] = 0.0f, ps[g] = f32x4{0, 0, 0, 0};
+    for (int g = 0; g < NG; ++g) z[g] = 0.0f;
     if (work) {
-        const LaneAt<D, G> at(lane, a.pool.pshift);
+        const LaneAt<D, G> at(lane, a.pool);
         Stage<D, G> cur, next;
         bool bad_page = false;
-        load_stage<D, G>(a, j, blk, first, at, cur, bad_page);
+        load_stage<D, G>(wat, blk, first, at, cur, bad_page);
 
-        // the group sums of q as accumulators
-        f32x4 neg_qs[NG];
-        float qs16[NG];
+        // the group sums of q, in the codes' unit
+        float qs[NG];
         {
-            constexpr uint32_t one = BF ? 0xBF80BF80u : 0xBC00BC00u;  // -1
-            const u32x4 ones = {one, one, one, one};
+            const u32x4 ones = {0x3C003C00u, 0x4C004C00u, 0x3C003C00u, 0x4C004C00u};  // 1, 16
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 f32x4 c = {0, 0, 0, 0};
 #pragma unroll
-                for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) c = mfma<BF>(ones, lds_q[s][lane], c);
-                neg_qs[g] = c;
-                qs16[g] = -c[0] * (1.0f / 16.0f);
+                for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) c = mfma(ones, lds_q[s][lane], c);
+                qs[g] = c[0] * 0x1p-24f;
             }
         }
+        uint32_t s_top = 0;  // every s so far is at most this, by its bits
+        float s_exp = -39.0f;  // log2 of a power of two above it, less 15
         const int pos = j.pos0 + qi;
         const int k_hi = a.causal ? min(j.len, pos + 1) : j.len;  // keys k_lo <= key < k_hi
         const int k_lo = a.window ? max(0, pos - a.window + 1) : 0;
         // keys that every row of the tile sees
         const int all_hi = a.causal ? min(j.len, j.pos0 + j.row0 / a.R + 1) : j.len;
         const int all_lo = a.window ? j.pos0 + min(j.row0 + 15, j.rows - 1) / a.R - a.window + 1 : 0;
-        // a scale of 0 becomes one too small to tell: 0 times the -inf of a
-        // masked key would be NaN
-        const float c2 = 16.0f * fmaxf(__builtin_fabsf(a.scale), 1.0e-30f) * (a.softcap > 0.0f ? 1.0f : kLog2e);
-
         // A block's codes are on their way while the one before is worked on,
         // and its pages one block earlier still.  The last turns load the last
         // tile again rather than branch: where a load may or may not have been
         // issued, the wait for an older one is a wait for all.
         for (; blk < b_end; blk += kWaves) {
             int32_t after[2];  // loads return in order: before the codes, or they would wait for them
-            load_pages(a, j, blk + 2 * kWaves, after);
-            load_stage<D, G>(a, j, blk + kWaves, pages, at, next, bad_page);
+            load_pages(wat, blk + 2 * kWaves, after);
+            load_stage<D, G>(wat, blk + kWaves, pages, at, next, bad_page);
             pages[0] = after[0], pages[1] = after[1];
 
 #pragma unroll
@@ -357,32 +390,44 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
                     prm[t * TILE + 64 * i + lane] = cur.kp[t][i];
                     prm[(2 + t) * TILE + 64 * i + lane] = cur.vp[t][i];
                 }
+            const int key0 = blk * 32;
+            const bool partial = key0 + 32 > all_hi || key0 < all_lo;
+            // the largest s of the block: of this lane's share of the parameters
+            uint32_t s_here = 0;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    uint32_t w = cur.vp[t][i] & 0xFFFFu;
+                    if (partial && (key0 + 16 * t + col < j.kbeg || key0 + 16 * t + col >= j.kend)) w = 0;
+                    s_here = max(s_here, w);
+                }
             float x[2][4] = {};
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                f32x4 c[2] = {neg_qs[g], neg_qs[g]};
+                f32x4 c[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
                 for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) {
                     const u32x4 q = lds_q[s][lane];
-                    c[0] = mfma<BF>(uk.octet(cur.k[0][s]), q, c[0]);
-                    c[1] = mfma<BF>(uk.octet(cur.k[1][s]), q, c[1]);
+                    c[0] = mfma(code_octet(cur.k[0][s]), q, c[0]);
+                    c[1] = mfma(code_octet(cur.k[1][s]), q, c[1]);
                 }
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const u32x4 kp = *(const u32x4 *)&prm[t * TILE + 16 * g + 4 * h];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        x[t][i] = __builtin_fmaf(lo_of(kp[i]), qs16[g], __builtin_fmaf(s_of(kp[i]), c[t][i], x[t][i]));
+                        x[t][i] = __builtin_fmaf(lo_of(kp[i]), qs[g], __builtin_fmaf(s_of(kp[i]), c[t][i], x[t][i]));
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
-            float mul = c2;
+            float mul = up;
             if (a.softcap > 0.0f) {
                 // or the compiler computes this for every call
 #pragma unroll
                 for (int i = 0; i < 8; ++i) __asm__ volatile("" : "+v"(x[i / 4][i % 4]));
                 // c tanh(y / c) = c - 2c / (exp(2y / c) + 1), in powers of 2
-                const float in = c2 * 2.0f * kLog2e / a.softcap, top = a.softcap * kLog2e;
+                const float in = up * 2.0f * kLog2e / a.softcap, top = a.softcap * kLog2e;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     float &y = x[i / 4][i % 4];
@@ -390,8 +435,6 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
                 }
                 mul = 1.0f;
             }
-            const int key0 = blk * 32;
-            const bool partial = key0 + 32 > all_hi || key0 < all_lo;
             if (partial)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -403,17 +446,22 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
             for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[i / 4][i % 4]);
             mx = row_max(mx);
             mx = mx == -__builtin_inff() ? mx : mx * mul;
-            if (__any(mx > m)) {
-                const float mn = fmaxf(m, mx);
-                const float f = mn == -__builtin_inff() ? 1.0f : exp2_fast(m - mn);
-                m = mn;
+            if (__any(mx > m || s_here > s_top)) {
+                // s_exp is the wave's: its rows share the keys
+                for (int off = 32; off; off >>= 1) s_here = max(s_here, (uint32_t)__shfl_xor((int)s_here, off, 64));
+                s_top = max(s_top, s_here);
+                s_exp = s_top ? (float)((int)(__builtin_bit_cast(uint32_t, kvc_h2f(s_top)) >> 23) - 126 - 15) : -39.0f;
+                m = fmaxf(m, mx);
+                const float to = m + s_exp;
+                const float f = ref == -__builtin_inff() ? 1.0f : exp2_fast(ref - to);
+                ref = to;
                 l *= f;
 #pragma unroll
-                for (int g = 0; g < NG; ++g) z[g] *= f, ps[g] *= f;
+                for (int g = 0; g < NG; ++g) z[g] *= f;
 #pragma unroll
                 for (int c = 0; c < NT; ++c) o[c] *= f;
             }
-            const float mu = m == -__builtin_inff() ? 0.0f : m;
+            const float mu = ref == -__builtin_inff() ? 0.0f : ref;
             float p[2][4];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -434,25 +482,28 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
                 for (int i = 0; i < 8; i += 2) {
                     const uint32_t w0 = vp[i / 4][i % 4], w1 = vp[i / 4][i % 4 + 1];
                     const float p0 = p[i / 4][i % 4], p1 = p[i / 4][i % 4 + 1];
-                    const float a0 = p0 * s_of(w0), a1 = p1 * s_of(w1);
                     z[g] = __builtin_fmaf(p0, lo_of(w0), z[g]);
                     z[g] = __builtin_fmaf(p1, lo_of(w1), z[g]);
-                    const uint32_t hp = bf16_pair(a0, a1);
-                    hi[i / 2] = hp;
-                    lo[i / 2] = bf16_pair(a0 - __builtin_bit_cast(float, hp << 16),
-                                          a1 - __builtin_bit_cast(float, hp & 0xFFFF0000u));
+                    const f16x2 t = {(_Float16)__builtin_fmaf(p0, s_of(w0), 0.0f), (_Float16)__builtin_fmaf(p1, s_of(w1), 0.0f)};
+                    const f16x2 u = {(_Float16)__builtin_fmaf(p0, s_of(w0), -(float)t[0]),
+                                     (_Float16)__builtin_fmaf(p1, s_of(w1), -(float)t[1])};
+                    hi[i / 2] = __builtin_bit_cast(uint32_t, t);
+                    lo[i / 2] = __builtin_bit_cast(uint32_t, u);
                 }
-                const u32x4 ones = {uv.one, uv.one, uv.one, uv.one};
-                ps[g] = mfma<true>(ones, hi, ps[g]);
-                ps[g] = mfma<true>(ones, lo, ps[g]);
+// by pairs of tiles: the two terms of one would wait for each other
 #pragma unroll
-                for (int c = g * (G / 16); c < (g + 1) * (G / 16); ++c) {
+                for (int c = g * (G / 16); c < (g + 1) * (G / 16); c += 2) {
                     if (c % 4 == 0) __builtin_amdgcn_sched_barrier(0);
                     const int w = 2 * (c / 4);
-                    const u32x4 va = {uv.pair(cur.v[0][w], c & 3), uv.pair(cur.v[0][w + 1], c & 3),
-                                      uv.pair(cur.v[1][w], c & 3), uv.pair(cur.v[1][w + 1], c & 3)};
-                    o[c] = mfma<true>(va, hi, o[c]);
-                    o[c] = mfma<true>(va, lo, o[c]);
+                    u32x4 va[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        va[k] = u32x4{code_pair(cur.v[0][w], (c & 3) + k), code_pair(cur.v[0][w + 1], (c & 3) + k),
+                                      code_pair(cur.v[1][w], (c & 3) + k), code_pair(cur.v[1][w + 1], (c & 3) + k)};
+                    o[c] = mfma(va[0], hi, o[c]);
+                    o[c + 1] = mfma(va[1], hi, o[c + 1]);
+                    o[c] = mfma(va[0], lo, o[c]);
+                    o[c + 1] = mfma(va[1], lo, o[c + 1]);
                 }
             }
             cur = next;
@@ -464,16 +515,16 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
     // the four waves' parts: out = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w
     l = row_sum(l);
 #pragma unroll
-    for (int g = 0; g < NG; ++g) z[g] = row_sum(z[g]) - 16.0f * ps[g][0];
+    for (int g = 0; g < NG; ++g) z[g] = row_sum(z[g]);
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
         f32x4 y;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(16.0f, o[c][i], z[16 * c / G]);
+        for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(c & 1 ? 0x1p20f : 0x1p24f, o[c][i], z[16 * c / G]);
         *(f32x4 *)&lds_o[wave][col][16 * c + 4 * h] = y;
     }
     if (h == 0) {
-        lds_ml[wave][0][col] = m;
+        lds_ml[wave][0][col] = ref;
         lds_ml[wave][1][col] = l;
     }
     __syncthreads();
