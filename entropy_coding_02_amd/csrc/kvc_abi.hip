@@ -867,6 +867,7 @@ int kvc_kv4_attention(const kvc_kv4_desc *desc, const kvc_kv4_attn *args, const 
     a.scale = args->scale;
     a.ns = plan.ns;
     a.tiles = plan.tiles;
+    a.prompt = plan.prompt;
     return launch_status(launch_kv4_attention(a, args->dtype == KVC_BF16, (hipStream_t)stream));
 }
 

@@ -44,6 +44,7 @@ struct Kv4Attn {
     bool o_vec;                 // every 4-channel piece of out is 8-byte aligned
     int32_t ns;                 // splits of a row's keys
     int32_t tiles;              // tiles of query rows a (sequence, kv head)
+    bool prompt;                // which kernel: tiles of 128 rows rather than 16
     float *part_o;              // [ns][n_q * Hq][D]
     float *part_ml;             // [ns][n_q * Hq][2]
 };
@@ -57,6 +58,7 @@ hipError_t launch_kv4_read(const Kv4Pool &pool, const Kv4Rows &k, const Kv4Rows 
 // workspace size both follow them; a window never takes more splits than none).
 struct Kv4Plan {
     int32_t tiles, ns;
+    bool prompt;
 };
 Kv4Plan kv4_plan(const Kv4Pool &p, int64_t n_seqs, int R, int64_t max_q, int64_t max_keys, int64_t window);
 hipError_t launch_kv4_attention(const Kv4Attn &a, bool bf16, hipStream_t stream);

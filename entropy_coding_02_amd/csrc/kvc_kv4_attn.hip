@@ -135,7 +135,7 @@ __device__ __forceinline__ void load_words(uint32_t *dst, const uint8_t *src)
     }
 }
 
-// What a block works on: one (sequence, kv head), 16 of its query rows (row =
+// What a block works on: one (sequence, kv head), ROWS of its query rows (row =
 // query * R + head within the group), one split of their keys.
 struct Job {
     int b, h, split, tile;
@@ -144,13 +144,14 @@ struct Job {
     int u0, u1;      // the split's units of 128 keys
 };
 
+template <int ROWS>
 __device__ __forceinline__ bool make_job(const Kv4Attn &a, Job &j)
 {
     uint32_t id = blockIdx.x;
     j.split = id % a.ns, id /= a.ns;
     j.h = id % a.pool.H, id /= a.pool.H;
     j.b = id % a.B;
-    j.tile = id / a.B;
+    j.tile = a.tiles - 1 - id / a.B;  // under a causal mask the last tiles have the most keys: they go first
     bool bad = false;
     int64_t c0 = a.cu_q ? scalar_load(a.cu_q, j.b) : (int64_t)j.b * a.max_q;
     int64_t c1 = a.cu_q ? scalar_load(a.cu_q, j.b + 1) : c0 + a.max_q;
@@ -167,12 +168,12 @@ __device__ __forceinline__ bool make_job(const Kv4Attn &a, Job &j)
     j.len = scalar_load(a.kv_len, j.b);
     if (j.len > cap) bad = true, j.len = cap;
     if (j.len < 0) j.len = 0;
-    if (bad && j.tile == 0 && threadIdx.x == 0) kvc_flag(a.pool.status, KVC_DEV_BAD_INDEX);
+    if (bad && j.tile == a.tiles - 1 && threadIdx.x == 0) kvc_flag(a.pool.status, KVC_DEV_BAD_INDEX);
     j.rows = j.nq * a.R;
-    j.row0 = j.tile * 16;
+    j.row0 = j.tile * ROWS;
     if (j.row0 >= j.rows) return false;
     j.pos0 = j.len - j.nq;
-    const int last = j.row0 + 15 < j.rows ? j.row0 + 15 : j.rows - 1;
+    const int last = min(j.row0 + ROWS, j.rows) - 1;
     const int i_lo = j.row0 / a.R, i_hi = last / a.R;
     j.kend = a.causal ? min(j.len, j.pos0 + i_hi + 1) : j.len;
     j.kbeg = a.window ? max(0, j.pos0 + i_lo - a.window + 1) : 0;
@@ -262,6 +263,92 @@ __device__ __forceinline__ void load_stage(const WaveAt<D, G> &w, int blk, const
     }
 }
 
+// Four channels of an output row.
+template <bool BF>
+__device__ __forceinline__ void store_out(const Kv4Attn &a, int64_t tok, int head, int c, f32x4 y)
+{
+    uint16_t *dst = a.out + tok * a.o_ts + head * a.o_hs + c;
+    const u32x2 w = {BF ? bf16_pair(y[0], y[1]) : kvc_f2h2(y[0], y[1]), BF ? bf16_pair(y[2], y[3]) : kvc_f2h2(y[2], y[3])};
+    if (a.o_vec) {
+        *(u32x2 *)dst = w;
+    } else {
+        for (int i = 0; i < 4; ++i) dst[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+    }
+}
+
+// A lane's part of a query row: channels 8h .. 8h + 7 of every 32.
+template <int D, bool BF>
+__device__ __forceinline__ void load_query(const Kv4Attn &a, const Job &j, int row, int qi, int h, bool real, u32x4 *q)
+{
+    const uint16_t *src = a.q + (int64_t)(j.q0 + qi) * a.q_ts + (int64_t)(j.h * a.R + row % a.R) * a.q_hs + 8 * h;
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s) {
+        q[s] = u32x4{0, 0, 0, 0};
+        if (!real) continue;
+        if (a.q_vec)
+            q[s] = *(const u32x4 *)(src + 32 * s);
+        else
+            for (int k = 0; k < 4; ++k) q[s][k] = src[32 * s + 2 * k] | (uint32_t)src[32 * s + 2 * k + 1] << 16;
+    }
+}
+
+// The power of two (signed as the scale) that takes a row's largest to just
+// under 2^15, and `up`, what its logits are then to be multiplied by.
+template <int D, bool BF>
+__device__ __forceinline__ float scale_query(const Kv4Attn &a, const u32x4 *q, float &up)
+{
+    uint32_t top = 0;  // the largest magnitude, by its bits
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = max(top, max(q[s][k] & 0x7FFFu, q[s][k] >> 16 & 0x7FFFu));
+    const float big = row_max(BF ? __builtin_bit_cast(float, top << 16) : kvc_h2f(top));
+    // 2^(14 - e) for a largest of 2^e; a row of zeros, or one with Inf or NaN, stays as it is
+    const int e = big > 0.0f && big < __builtin_inff() ? max((int)(__builtin_bit_cast(uint32_t, big) >> 23) - 127, -100) : 14;
+    // A scale of 0 is one too small to tell (0 times the -inf of a masked key
+    // would be NaN).  2^24 is the codes' unit.
+    up = fmaxf(__builtin_fabsf(a.scale), 1.0e-30f) * (a.softcap > 0.0f ? 1.0f : kLog2e);
+    up = fmaxf(up * __builtin_bit_cast(float, (uint32_t)(127 + min(24 - 14 + e, 127)) << 23), 1.0e-37f);
+    // a negative scale becomes a positive one of -q, so that the largest logit is found before scaling
+    const float f = __builtin_bit_cast(float, (uint32_t)(127 + 14 - e) << 23);
+    return a.scale < 0.0f ? -f : f;
+}
+
+// Eight channels of q, scaled, in the order and weight of code_octet.
+template <bool BF>
+__device__ __forceinline__ u32x4 query_operand(u32x4 w, float f)
+{
+    float y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t b = w[k / 2] >> (16 * (k & 1)) & 0xFFFFu;
+        y[k] = (BF ? __builtin_bit_cast(float, b << 16) : kvc_h2f(b)) * f;
+    }
+    return u32x4{f16_pair(y[0], y[4]), f16_pair(y[1] * 0.0625f, y[5] * 0.0625f), f16_pair(y[2], y[6]),
+                 f16_pair(y[3] * 0.0625f, y[7] * 0.0625f)};
+}
+
+// log2 of a power of two above s (by its bits), less 15; of 2^-24 where all s are 0
+__device__ __forceinline__ float exponent_above(uint32_t s)
+{
+    return s ? (float)((int)(__builtin_bit_cast(uint32_t, kvc_h2f(s)) >> 23) - 126 - 15) : -39.0f;
+}
+
+// c tanh(x up / c) = c - 2c / (exp(2 x up / c) + 1), in powers of 2
+__device__ __forceinline__ void cap_logits(float cap, float (&x)[2][4], float &up)
+{
+    // or the compiler computes this for every call
+#pragma unroll
+    for (int i = 0; i < 8; ++i) __asm__ volatile("" : "+v"(x[i / 4][i % 4]));
+    const float in = up * 2.0f * kLog2e / cap, top = cap * kLog2e;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float &y = x[i / 4][i % 4];
+        y = top - 2.0f * top * __builtin_amdgcn_rcpf(exp2_fast(y * in) + 1.0f);
+    }
+    up = 1.0f;
+}
+
 template <int D, int G, bool BF>
 __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2 : 3) : 4) void k_kv4_attn(Kv4Attn a)
 {
@@ -272,7 +359,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
     // The query operands, which as registers would cost a wave a SIMD.
     __shared__ u32x4 lds_q[NW][64];
     Job j;
-    if (!make_job(a, j)) return;
+    if (!make_job<16>(a, j)) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, h = lane >> 4;  // this lane's query row, and its four keys of each tile
     uint32_t *const prm = (uint32_t *)&lds_o[wave][0][0];
@@ -287,56 +374,21 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
     int32_t first[2] = {0, 0}, pages[2] = {0, 0};
     float up;  // what the lane's row of logits is to be multiplied by
     {
-        const bool real = row < j.rows;
-        const uint16_t *src = a.q + (int64_t)(j.q0 + qi) * a.q_ts + (int64_t)(j.h * a.R + row % a.R) * a.q_hs + 8 * h;
         u32x4 qw[NW];
-#pragma unroll
-        for (int s = 0; s < NW; ++s) {
-            qw[s] = u32x4{0, 0, 0, 0};
-            if (!real) continue;
-            if (a.q_vec)
-                qw[s] = *(const u32x4 *)(src + 32 * s);
-            else
-                for (int k = 0; k < 4; ++k) qw[s][k] = src[32 * s + 2 * k] | (uint32_t)src[32 * s + 2 * k + 1] << 16;
-        }
+        load_query<D, BF>(a, j, row, qi, h, row < j.rows, qw);
         if (work) {
             load_pages(wat, blk, first);
             load_pages(wat, blk + kWaves, pages);
         }
-        uint32_t top = 0;  // the largest magnitude, by its bits
-#pragma unroll
-        for (int s = 0; s < NW; ++s)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) top = max(top, max(qw[s][k] & 0x7FFFu, qw[s][k] >> 16 & 0x7FFFu));
-        const float big = row_max(BF ? __builtin_bit_cast(float, top << 16) : kvc_h2f(top));
-        // 2^(14 - e) for a largest of 2^e (a row of zeros and one of Inf or
-        // NaN, taken for 0 here, stay as they are)
-        const int e = big > 0.0f && big < __builtin_inff() ? max((int)(__builtin_bit_cast(uint32_t, big) >> 23) - 127, -100) : 14;
-        const float f = __builtin_bit_cast(float, (uint32_t)(127 + 14 - e) << 23);
-        // A negative scale becomes a positive one of -q, so that the largest
-        // logit is found before scaling, and 0 one too small to tell (0 times
-        // the -inf of a masked key would be NaN).
-        const float sign = a.scale < 0.0f ? -f : f;
+        const float f = scale_query<D, BF>(a, qw, up);
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
-            float y[8];
             u32x4 w = qw[i * kWaves];
 #pragma unroll
             for (int k = 1; k < kWaves; ++k)
                 if (k < NW && wave == k) w = qw[(i * kWaves + k) % NW];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t b = w[k / 2] >> (16 * (k & 1)) & 0xFFFFu;
-                y[k] = (BF ? __builtin_bit_cast(float, b << 16) : kvc_h2f(b)) * sign;
-            }
-            if (wave + i * kWaves < NW)
-                lds_q[wave + i * kWaves][lane] =
-                    u32x4{f16_pair(y[0], y[4]), f16_pair(y[1] * 0.0625f, y[5] * 0.0625f), f16_pair(y[2], y[6]),
-                          f16_pair(y[3] * 0.0625f, y[7] * 0.0625f)};
+            if (wave + i * kWaves < NW) lds_q[wave + i * kWaves][lane] = query_operand<BF>(w, f);
         }
-        // 2^24 for the codes, 2^(e - 14) for q
-        up = fmaxf(__builtin_fabsf(a.scale), 1.0e-30f) * (a.softcap > 0.0f ? 1.0f : kLog2e);
-        up = fmaxf(up * __builtin_bit_cast(float, (uint32_t)(127 + min(24 - 14 + e, 127)) << 23), 1.0e-37f);
         lds_barrier();
     }
 
@@ -422,19 +474,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
             }
             __builtin_amdgcn_sched_barrier(0);
             float mul = up;
-            if (a.softcap > 0.0f) {
-                // or the compiler computes this for every call
-#pragma unroll
-                for (int i = 0; i < 8; ++i) __asm__ volatile("" : "+v"(x[i / 4][i % 4]));
-                // c tanh(y / c) = c - 2c / (exp(2y / c) + 1), in powers of 2
-                const float in = up * 2.0f * kLog2e / a.softcap, top = a.softcap * kLog2e;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float &y = x[i / 4][i % 4];
-                    y = top - 2.0f * top * __builtin_amdgcn_rcpf(exp2_fast(y * in) + 1.0f);
-                }
-                mul = 1.0f;
-            }
+            if (a.softcap > 0.0f) cap_logits(a.softcap, x, mul);
             if (partial)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -450,7 +490,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
                 // s_exp is the wave's: its rows share the keys
                 for (int off = 32; off; off >>= 1) s_here = max(s_here, (uint32_t)__shfl_xor((int)s_here, off, 64));
                 s_top = max(s_top, s_here);
-                s_exp = s_top ? (float)((int)(__builtin_bit_cast(uint32_t, kvc_h2f(s_top)) >> 23) - 126 - 15) : -39.0f;
+                s_exp = exponent_above(s_top);
                 m = fmaxf(m, mx);
                 const float to = m + s_exp;
                 const float f = ref == -__builtin_inff() ? 1.0f : exp2_fast(ref - to);
@@ -552,14 +592,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
         if (a.ns > 1) {
             *(f32x4 *)(a.part_o + prow * D + c) = y;
         } else {
-            uint16_t *dst = a.out + tok * a.o_ts + head * a.o_hs + c;
-            const u32x2 w = {BF ? bf16_pair(y[0], y[1]) : kvc_f2h2(y[0], y[1]), BF ? bf16_pair(y[2], y[3]) : kvc_f2h2(y[2], y[3])};
-            if (a.o_vec) {
-                *(u32x2 *)dst = w;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dst[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
-            }
+            store_out<BF>(a, tok, head, c, y);
         }
     }
     if (part == 0) {
@@ -568,6 +601,278 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
             a.part_ml[prow * 2 + 1] = L;
         } else if (a.lse) {
             a.lse[grow] = lse_of(M, L);
+        }
+    }
+}
+
+// ------------------------------------------------------------ prompt pieces
+
+constexpr int kRows = 128;   // query rows of a block, 32 a wave
+constexpr int kKeys = 64;    // keys a turn
+
+// Many query rows: a block's four waves have 32 rows each and share the keys.
+// Each wave unpacks a tile of 16 of a turn's 64 keys into LDS, as the matrix
+// operands that all of them read (in the order in which lanes read them: 16
+// bytes a lane, no conflicts), while the codes of the next turn are on their
+// way.  The terms are those of k_kv4_attn; with bf16 outputs p s is one fp16
+// term: its 2^-12 is an eighth of the output's own rounding, doubled by n s.
+template <int D, int G, bool BF>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
+{
+    constexpr int NW = D / 32, NG = D / G, NT = D / 16, NP = Stage<D, G>::NP, TILE = 64 * NP, TERMS = BF ? 1 : 2;
+    constexpr int NK = 4 * NW * 64, NV = 2 * NT * 64;  // 16-byte operands of a turn
+    struct Turn {
+        u32x4 k[NK], v[NV];
+        uint32_t kp[4 * TILE], vp[4 * TILE];
+    };
+    extern __shared__ __align__(16) uint8_t lds_raw[];
+    Turn *const turns = (Turn *)lds_raw;
+    Job j;
+    if (!make_job<kRows>(a, j)) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 15, h = lane >> 4;
+    const int t_end = min(j.u1 * 2, (j.kend + kKeys - 1) / kKeys);
+    int turn = j.u0 * 2;
+    const WaveAt<D, G> wat(a, j);
+    const LaneAt<D, G> at(lane, a.pool);
+
+    // the wave's rows: two column tiles of 16
+    const int row_w = j.row0 + 32 * wave;
+    u32x4 q[2][NW];
+    float up[2], qs[2][NG];
+    int k_lo[2], k_hi[2];
+#pragma unroll
+    for (int ct = 0; ct < 2; ++ct) {
+        const int row = row_w + 16 * ct + col, qi = row / a.R;
+        const bool real = row < j.rows;
+        const int pos = j.pos0 + qi;
+        k_hi[ct] = a.causal ? min(j.len, pos + 1) : j.len;
+        k_lo[ct] = a.window ? max(0, pos - a.window + 1) : 0;
+        load_query<D, BF>(a, j, row, qi, h, real, q[ct]);
+        const float sign = scale_query<D, BF>(a, q[ct], up[ct]);
+#pragma unroll
+        for (int s = 0; s < NW; ++s) q[ct][s] = query_operand<BF>(q[ct][s], sign);
+        const u32x4 ones = {0x3C003C00u, 0x4C004C00u, 0x3C003C00u, 0x4C004C00u};
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            f32x4 c = {0, 0, 0, 0};
+#pragma unroll
+            for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) c = mfma(ones, q[ct][s], c);
+            qs[ct][g] = c[0] * 0x1p-24f;
+        }
+    }
+    // keys that some row of the wave sees, and that every row does
+    const int last = min(row_w + 32, j.rows) - 1;
+    const int any_hi = row_w >= j.rows ? 0 : a.causal ? min(j.len, j.pos0 + last / a.R + 1) : j.len;
+    const int any_lo = a.window ? j.pos0 + row_w / a.R - a.window + 1 : 0;
+    const int all_hi = a.causal ? min(j.len, j.pos0 + row_w / a.R + 1) : j.len;
+    const int all_lo = a.window ? j.pos0 + last / a.R - a.window + 1 : 0;
+
+    f32x4 o[2][NT];
+    float z[2][NG], m[2], ref[2], l[2];
+#pragma unroll
+    for (int ct = 0; ct < 2; ++ct) {
+#pragma unroll
+        for (int c = 0; c < NT; ++c) o[ct][c] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int g = 0; g < NG; ++g) z[ct][g] = 0.0f;
+        m[ct] = ref[ct] = -__builtin_inff();
+        l[ct] = 0.0f;
+    }
+    uint32_t s_top = 0;
+    float s_exp = -39.0f;
+    bool bad_page = false;
+
+    // this wave's tile of a turn: loaded, then laid out in LDS
+    uint32_t kw[NW], vw[NW], kp[NP], vp[NP];
+    int32_t page = 0;
+    const auto fetch = [&](int t) {
+        const uint32_t entry = (uint32_t)__builtin_amdgcn_readfirstlane(page);
+        bad_page |= entry >= wat.n_pages;
+        const uint32_t pg = entry < wat.n_pages ? entry : 0;
+        const uint32_t in = (uint32_t)(wat.tile(2 * t, wave) & wat.mask);
+        const uint8_t *codes = wat.codes + (uint64_t)pg * wat.page_codes + in * (8 * D);
+        const uint8_t *params = wat.params + (uint64_t)pg * wat.page_params + in * 64;
+        load_words<D, G>(kw, codes + at.k);
+        load_words<D, G>(vw, codes + at.v);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            kp[i] = *(const uint32_t *)(params + at.kp[i]);
+            vp[i] = *(const uint32_t *)(params + at.vp[i]);
+        }
+    };
+    const auto look_up = [&](int t) { page = wat.table[wat.tile(2 * t, wave) >> wat.shift]; };
+    const auto lay_out = [&](int t, Turn &to) {
+#pragma unroll
+        for (int s = 0; s < NW; ++s) to.k[(wave * NW + s) * 64 + lane] = code_octet(kw[s]);
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+            const int w = 2 * (c / 4);
+            const u32x2 d = {code_pair(vw[w], c & 3), code_pair(vw[w + 1], c & 3)};
+            *(u32x2 *)((uint8_t *)&to.v[((wave >> 1) * NT + c) * 64 + lane] + 8 * (wave & 1)) = d;
+        }
+        // what lies at keys that no row sees may be anything
+        const int key = t * kKeys + 16 * wave + col;
+        const bool in = key >= j.kbeg && key < j.kend;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            to.kp[wave * TILE + 64 * i + lane] = in ? kp[i] : 0;
+            to.vp[wave * TILE + 64 * i + lane] = in ? vp[i] : 0;
+        }
+    };
+    if (turn < t_end) {
+        look_up(turn);
+        fetch(turn);
+        look_up(turn + 1);
+        lay_out(turn, turns[0]);
+    }
+    for (int side = 0; turn < t_end; ++turn, side ^= 1) {
+        lds_barrier();
+        const Turn &now = turns[side];
+        fetch(turn + 1);  // past the end: the last tile again
+        look_up(turn + 2);
+        if (turn * kKeys < any_hi && (turn + 1) * kKeys > any_lo) {
+            uint32_t s_here = 0;
+#pragma unroll
+            for (int i = 0; i < 4 * NP; ++i) s_here = max(s_here, now.vp[64 * i + lane] & 0xFFFFu);
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                const int key0 = turn * kKeys + 32 * half;
+                const bool partial = key0 + 32 > all_hi || key0 < all_lo;
+                float x[2][2][4] = {};
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        f32x4 c[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+                        for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) {
+                            const u32x4 k = now.k[((2 * half + t) * NW + s) * 64 + lane];
+                            c[0] = mfma(k, q[0][s], c[0]);
+                            c[1] = mfma(k, q[1][s], c[1]);
+                        }
+                        const u32x4 w = *(const u32x4 *)&now.kp[(2 * half + t) * TILE + 16 * g + 4 * h];
+#pragma unroll
+                        for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                x[ct][t][i] = __builtin_fmaf(lo_of(w[i]), qs[ct][g], __builtin_fmaf(s_of(w[i]), c[ct][i], x[ct][t][i]));
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                float mul[2] = {up[0], up[1]}, mx[2];
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct) {
+                    if (a.softcap > 0.0f) cap_logits(a.softcap, x[ct], mul[ct]);
+                    if (partial)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int key = key0 + 16 * (i / 4) + 4 * h + i % 4;
+                            if (key < k_lo[ct] || key >= k_hi[ct]) x[ct][i / 4][i % 4] = -__builtin_inff();
+                        }
+                    mx[ct] = x[ct][0][0];
+#pragma unroll
+                    for (int i = 1; i < 8; ++i) mx[ct] = fmaxf(mx[ct], x[ct][i / 4][i % 4]);
+                    mx[ct] = row_max(mx[ct]);
+                    mx[ct] = mx[ct] == -__builtin_inff() ? mx[ct] : mx[ct] * mul[ct];
+                }
+                if (__any(mx[0] > m[0] || mx[1] > m[1] || s_here > s_top)) {
+                    for (int off = 32; off; off >>= 1) s_here = max(s_here, (uint32_t)__shfl_xor((int)s_here, off, 64));
+                    s_top = max(s_top, s_here);
+                    s_exp = exponent_above(s_top);
+#pragma unroll
+                    for (int ct = 0; ct < 2; ++ct) {
+                        m[ct] = fmaxf(m[ct], mx[ct]);
+                        const float to = m[ct] + s_exp;
+                        const float f = ref[ct] == -__builtin_inff() ? 1.0f : exp2_fast(ref[ct] - to);
+                        ref[ct] = to;
+                        l[ct] *= f;
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) z[ct][g] *= f;
+#pragma unroll
+                        for (int c = 0; c < NT; ++c) o[ct][c] *= f;
+                    }
+                }
+                u32x4 ps[2][NG][TERMS];
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct) {
+                    const float mu = ref[ct] == -__builtin_inff() ? 0.0f : ref[ct];
+                    float p[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        p[i] = exp2_fast(__builtin_fmaf(x[ct][i / 4][i % 4], mul[ct], -mu));
+                        l[ct] += p[i];
+                    }
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        u32x4 w[2] = {*(const u32x4 *)&now.vp[(2 * half) * TILE + 16 * g + 4 * h],
+                                      *(const u32x4 *)&now.vp[(2 * half + 1) * TILE + 16 * g + 4 * h]};
+                        if (partial) {
+                            // a NaN there must not reach a row that does not see it
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (x[ct][i / 4][i % 4] == -__builtin_inff()) w[i / 4][i % 4] = 0;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2) {
+                            const uint32_t w0 = w[i / 4][i % 4], w1 = w[i / 4][i % 4 + 1];
+                            z[ct][g] = __builtin_fmaf(p[i], lo_of(w0), z[ct][g]);
+                            z[ct][g] = __builtin_fmaf(p[i + 1], lo_of(w1), z[ct][g]);
+                            const f16x2 t = {(_Float16)__builtin_fmaf(p[i], s_of(w0), 0.0f), (_Float16)__builtin_fmaf(p[i + 1], s_of(w1), 0.0f)};
+                            ps[ct][g][0][i / 2] = __builtin_bit_cast(uint32_t, t);
+                            if (TERMS == 2) {
+                                const f16x2 u = {(_Float16)__builtin_fmaf(p[i], s_of(w0), -(float)t[0]),
+                                                 (_Float16)__builtin_fmaf(p[i + 1], s_of(w1), -(float)t[1])};
+                                ps[ct][g][TERMS - 1][i / 2] = __builtin_bit_cast(uint32_t, u);
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < NT; ++c) {
+                    if (c % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+                    const u32x4 v = now.v[(half * NT + c) * 64 + lane];
+#pragma unroll
+                    for (int e = 0; e < TERMS; ++e) {
+                        o[0][c] = mfma(v, ps[0][16 * c / G][e], o[0][c]);
+                        o[1][c] = mfma(v, ps[1][16 * c / G][e], o[1][c]);
+                    }
+                }
+            }
+        }
+        lay_out(turn + 1, turns[side ^ 1]);  // nobody reads that side before the next barrier, nor since the last
+    }
+    if (bad_page && lane == 0) kvc_flag(a.pool.status, KVC_DEV_BAD_INDEX);
+
+#pragma unroll
+    for (int ct = 0; ct < 2; ++ct) {
+        l[ct] = row_sum(l[ct]);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) z[ct][g] = row_sum(z[ct][g]);
+        const int row = row_w + 16 * ct + col;
+        if (row >= j.rows) continue;
+        const int head = j.h * a.R + row % a.R;
+        const int64_t tok = j.q0 + row / a.R, grow = tok * a.Hq + head;
+        const int64_t prow = (int64_t)j.split * a.n_q * a.Hq + grow;
+        const float inv = a.ns > 1 ? 1.0f : (l[ct] == 0.0f ? 0.0f : 1.0f / l[ct]);
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+            f32x4 y;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                y[i] = __builtin_fmaf(c & 1 ? 0x1p20f : 0x1p24f, o[ct][c][i], z[ct][16 * c / G]) * inv;
+            if (a.ns > 1)
+                *(f32x4 *)(a.part_o + prow * D + 16 * c + 4 * h) = y;
+            else
+                store_out<BF>(a, tok, head, 16 * c + 4 * h, y);
+        }
+        if (h == 0) {
+            if (a.ns > 1) {
+                a.part_ml[prow * 2] = ref[ct];
+                a.part_ml[prow * 2 + 1] = l[ct];
+            } else if (a.lse) {
+                a.lse[grow] = lse_of(ref[ct], l[ct]);
+            }
         }
     }
 }
@@ -607,14 +912,7 @@ __global__ __launch_bounds__(THREADS) void k_kv4_join(Kv4Attn a)
     const int64_t tok = row / a.Hq;
     const int head = (int)(row % a.Hq);
     y *= L == 0.0f ? 0.0f : 1.0f / L;
-    uint16_t *dst = a.out + tok * a.o_ts + head * a.o_hs + 4 * part;
-    const u32x2 w = {BF ? bf16_pair(y[0], y[1]) : kvc_f2h2(y[0], y[1]), BF ? bf16_pair(y[2], y[3]) : kvc_f2h2(y[2], y[3])};
-    if (a.o_vec) {
-        *(u32x2 *)dst = w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dst[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
-    }
+    store_out<BF>(a, tok, head, 4 * part, y);
     if (a.lse && part == 0) a.lse[row] = lse_of(M, L);
 }
 
@@ -622,8 +920,19 @@ template <int D, int G, bool BF>
 hipError_t attend(const Kv4Attn &a, hipStream_t s)
 {
     const int64_t blocks = (int64_t)a.ns * a.pool.H * a.B * a.tiles;
-    k_kv4_attn<D, G, BF><<<dim3((uint32_t)blocks), dim3(64 * kWaves), 0, s>>>(a);
-    hipError_t e = hipGetLastError();
+    hipError_t e;
+    if (a.prompt) {
+        constexpr int lds = 2 * (4 * (D / 32) * 1024 + 2 * (D / 16) * 1024 + 2 * 4 * 64 * Stage<D, G>::NP * 4);
+        // above 64 KB LDS has to be asked for; the attribute is per device, and cheap
+        if (lds > 65536) {
+            e = hipFuncSetAttribute((const void *)k_kv4_prompt<D, G, BF>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+            if (e != hipSuccess) return e;
+        }
+        k_kv4_prompt<D, G, BF><<<dim3((uint32_t)blocks), dim3(256), lds, s>>>(a);
+    } else {
+        k_kv4_attn<D, G, BF><<<dim3((uint32_t)blocks), dim3(64 * kWaves), 0, s>>>(a);
+    }
+    e = hipGetLastError();
     if (e == hipSuccess && a.ns > 1) {
         const dim3 rows((uint32_t)(a.n_q * a.Hq));
         if (a.ns <= 8)
@@ -654,7 +963,9 @@ hipError_t attend_dt(const Kv4Attn &a, bool bf16, hipStream_t s)
 Kv4Plan kv4_plan(const Kv4Pool &p, int64_t n_seqs, int R, int64_t max_q, int64_t max_keys, int64_t window)
 {
     Kv4Plan plan;
-    plan.tiles = (int32_t)((max_q * R + 15) / 16);
+    plan.prompt = max_q * R > 64;
+    const int rows = plan.prompt ? kRows : 16;
+    plan.tiles = (int32_t)((max_q * R + rows - 1) / rows);
     const int64_t blocks = n_seqs * p.H * plan.tiles;
     if (window && window + max_q < max_keys) max_keys = window + max_q;
     int64_t ns = 1;
