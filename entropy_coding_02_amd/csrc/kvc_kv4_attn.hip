@@ -13,8 +13,10 @@
 // p_j s_jg enters the matrix product as two fp16 terms (22 bits): one would
 // be an error of the output's own size, since n s is up to twice the value it
 // belongs to.  They keep those bits because p is taken relative not to the
-// row's maximum alone but also to a power of two above every s met so far:
-// p s lies just under 2^15 at its largest.
+// row's maximum alone but also to a power of two above every s met so far: p s
+// is at most 2^7.  The maximum is let be until a logit passes it by 8 (in
+// powers of 2): the sums are rescaled a few times a row rather than at every
+// new maximum of any of a wave's rows, and p s stays below 2^15.
 //
 // Orientation: S^T = K q^T (16 keys x 16 query rows), so a lane holds one
 // query row and four keys of a tile, which is just what P^T needs as the
@@ -328,10 +330,10 @@ __device__ __forceinline__ u32x4 query_operand(u32x4 w, float f)
                  f16_pair(y[3] * 0.0625f, y[7] * 0.0625f)};
 }
 
-// log2 of a power of two above s (by its bits), less 15; of 2^-24 where all s are 0
+// log2 of a power of two above s (by its bits), less 7; of 2^-24 where all s are 0
 __device__ __forceinline__ float exponent_above(uint32_t s)
 {
-    return s ? (float)((int)(__builtin_bit_cast(uint32_t, kvc_h2f(s)) >> 23) - 126 - 15) : -39.0f;
+    return s ? (float)((int)(__builtin_bit_cast(uint32_t, kvc_h2f(s)) >> 23) - 126 - 7) : -31.0f;
 }
 
 // c tanh(x up / c) = c - 2c / (exp(2 x up / c) + 1), in powers of 2
@@ -393,8 +395,9 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
     }
 
     f32x4 o[NT];
-    // ref: the row's largest logit and 2^15 below the bound of s, in powers of 2
-    float z[NG], m = -__builtin_inff(), ref = -__builtin_inff(), l = 0.0f;
+    // In powers of 2: m, a logit that no later one passes by more than 8 (pass:
+    // that bound, in the unit of x), and ref, what p is relative to.
+    float z[NG], m = -__builtin_inff(), pass = -__builtin_inff(), ref = -__builtin_inff(), mu = 0.0f, l = 0.0f;
 #pragma unroll
     for (int c = 0; c < NT; ++c) o[c] = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -418,7 +421,6 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
             }
         }
         uint32_t s_top = 0;  // every s so far is at most this, by its bits
-        float s_exp = -39.0f;  // log2 of a power of two above it, less 15
         const int pos = j.pos0 + qi;
         const int k_hi = a.causal ? min(j.len, pos + 1) : j.len;  // keys k_lo <= key < k_hi
         const int k_lo = a.window ? max(0, pos - a.window + 1) : 0;
@@ -484,24 +486,22 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
             float mx = x[0][0];
 #pragma unroll
             for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[i / 4][i % 4]);
-            mx = row_max(mx);
-            mx = mx == -__builtin_inff() ? mx : mx * mul;
-            if (__any(mx > m || s_here > s_top)) {
+            if (__any(mx > pass || s_here > s_top)) {
                 // s_exp is the wave's: its rows share the keys
                 for (int off = 32; off; off >>= 1) s_here = max(s_here, (uint32_t)__shfl_xor((int)s_here, off, 64));
                 s_top = max(s_top, s_here);
-                s_exp = exponent_above(s_top);
-                m = fmaxf(m, mx);
-                const float to = m + s_exp;
+                mx = row_max(mx);
+                if (mx > pass) m = mx * mul, pass = (m + 8.0f) / mul;
+                const float to = m + exponent_above(s_top);
                 const float f = ref == -__builtin_inff() ? 1.0f : exp2_fast(ref - to);
                 ref = to;
+                mu = ref == -__builtin_inff() ? 0.0f : ref;
                 l *= f;
 #pragma unroll
                 for (int g = 0; g < NG; ++g) z[g] *= f;
 #pragma unroll
                 for (int c = 0; c < NT; ++c) o[c] *= f;
             }
-            const float mu = ref == -__builtin_inff() ? 0.0f : ref;
             float p[2][4];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -669,18 +669,17 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
     const int all_lo = a.window ? j.pos0 + last / a.R - a.window + 1 : 0;
 
     f32x4 o[2][NT];
-    float z[2][NG], m[2], ref[2], l[2];
+    float z[2][NG], m[2], pass[2], ref[2], mu[2], l[2];
 #pragma unroll
     for (int ct = 0; ct < 2; ++ct) {
 #pragma unroll
         for (int c = 0; c < NT; ++c) o[ct][c] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int g = 0; g < NG; ++g) z[ct][g] = 0.0f;
-        m[ct] = ref[ct] = -__builtin_inff();
-        l[ct] = 0.0f;
+        m[ct] = pass[ct] = ref[ct] = -__builtin_inff();
+        mu[ct] = l[ct] = 0.0f;
     }
     uint32_t s_top = 0;
-    float s_exp = -39.0f;
     bool bad_page = false;
 
     // this wave's tile of a turn: loaded, then laid out in LDS
@@ -773,19 +772,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
                     mx[ct] = x[ct][0][0];
 #pragma unroll
                     for (int i = 1; i < 8; ++i) mx[ct] = fmaxf(mx[ct], x[ct][i / 4][i % 4]);
-                    mx[ct] = row_max(mx[ct]);
-                    mx[ct] = mx[ct] == -__builtin_inff() ? mx[ct] : mx[ct] * mul[ct];
                 }
-                if (__any(mx[0] > m[0] || mx[1] > m[1] || s_here > s_top)) {
+                if (__any(mx[0] > pass[0] || mx[1] > pass[1] || s_here > s_top)) {
                     for (int off = 32; off; off >>= 1) s_here = max(s_here, (uint32_t)__shfl_xor((int)s_here, off, 64));
                     s_top = max(s_top, s_here);
-                    s_exp = exponent_above(s_top);
 #pragma unroll
                     for (int ct = 0; ct < 2; ++ct) {
-                        m[ct] = fmaxf(m[ct], mx[ct]);
-                        const float to = m[ct] + s_exp;
+                        mx[ct] = row_max(mx[ct]);
+                        if (mx[ct] > pass[ct]) m[ct] = mx[ct] * mul[ct], pass[ct] = (m[ct] + 8.0f) / mul[ct];
+                        const float to = m[ct] + exponent_above(s_top);
                         const float f = ref[ct] == -__builtin_inff() ? 1.0f : exp2_fast(ref[ct] - to);
                         ref[ct] = to;
+                        mu[ct] = ref[ct] == -__builtin_inff() ? 0.0f : ref[ct];
                         l[ct] *= f;
 #pragma unroll
                         for (int g = 0; g < NG; ++g) z[ct][g] *= f;
@@ -796,11 +794,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
                 u32x4 ps[2][NG][TERMS];
 #pragma unroll
                 for (int ct = 0; ct < 2; ++ct) {
-                    const float mu = ref[ct] == -__builtin_inff() ? 0.0f : ref[ct];
                     float p[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        p[i] = exp2_fast(__builtin_fmaf(x[ct][i / 4][i % 4], mul[ct], -mu));
+                        p[i] = exp2_fast(__builtin_fmaf(x[ct][i / 4][i % 4], mul[ct], -mu[ct]));
                         l[ct] += p[i];
                     }
 #pragma unroll
