@@ -807,7 +807,7 @@ int64_t kvc_kv4_work_bytes(const kvc_kv4_desc *desc, int64_t n_q, int32_t n_seqs
     if (rc != KVC_OK) return rc;
     if (!kv4_attn_sizes(p, n_q, n_seqs, n_q_heads, max_pages, max_q)) return KVC_ERR_ARG;
     const Kv4Plan plan = kv4_plan(p, n_seqs, n_q_heads / p.H, max_q, (int64_t)max_pages << p.pshift, 0);
-    return plan.ns > 1 ? plan.ns * n_q * n_q_heads * (p.D + 2) * 4 : 0;
+    return plan.most_ns > 1 ? plan.most_ns * n_q * n_q_heads * (p.D + 2) * 4 : 0;
 }
 
 int kvc_kv4_attention(const kvc_kv4_desc *desc, const kvc_kv4_attn *args, const uint8_t *codes,

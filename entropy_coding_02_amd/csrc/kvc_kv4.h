@@ -55,10 +55,11 @@ hipError_t launch_kv4_read(const Kv4Pool &pool, const Kv4Rows &k, const Kv4Rows 
                            int dtype, const int64_t *slots, hipStream_t stream);
 
 // Tiles of query rows and splits of the keys for a call (the launch and the
-// workspace size both follow them; a window never takes more splits than none).
+// workspace size both follow them).
 struct Kv4Plan {
     int32_t tiles, ns;
-    bool prompt;
+    int32_t most_ns;  // with window = 0: the most that any window makes it
+    bool prompt;      // which kernel
 };
 Kv4Plan kv4_plan(const Kv4Pool &p, int64_t n_seqs, int R, int64_t max_q, int64_t max_keys, int64_t window);
 hipError_t launch_kv4_attention(const Kv4Attn &a, bool bf16, hipStream_t stream);

@@ -487,7 +487,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
 #pragma unroll
             for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[i / 4][i % 4]);
             if (__any(mx > pass || s_here > s_top)) {
-                // s_exp is the wave's: its rows share the keys
+                // the bound of s is the wave's: its rows share the keys
                 for (int off = 32; off; off >>= 1) s_here = max(s_here, (uint32_t)__shfl_xor((int)s_here, off, 64));
                 s_top = max(s_top, s_here);
                 mx = row_max(mx);
@@ -623,7 +623,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
     constexpr int NK = 4 * NW * 64, NV = 2 * NT * 64;  // 16-byte operands of a turn
     struct Turn {
         u32x4 k[NK], v[NV];
-        uint32_t kp[4 * TILE], vp[4 * TILE];
+        float ks[4 * TILE], klo[4 * TILE];  // K's (s, lo), in fp32 once for all rows
+        uint32_t vp[4 * TILE];
     };
     extern __shared__ __align__(16) uint8_t lds_raw[];
     Turn *const turns = (Turn *)lds_raw;
@@ -715,7 +716,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
         const bool in = key >= j.kbeg && key < j.kend;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            to.kp[wave * TILE + 64 * i + lane] = in ? kp[i] : 0;
+            to.ks[wave * TILE + 64 * i + lane] = in ? s_of(kp[i]) : 0.0f;
+            to.klo[wave * TILE + 64 * i + lane] = in ? lo_of(kp[i]) : 0.0f;
             to.vp[wave * TILE + 64 * i + lane] = in ? vp[i] : 0;
         }
     };
@@ -738,7 +740,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
             for (int half = 0; half < 2; ++half) {
                 const int key0 = turn * kKeys + 32 * half;
                 const bool partial = key0 + 32 > all_hi || key0 < all_lo;
-                float x[2][2][4] = {};
+                float x[2][2][4];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
 #pragma unroll
@@ -750,12 +752,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
                             c[0] = mfma(k, q[0][s], c[0]);
                             c[1] = mfma(k, q[1][s], c[1]);
                         }
-                        const u32x4 w = *(const u32x4 *)&now.kp[(2 * half + t) * TILE + 16 * g + 4 * h];
+                        const f32x4 ks = *(const f32x4 *)&now.ks[(2 * half + t) * TILE + 16 * g + 4 * h];
+                        const f32x4 klo = *(const f32x4 *)&now.klo[(2 * half + t) * TILE + 16 * g + 4 * h];
 #pragma unroll
                         for (int ct = 0; ct < 2; ++ct)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                x[ct][t][i] = __builtin_fmaf(lo_of(w[i]), qs[ct][g], __builtin_fmaf(s_of(w[i]), c[ct][i], x[ct][t][i]));
+                                x[ct][t][i] = g == 0 ? __builtin_fmaf(klo[i], qs[ct][g], ks[i] * c[ct][i])
+                                                     : __builtin_fmaf(klo[i], qs[ct][g], __builtin_fmaf(ks[i], c[ct][i], x[ct][t][i]));
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);
@@ -919,7 +923,7 @@ hipError_t attend(const Kv4Attn &a, hipStream_t s)
     const int64_t blocks = (int64_t)a.ns * a.pool.H * a.B * a.tiles;
     hipError_t e;
     if (a.prompt) {
-        constexpr int lds = 2 * (4 * (D / 32) * 1024 + 2 * (D / 16) * 1024 + 2 * 4 * 64 * Stage<D, G>::NP * 4);
+        constexpr int lds = 2 * (4 * (D / 32) * 1024 + 2 * (D / 16) * 1024 + 3 * 4 * 64 * Stage<D, G>::NP * 4);
         // above 64 KB LDS has to be asked for; the attribute is per device, and cheap
         if (lds > 65536) {
             e = hipFuncSetAttribute((const void *)k_kv4_prompt<D, G, BF>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -949,27 +953,56 @@ hipError_t attend_dt(const Kv4Attn &a, bool bf16, hipStream_t s)
 
 }  // namespace
 
-// How many ways a row's keys are split.  A split costs a block's start and its
-// part of the join, so it gets at least 256 keys while the blocks are fewer
-// than the compute units, 512 up to two blocks a unit (D = 256: a unit holds
-// one), 1024 beyond, up to eight a unit, which even out unequal sequences.
-// Measured with 8 kv heads of 128 (us a call, this rule against its
-// neighbours): 1 x 4000 keys 11.4 (at least 512: 14.4, 1024: 19.0), 1 x 16000
-// 15.4 (256: 18.5, 1024: 19.5), 64 x up to 8192 100 (1024 blocks 114, 4096 108),
-// 64 x up to 1000 21 (split in two 27.5).
+// Which kernel, and how many ways a row's keys are split.
+//
+// Blocks of 128 rows unpack a key once for all of them, but are few and long:
+// they are taken where every sequence may fill one, the keys are 2048 or more
+// and blocks and thousands of keys together occupy the chip (8 kv heads of
+// 128, R = 4, us a call, this kernel against tiles of 16 rows: 2048 queries
+// over 8192 keys 415 : 576, 2 x 512 over 4096 169 : 174, 8 x 32 over 4096
+// 45 : 51, 128 over 16000 82 : 108; not for 1 x 64 over 4096 32 : 25, 1024
+// over 1024 49 : 40, nor D = 256 with G = 32, whose 512 registers do not
+// hold it, 310 : 242).  Split: two blocks a compute unit (2 x 512 over 4096
+// 169, unsplit 220, in four 181), 512 keys or more each.
+//
+// Tiles of 16 rows: a split costs a block's start and its part of the join, so
+// it gets at least 256 keys while the blocks are fewer than the compute units,
+// 512 up to two blocks a unit (D = 256: a unit holds one), 1024 beyond, up to
+// eight a unit, which even out unequal sequences (us a call, this rule against
+// its neighbours: 1 x 4000 keys 11.4, at least 512: 14.4, 1024: 19.0; 1 x 16000
+// 15.4, 256: 18.5, 1024: 19.5; 64 x up to 8192 100, 1024 blocks 114, 4096 108;
+// 64 x up to 1000 21, split in two 27.5).
+namespace {
+
+int64_t prompt_splits(const Kv4Pool &p, int64_t blocks, int64_t keys)
+{
+    const int64_t ns = std::min((p.D == 256 ? 256 : 512) / blocks, (keys + 511) / 512);
+    return std::min<int64_t>(std::max<int64_t>(ns, 1), 128);
+}
+
+int64_t narrow_splits(const Kv4Pool &p, int64_t blocks, int64_t keys)
+{
+    const int64_t level[3][2] = {{256, 256}, {p.D == 256 ? 256 : 512, 512}, {2048, 1024}};  // blocks, keys
+    int64_t ns = 1;
+    for (int i = 0; i < 3; ++i) ns = std::max(ns, std::min(level[i][0] / blocks, (keys + level[i][1] - 1) / level[i][1]));
+    return std::min<int64_t>(ns, 128);
+}
+
+}  // namespace
+
 Kv4Plan kv4_plan(const Kv4Pool &p, int64_t n_seqs, int R, int64_t max_q, int64_t max_keys, int64_t window)
 {
     Kv4Plan plan;
-    plan.prompt = max_q * R > 64;
-    const int rows = plan.prompt ? kRows : 16;
-    plan.tiles = (int32_t)((max_q * R + rows - 1) / rows);
-    const int64_t blocks = n_seqs * p.H * plan.tiles;
-    if (window && window + max_q < max_keys) max_keys = window + max_q;
-    int64_t ns = 1;
-    const int64_t level[3][2] = {{256, 256}, {p.D == 256 ? 256 : 512, 512}, {2048, 1024}};  // blocks, keys
-    for (int i = 0; i < 3 && blocks; ++i)
-        ns = std::max(ns, std::min(level[i][0] / blocks, (max_keys + level[i][1] - 1) / level[i][1]));
-    plan.ns = (int32_t)std::min<int64_t>(ns, 128);
+    // keys that a block of `rows` rows sees at most
+    const auto keys_of = [&](int rows) { return window ? std::min(max_keys, window + rows / R + 1) : max_keys; };
+    const int64_t wide_tiles = (max_q * R + kRows - 1) / kRows, tiles = (max_q * R + 15) / 16;
+    const int64_t wide = std::max<int64_t>(n_seqs * p.H * wide_tiles, 1), narrow = std::max<int64_t>(n_seqs * p.H * tiles, 1);
+    const int64_t keys = keys_of(kRows);
+    plan.prompt = max_q * R >= kRows && (p.D < 256 || p.G >= 64) && keys >= 2048 && wide * ((keys + 1023) / 1024) >= 256;
+    plan.tiles = (int32_t)(plan.prompt ? wide_tiles : tiles);
+    plan.ns = (int32_t)(plan.prompt ? prompt_splits(p, wide, keys) : narrow_splits(p, narrow, keys_of(16)));
+    // either kernel's splits grow with the keys, so no window takes more than these
+    plan.most_ns = (int32_t)std::max(narrow_splits(p, narrow, max_keys), plan.prompt ? prompt_splits(p, wide, max_keys) : 1);
     return plan;
 }
 

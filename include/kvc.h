@@ -522,7 +522,7 @@ typedef struct kvc_kv4_attn {
     int64_t work_bytes;
 } kvc_kv4_attn;
 
-/* Workspace of a call with these sizes (0 when no row's keys are split). */
+/* Workspace of a call with these sizes, whatever its window (0 when no row's keys are split). */
 int64_t kvc_kv4_work_bytes(const kvc_kv4_desc *desc, int64_t n_q, int32_t n_seqs, int32_t n_q_heads,
                            int32_t max_pages, int32_t max_q);
 

@@ -143,3 +143,25 @@ def test_packed_arguments_match_the_structure():
     vals = [0.5 + i if n in ("softcap", "scale") else i + 1 for i, n in enumerate(fields)]
     got = kvc.KvcKv4Attn.from_buffer_copy(kvc._ATTN.pack(*vals))
     assert [getattr(got, n) for n in fields] == vals
+
+
+@pytest.mark.parametrize("D,G", [(64, 64), (128, 64), (256, 32), (256, 64)])
+def test_workspace_covers_every_window(D, G):
+    """kvc_kv4_work_bytes does not know the window, which may change the launch: with that much workspace no
+    call is refused.  (Accepted calls fail at the launch: there is no device.)"""
+    import torch
+    if torch.cuda.device_count():
+        pytest.skip("accepted calls would launch on stand-in addresses")
+    lib = kvc.lib()
+    rng = np.random.default_rng(D)
+    for _ in range(400):
+        H, R, B = (int(rng.integers(1, n)) for n in (17, 13, 40))
+        max_q = int(2 ** rng.uniform(0, 11))
+        pages = int(2 ** rng.uniform(0, 12))
+        d = desc(H, D, G, 32, pages)
+        need = lib.kvc_kv4_work_bytes(d, B * max_q, B, H * R, pages, max_q)
+        assert need >= 0
+        for window in [0] + [int(2 ** rng.uniform(0, 17)) for _ in range(4)] + [2047, 2000, pages * 16]:
+            a = attn(cu_q=None, n_q=B * max_q, n_seqs=B, n_q_heads=H * R, max_pages=pages, max_q=max_q, window=window,
+                     work=OK if need else None, work_bytes=need)
+            assert lib.kvc_kv4_attention(d, ctypes.byref(a), OK, OK, None, None) == kvc.KVC_ERR_HIP
