@@ -2,10 +2,8 @@
 // back.  Both are bound by memory: a row of D channels is 2D (16-bit) or 4D
 // bytes outside and D/2 + 4D/G bytes in the cache.
 //
-// Work is cut into quads of four consecutive tokens of one head, because four
-// tokens' V pieces lie side by side in a page: a quad whose slots are four
-// consecutive ones at a multiple of four (any run of a prompt) moves its V
-// codes 8 bytes at a time, any other quad 2 bytes at a time.
+// Work is cut into quads of four consecutive tokens of one head: four tokens'
+// K rows and V pieces are neighbours in a page.
 #include "kvc_kernels.h"
 #include "kvc_kv4.h"
 
@@ -16,8 +14,7 @@ typedef _Float16 half1;
 template <int CTRL>
 __device__ __forceinline__ float dpp(float x)
 {
-    const int i = __builtin_bit_cast(int, x);
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, CTRL, 0xF, 0xF, false));
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true));
 }
 
 // Max over aligned runs of LANES lanes (4, 8 or 16), within a row of 16:
@@ -57,15 +54,23 @@ __device__ __forceinline__ void load8(const void *src, int64_t i, bool vec, floa
     }
 }
 
-// A channel's part in its group's extremes: x clamped to the fp16 range, and
-// for a non-finite x an infinity that no clamped x reaches.
-__device__ __forceinline__ void clamp_in(float &x, float &hi, float &nlo)
-{
-    const bool fin = __builtin_fabsf(x) < __builtin_inff();
-    x = fminf(fmaxf(x, -65504.0f), 65504.0f);
-    hi = fmaxf(hi, fin ? x : __builtin_inff());
-    nlo = fmaxf(nlo, -x);
-}
+// A group's extremes as a lane collects them.  0 * x is NaN where x is Inf or
+// NaN, and adding it up costs one operation a channel.
+struct Extremes {
+    float hi = -__builtin_inff(), nlo = -__builtin_inff(), zero = 0.0f;
+    __device__ __forceinline__ void take(float x)
+    {
+        hi = fmaxf(hi, x);
+        nlo = fmaxf(nlo, -x);
+        zero = __builtin_fmaf(x, 0.0f, zero);
+    }
+    // a group with Inf or NaN has hi = Inf; a finite x past the fp16 range counts as its border
+    __device__ __forceinline__ void close()
+    {
+        hi = zero == 0.0f ? __builtin_amdgcn_fmed3f(hi, -65504.0f, 65504.0f) : __builtin_inff();
+        nlo = __builtin_amdgcn_fmed3f(nlo, -65504.0f, 65504.0f);
+    }
+};
 
 struct GroupScale {
     uint32_t bits;  // s | lo << 16
@@ -81,11 +86,17 @@ __device__ __forceinline__ GroupScale group_scale(float hi, float nlo)
     const uint32_t lob = kvc_f2h(-nlo), sb = kvc_f2h(d * (1.0f / 15.0f));
     g.lo = kvc_h2f(lob);
     const float s = kvc_h2f(sb);
-    g.inv = s > 0.0f ? 1.0f / s : 0.0f;
+    // 1 / s, correctly rounded: the hardware's reciprocal is within one unit in
+    // the last place, and one Newton step in fused arithmetic from there rounds
+    // correctly unless the divisor's significand is all ones (Markstein 1990);
+    // s has 11 bits of 24.
+    const float y = __builtin_amdgcn_rcpf(s);
+    const float r = __builtin_fmaf(__builtin_fmaf(-s, y, 1.0f), y, y);
+    g.inv = s > 0.0f ? r : 0.0f;
     g.bits = sb | (lob << 16);
     if (g.bad) {
         g.bits = 0x7E00u << 16;
-        g.lo = g.inv = 0.0f;
+        g.lo = g.inv = 0.0f;  // every code 0 (0 times Inf or NaN is NaN, which the clamp takes to 0)
     }
     return g;
 }
@@ -93,7 +104,7 @@ __device__ __forceinline__ GroupScale group_scale(float hi, float nlo)
 __device__ __forceinline__ uint32_t code4(float x, const GroupScale &g)
 {
     const float r = __builtin_rintf((x - g.lo) * g.inv);
-    return g.bad ? 0u : (uint32_t)fminf(fmaxf(r, 0.0f), 15.0f);
+    return (uint32_t)fminf(fmaxf(r, 0.0f), 15.0f);
 }
 
 // The slots of a quad; a token that is past the end, skipped or out of the
@@ -119,107 +130,80 @@ __device__ __forceinline__ Quad load_quad(const Kv4Pool &p, const int64_t *slots
     return q;
 }
 
-// K: a lane quantises 8 contiguous channels of one token into one dword; a
-// group is G/8 neighbouring lanes.
-template <int D, int G, int DT>
-__device__ __forceinline__ void append_k(const Kv4Pool &p, const Kv4Rows &r, int64_t n, const int64_t *slots, uint32_t item)
+// The 16-bit V pieces that the four lanes of one u and one half of the n's hold
+// a nibble each of (i = 8u + 2c + half, c the nibble): every lane spreads its
+// codes, dword q holding pieces 2q and 2q + 1 of the half's eight, the four
+// are OR-ed, and lane c keeps dword c.
+__device__ __forceinline__ uint32_t v_pieces(uint32_t codes, int i)
+{
+    const int c = i / 2 % 4;
+    uint32_t d[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t two = codes >> (8 * q);
+        uint32_t w = ((two & 0xFu) | (two & 0xF0u) << 12) << (4 * c);
+        w |= (uint32_t)__builtin_amdgcn_mov_dpp((int)w, 0x4E, 0xF, 0xF, true);  // lanes i ^ 2
+        // lanes i ^ 4: i + 4 for the even quads of a row of 16, i - 4 for the odd ones
+        int o = __builtin_amdgcn_update_dpp((int)w, (int)w, 0x104, 0xF, 0x5, false);
+        o = __builtin_amdgcn_update_dpp(o, (int)w, 0x114, 0xF, 0xA, false);
+        d[q] = w | (uint32_t)o;
+    }
+    const uint32_t a = c & 1 ? d[1] : d[0], b = c & 1 ? d[3] : d[2];
+    return c & 2 ? b : a;
+}
+
+// A lane quantises 8 contiguous channels of one token: one K dword, or two V
+// pieces; a group is G/8 neighbouring lanes.  Both halves read alike, 16 bytes
+// a lane (a V half that read each piece's own channels, 2 bytes at a time, was
+// bound by L1 misses: 75 us against 45 for 32768 tokens of 8 heads of 128).
+template <int D, int G, int DT, bool V>
+__device__ __forceinline__ void append_rows(const Kv4Pool &p, const Kv4Rows &r, int64_t n, const int64_t *slots, uint32_t item)
 {
     const int i = item % (D / 8), tok = item / (D / 8) % 4;
     const uint32_t qh = item / (D / 2);
     const int head = qh % p.H;
     const int64_t t = (int64_t)(qh / p.H) * 4 + tok;
     if (t >= n) return;  // the D/8 lanes of a token leave together
+    float x[8];
+    load8<DT>(r.src, t * r.token_stride + head * r.head_stride + 8 * i, r.vec, x);
     const int64_t slot = slots[t];
     if (slot < 0 || slot >= p.n_pages << p.pshift) {
         if (slot >= 0 && i == 0) kvc_flag(p.status, KVC_DEV_BAD_INDEX);
         return;
     }
-    float x[8], hi = -__builtin_inff(), nlo = -__builtin_inff();
-    load8<DT>(r.src, t * r.token_stride + head * r.head_stride + 8 * i, r.vec, x);
-    for (int j = 0; j < 8; ++j) clamp_in(x[j], hi, nlo);
-    const GroupScale g = group_scale(run_max<G / 8>(hi), run_max<G / 8>(nlo));
+    Extremes e;
+    for (int j = 0; j < 8; ++j) e.take(x[j]);
+    e.close();
+    const GroupScale g = group_scale(run_max<G / 8>(e.hi), run_max<G / 8>(e.nlo));
     uint32_t w = 0;
     for (int j = 0; j < 8; ++j) w |= code4(x[j], g) << (4 * j);
     const int P = 1 << p.pshift, off = (int)(slot & (P - 1));
-    const int64_t blk = kv4_block(p, slot >> p.pshift, 0, head);
-    *(uint32_t *)(p.codes + blk * (P * (D / 2)) + off * (D / 2) + 4 * ((i % 4) * (D / 32) + i / 4)) = w;
+    const int64_t blk = kv4_block(p, slot >> p.pshift, V, head);
+    uint8_t *dst = p.codes + blk * (P * (D / 2));
+    if (V) {
+        const uint32_t two = v_pieces(w, i);
+        const int piece = 8 * (i % 2) + 2 * (i / 2 % 4);  // the first one's n
+        uint16_t *at = (uint16_t *)(dst + (off / 4) * (2 * D) + piece * (D / 8) + i / 8 * 8 + (off % 4) * 2);
+        at[0] = (uint16_t)two;
+        at[D / 16] = (uint16_t)(two >> 16);
+    } else {
+        *(uint32_t *)(dst + off * (D / 2) + 4 * ((i % 4) * (D / 32) + i / 4)) = w;
+    }
     if (i % (G / 8) == 0) {
         p.params[(blk * (D / G) + i / (G / 8)) * P + off] = g.bits;
         if (g.bad) kvc_flag(p.status, KVC_DEV_NONFINITE);
     }
 }
 
-// V: a lane quantises channels 64u + n + {0, 16, 32, 48} of the quad's four
-// tokens into four 16-bit pieces; a group of 64 is 16 lanes (the n), one of
-// 32 half of each lane's channels, one of 128 two runs of 16 lanes.
-template <int D, int G, int DT>
-__device__ __forceinline__ void append_v(const Kv4Pool &p, const Kv4Rows &r, int64_t n, const int64_t *slots, uint32_t item)
-{
-    constexpr int HALVES = G == 32 ? 2 : 1;
-    const int nn = item % 16, u = item / 16 % (D / 64);
-    const uint32_t qh = item / (D / 4);
-    const int head = qh % p.H;
-    const int64_t t0 = (int64_t)(qh / p.H) * 4;
-    if (t0 >= n) return;
-    const Quad q = load_quad(p, slots, t0, n, nn == 0 && u == 0);
-    uint32_t piece[4], bits[HALVES][4];
-    float x[4][4];
-    for (int k = 0; k < 4; ++k)
-        for (int j = 0; j < 4; ++j)
-            x[k][j] = q.slot[k] < 0 ? 0.0f
-                                    : load1((const uint16_t *)r.src, (t0 + k) * r.token_stride + head * r.head_stride + 64 * u + 16 * j + nn, DT);
-    bool bad = false;
-    for (int k = 0; k < 4; ++k) {
-        piece[k] = 0;
-        for (int f = 0; f < HALVES; ++f) {
-            float hi = -__builtin_inff(), nlo = -__builtin_inff();
-            for (int j = f * 4 / HALVES; j < (f + 1) * 4 / HALVES; ++j) clamp_in(x[k][j], hi, nlo);
-            hi = run_max<16>(hi), nlo = run_max<16>(nlo);
-            if (G == 128) {
-                hi = fmaxf(hi, __shfl_xor(hi, 16, 64));
-                nlo = fmaxf(nlo, __shfl_xor(nlo, 16, 64));
-            }
-            const GroupScale g = group_scale(hi, nlo);
-            for (int j = f * 4 / HALVES; j < (f + 1) * 4 / HALVES; ++j) piece[k] |= code4(x[k][j], g) << (4 * j);
-            bits[f][k] = g.bits;
-            bad |= g.bad;
-        }
-    }
-    const int P = 1 << p.pshift;
-    const bool owner = nn == 0 && (G < 128 || u % 2 == 0);
-    if (bad && owner) kvc_flag(p.status, KVC_DEV_NONFINITE);
-    const int grp = 64 * u / G;
-    if (q.run) {
-        const int off = (int)(q.slot[0] & (P - 1));
-        const int64_t blk = kv4_block(p, q.slot[0] >> p.pshift, 1, head);
-        const u32x2 w = {piece[0] | piece[1] << 16, piece[2] | piece[3] << 16};
-        *(u32x2 *)(p.codes + blk * (P * (D / 2)) + (off / 4) * (2 * D) + nn * (D / 8) + u * 8) = w;
-        if (owner)
-            for (int f = 0; f < HALVES; ++f) {
-                const u32x4 b = {bits[f][0], bits[f][1], bits[f][2], bits[f][3]};
-                *(u32x4 *)(p.params + (blk * (D / G) + grp + f) * P + off) = b;
-            }
-        return;
-    }
-    for (int k = 0; k < 4; ++k) {
-        if (q.slot[k] < 0) continue;
-        const int off = (int)(q.slot[k] & (P - 1));
-        const int64_t blk = kv4_block(p, q.slot[k] >> p.pshift, 1, head);
-        *(uint16_t *)(p.codes + blk * (P * (D / 2)) + (off / 4) * (2 * D) + nn * (D / 8) + u * 8 + (off % 4) * 2) =
-            (uint16_t)piece[k];
-        if (owner)
-            for (int f = 0; f < HALVES; ++f) p.params[(blk * (D / G) + grp + f) * P + off] = bits[f][k];
-    }
-}
-
-// Blocks 0 .. k_blocks - 1 write K, the rest V.
+// The first half of the blocks writes K, the second V; neighbouring blocks,
+// which fill the same lines of parameters, run on one XCD.
 template <int D, int G, int DT>
 __global__ __launch_bounds__(256) void k_kv4_append(Kv4Pool p, Kv4Rows k, Kv4Rows v, int64_t n, const int64_t *slots, uint32_t k_blocks)
 {
     if (blockIdx.x < k_blocks)
-        append_k<D, G, DT>(p, k, n, slots, blockIdx.x * 256 + threadIdx.x);
+        append_rows<D, G, DT, false>(p, k, n, slots, (uint32_t)xcd_block(blockIdx.x, k_blocks) * 256 + threadIdx.x);
     else
-        append_v<D, G, DT>(p, v, n, slots, (blockIdx.x - k_blocks) * 256 + threadIdx.x);
+        append_rows<D, G, DT, true>(p, v, n, slots, (uint32_t)xcd_block(blockIdx.x - k_blocks, k_blocks) * 256 + threadIdx.x);
 }
 
 template <int DT>
@@ -343,7 +327,7 @@ hipError_t move_rows(bool append, const Kv4Pool &p, const Kv4Rows &k, const Kv4R
 {
     const uint32_t qh = (uint32_t)((n + 3) / 4 * p.H);
     const uint32_t kb = append || k.dst ? (qh * (D / 2) + 255) / 256 : 0;
-    const uint32_t vb = append ? (qh * (D / 4) + 255) / 256 : (v.dst ? (qh * (D / 8) + 255) / 256 : 0);
+    const uint32_t vb = append ? kb : (v.dst ? (qh * (D / 8) + 255) / 256 : 0);
     const dim3 grid(kb + vb), block(256);
 #define KV4_CASE(KERNEL)                                                                       \
     if (dt == KVC_F16) KERNEL<D, G, KVC_F16><<<grid, block, 0, s>>>(p, k, v, n, slots, kb);      \
