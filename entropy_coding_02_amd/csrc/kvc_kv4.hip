@@ -9,7 +9,6 @@
 
 namespace {
 
-typedef _Float16 half1;
 
 template <int CTRL>
 __device__ __forceinline__ float dpp(float x)
@@ -30,29 +29,34 @@ __device__ __forceinline__ float run_max(float v)
     return v;
 }
 
-__device__ __forceinline__ float load1(const uint16_t *p, int64_t i, int dtype)
-{
-    if (dtype == KVC_F32) return ((const float *)p)[i];
-    const uint32_t b = p[i];
-    return dtype == KVC_F16 ? kvc_h2f(b) : __builtin_bit_cast(float, b << 16);
-}
-
+// Eight channels as they lie in memory, and as floats.
 template <int DT>
-__device__ __forceinline__ void load8(const void *src, int64_t i, bool vec, float *x)
-{
-    if (!vec) {
-        for (int j = 0; j < 8; ++j) x[j] = load1((const uint16_t *)src, i + j, DT);
-    } else if (DT == KVC_F32) {
-        const float4 a = *(const float4 *)((const float *)src + i), b = *(const float4 *)((const float *)src + i + 4);
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-        const u32x4 w = *(const u32x4 *)((const uint16_t *)src + i);
-        for (int j = 0; j < 4; ++j) {
-            x[2 * j] = DT == KVC_F16 ? kvc_h2f(w[j] & 0xFFFF) : __builtin_bit_cast(float, w[j] << 16);
-            x[2 * j + 1] = DT == KVC_F16 ? kvc_h2f(w[j] >> 16) : __builtin_bit_cast(float, w[j] & 0xFFFF0000u);
+struct Eight {
+    u32x4 w[DT == KVC_F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void *src, int64_t i, bool vec)
+    {
+        if (vec) {
+            const u32x4 *s = (const u32x4 *)((const uint8_t *)src + i * (DT == KVC_F32 ? 4 : 2));
+            w[0] = s[0];
+            if (DT == KVC_F32) w[DT == KVC_F32] = s[1];
+        } else if (DT == KVC_F32) {
+            for (int j = 0; j < 8; ++j) w[j / 4][j % 4] = ((const uint32_t *)src)[i + j];
+        } else {
+            for (int j = 0; j < 4; ++j)
+                w[0][j] = ((const uint16_t *)src)[i + 2 * j] | (uint32_t)((const uint16_t *)src)[i + 2 * j + 1] << 16;
         }
     }
-}
+    __device__ __forceinline__ float at(int j) const
+    {
+        if (DT == KVC_F32) {
+            const uint32_t b = w[j / 4][j % 4];
+            return __builtin_bit_cast(float, b);
+        }
+        const uint32_t b = w[0][j / 2 % 4];
+        if (DT == KVC_F16) return kvc_h2f(j & 1 ? b >> 16 : b & 0xFFFFu);
+        return __builtin_bit_cast(float, j & 1 ? b & 0xFFFF0000u : b << 16);
+    }
+};
 
 // A group's extremes as a lane collects them.  0 * x is NaN where x is Inf or
 // NaN, and adding it up costs one operation a channel.
@@ -155,55 +159,68 @@ __device__ __forceinline__ uint32_t v_pieces(uint32_t codes, int i)
 // A lane quantises 8 contiguous channels of one token: one K dword, or two V
 // pieces; a group is G/8 neighbouring lanes.  Both halves read alike, 16 bytes
 // a lane (a V half that read each piece's own channels, 2 bytes at a time, was
-// bound by L1 misses: 75 us against 45 for 32768 tokens of 8 heads of 128).
-template <int D, int G, int DT, bool V>
-__device__ __forceinline__ void append_rows(const Kv4Pool &p, const Kv4Rows &r, int64_t n, const int64_t *slots, uint32_t item)
+// bound by L1 misses: 75 us against 57 for 32768 tokens of 8 heads of 128).
+template <int D, int G, int DT, int ITEMS, bool V>
+__device__ __forceinline__ void append_rows(const Kv4Pool &p, const Kv4Rows &r, int64_t n, const int64_t *slots, uint32_t block)
 {
-    const int i = item % (D / 8), tok = item / (D / 8) % 4;
-    const uint32_t qh = item / (D / 2);
-    const int head = qh % p.H;
-    const int64_t t = (int64_t)(qh / p.H) * 4 + tok;
-    if (t >= n) return;  // the D/8 lanes of a token leave together
-    float x[8];
-    load8<DT>(r.src, t * r.token_stride + head * r.head_stride + 8 * i, r.vec, x);
-    const int64_t slot = slots[t];
-    if (slot < 0 || slot >= p.n_pages << p.pshift) {
-        if (slot >= 0 && i == 0) kvc_flag(p.status, KVC_DEV_BAD_INDEX);
-        return;
+    // ITEMS pieces a lane, their loads under way together
+    Eight<DT> x[ITEMS];
+    int64_t slot[ITEMS];
+    int head[ITEMS];
+    const int64_t end = p.n_pages << p.pshift;
+#pragma unroll
+    for (int u = 0; u < ITEMS; ++u) {
+        const uint32_t item = (block * ITEMS + u) * 256 + threadIdx.x;
+        const int i = item % (D / 8), tok = item / (D / 8) % 4;
+        const uint32_t qh = item / (D / 2);
+        head[u] = qh % p.H;
+        const int64_t t = (int64_t)(qh / p.H) * 4 + tok;
+        slot[u] = -1;
+        if (t >= n) continue;
+        slot[u] = slots[t];
+        x[u].load(r.src, t * r.token_stride + head[u] * r.head_stride + 8 * i, r.vec);
     }
-    Extremes e;
-    for (int j = 0; j < 8; ++j) e.take(x[j]);
-    e.close();
-    const GroupScale g = group_scale(run_max<G / 8>(e.hi), run_max<G / 8>(e.nlo));
-    uint32_t w = 0;
-    for (int j = 0; j < 8; ++j) w |= code4(x[j], g) << (4 * j);
-    const int P = 1 << p.pshift, off = (int)(slot & (P - 1));
-    const int64_t blk = kv4_block(p, slot >> p.pshift, V, head);
-    uint8_t *dst = p.codes + blk * (P * (D / 2));
-    if (V) {
-        const uint32_t two = v_pieces(w, i);
-        const int piece = 8 * (i % 2) + 2 * (i / 2 % 4);  // the first one's n
-        uint16_t *at = (uint16_t *)(dst + (off / 4) * (2 * D) + piece * (D / 8) + i / 8 * 8 + (off % 4) * 2);
-        at[0] = (uint16_t)two;
-        at[D / 16] = (uint16_t)(two >> 16);
-    } else {
-        *(uint32_t *)(dst + off * (D / 2) + 4 * ((i % 4) * (D / 32) + i / 4)) = w;
-    }
-    if (i % (G / 8) == 0) {
-        p.params[(blk * (D / G) + i / (G / 8)) * P + off] = g.bits;
-        if (g.bad) kvc_flag(p.status, KVC_DEV_NONFINITE);
+#pragma unroll
+    for (int u = 0; u < ITEMS; ++u) {
+        const int i = threadIdx.x % (D / 8);
+        if (slot[u] < 0 || slot[u] >= end) {  // the D/8 lanes of a token skip it together
+            if (slot[u] >= 0 && i == 0) kvc_flag(p.status, KVC_DEV_BAD_INDEX);
+            continue;
+        }
+        Extremes e;
+        for (int j = 0; j < 8; ++j) e.take(x[u].at(j));
+        e.close();
+        const GroupScale g = group_scale(run_max<G / 8>(e.hi), run_max<G / 8>(e.nlo));
+        uint32_t w = 0;
+        for (int j = 0; j < 8; ++j) w |= code4(x[u].at(j), g) << (4 * j);
+        const int P = 1 << p.pshift, off = (int)(slot[u] & (P - 1));
+        const int64_t blk = kv4_block(p, slot[u] >> p.pshift, V, head[u]);
+        uint8_t *dst = p.codes + blk * (P * (D / 2));
+        if (V) {
+            const uint32_t two = v_pieces(w, i);
+            const int piece = 8 * (i % 2) + 2 * (i / 2 % 4);  // the first one's n
+            uint16_t *at = (uint16_t *)(dst + (off / 4) * (2 * D) + piece * (D / 8) + i / 8 * 8 + (off % 4) * 2);
+            at[0] = (uint16_t)two;
+            at[D / 16] = (uint16_t)(two >> 16);
+        } else {
+            *(uint32_t *)(dst + off * (D / 2) + 4 * ((i % 4) * (D / 32) + i / 4)) = w;
+        }
+        if (i % (G / 8) == 0) {
+            p.params[(blk * (D / G) + i / (G / 8)) * P + off] = g.bits;
+            if (g.bad) kvc_flag(p.status, KVC_DEV_NONFINITE);
+        }
     }
 }
 
 // The first half of the blocks writes K, the second V; neighbouring blocks,
 // which fill the same lines of parameters, run on one XCD.
-template <int D, int G, int DT>
+template <int D, int G, int DT, int ITEMS>
 __global__ __launch_bounds__(256) void k_kv4_append(Kv4Pool p, Kv4Rows k, Kv4Rows v, int64_t n, const int64_t *slots, uint32_t k_blocks)
 {
     if (blockIdx.x < k_blocks)
-        append_rows<D, G, DT, false>(p, k, n, slots, (uint32_t)xcd_block(blockIdx.x, k_blocks) * 256 + threadIdx.x);
+        append_rows<D, G, DT, ITEMS, false>(p, k, n, slots, (uint32_t)xcd_block(blockIdx.x, k_blocks));
     else
-        append_rows<D, G, DT, true>(p, v, n, slots, (uint32_t)xcd_block(blockIdx.x - k_blocks, k_blocks) * 256 + threadIdx.x);
+        append_rows<D, G, DT, ITEMS, true>(p, v, n, slots, (uint32_t)xcd_block(blockIdx.x - k_blocks, k_blocks));
 }
 
 template <int DT>
@@ -245,26 +262,38 @@ __device__ __forceinline__ float value4(uint32_t code, uint32_t bits)
     return __builtin_fmaf((float)code, kvc_h2f(bits & 0xFFFF), kvc_h2f(bits >> 16));
 }
 
-template <int D, int G, int DT>
-__device__ __forceinline__ void read_k(const Kv4Pool &p, const Kv4Rows &r, int64_t n, const int64_t *slots, uint32_t item)
+template <int D, int G, int DT, int ITEMS>
+__device__ __forceinline__ void read_k(const Kv4Pool &p, const Kv4Rows &r, int64_t n, const int64_t *slots, uint32_t block)
 {
-    const int i = item % (D / 8), tok = item / (D / 8) % 4;
-    const uint32_t qh = item / (D / 2);
-    const int head = qh % p.H;
-    const int64_t t = (int64_t)(qh / p.H) * 4 + tok;
-    if (t >= n) return;
-    const int64_t slot = slots[t];
-    float y[8] = {};
-    if (slot >= 0 && slot < p.n_pages << p.pshift) {
-        const int P = 1 << p.pshift, off = (int)(slot & (P - 1));
-        const int64_t blk = kv4_block(p, slot >> p.pshift, 0, head);
-        const uint32_t w = *(const uint32_t *)(p.codes + blk * (P * (D / 2)) + off * (D / 2) + 4 * ((i % 4) * (D / 32) + i / 4));
-        const uint32_t b = p.params[(blk * (D / G) + i / (G / 8)) * P + off];
-        for (int j = 0; j < 8; ++j) y[j] = value4(w >> (4 * j) & 15, b);
-    } else if (slot >= 0 && i == 0) {
-        kvc_flag(p.status, KVC_DEV_BAD_INDEX);
+    uint32_t w[ITEMS], bits[ITEMS];
+    int64_t slot[ITEMS], t[ITEMS];
+    int head[ITEMS];
+    const int i = threadIdx.x % (D / 8), P = 1 << p.pshift;
+    const int64_t end = p.n_pages << p.pshift;
+#pragma unroll
+    for (int u = 0; u < ITEMS; ++u) {
+        const uint32_t item = (block * ITEMS + u) * 256 + threadIdx.x, qh = item / (D / 2);
+        head[u] = qh % p.H;
+        t[u] = (int64_t)(qh / p.H) * 4 + item / (D / 8) % 4;
+        slot[u] = t[u] < n ? slots[t[u]] : -1;
     }
-    store8<DT>(r.dst, t * r.token_stride + head * r.head_stride + 8 * i, r.vec, y);
+#pragma unroll
+    for (int u = 0; u < ITEMS; ++u) {
+        w[u] = bits[u] = 0;
+        if (slot[u] < 0 || slot[u] >= end) continue;
+        const int off = (int)(slot[u] & (P - 1));
+        const int64_t blk = kv4_block(p, slot[u] >> p.pshift, 0, head[u]);
+        w[u] = *(const uint32_t *)(p.codes + blk * (P * (D / 2)) + off * (D / 2) + 4 * ((i % 4) * (D / 32) + i / 4));
+        bits[u] = p.params[(blk * (D / G) + i / (G / 8)) * P + off];
+    }
+#pragma unroll
+    for (int u = 0; u < ITEMS; ++u) {
+        if (t[u] >= n) continue;
+        if (slot[u] >= end && i == 0) kvc_flag(p.status, KVC_DEV_BAD_INDEX);
+        float y[8];
+        for (int j = 0; j < 8; ++j) y[j] = value4(w[u] >> (4 * j) & 15, bits[u]);
+        store8<DT>(r.dst, t[u] * r.token_stride + head[u] * r.head_stride + 8 * i, r.vec, y);
+    }
 }
 
 // A lane writes channels 8i .. 8i + 7 of the quad's four tokens: one nibble of
@@ -312,13 +341,13 @@ __device__ __forceinline__ void read_v(const Kv4Pool &p, const Kv4Rows &r, int64
     }
 }
 
-template <int D, int G, int DT>
+template <int D, int G, int DT, int ITEMS>
 __global__ __launch_bounds__(256) void k_kv4_read(Kv4Pool p, Kv4Rows k, Kv4Rows v, int64_t n, const int64_t *slots, uint32_t k_blocks)
 {
     if (blockIdx.x < k_blocks)
-        read_k<D, G, DT>(p, k, n, slots, blockIdx.x * 256 + threadIdx.x);
+        read_k<D, G, DT, ITEMS>(p, k, n, slots, (uint32_t)xcd_block(blockIdx.x, k_blocks));
     else
-        read_v<D, G, DT>(p, v, n, slots, (blockIdx.x - k_blocks) * 256 + threadIdx.x);
+        read_v<D, G, DT>(p, v, n, slots, (uint32_t)xcd_block(blockIdx.x - k_blocks, gridDim.x - k_blocks) * 256 + threadIdx.x);
 }
 
 template <int D, int G>
@@ -326,15 +355,23 @@ hipError_t move_rows(bool append, const Kv4Pool &p, const Kv4Rows &k, const Kv4R
                      const int64_t *slots, hipStream_t s)
 {
     const uint32_t qh = (uint32_t)((n + 3) / 4 * p.H);
-    const uint32_t kb = append || k.dst ? (qh * (D / 2) + 255) / 256 : 0;
+    // One piece a lane while the chip is not full (64 tokens: 2.9 us, with two
+    // 3.4), two beyond (32768 tokens of 8 heads: 44 us, with one 57, four 44).
+    const int items = qh * (D / 2) > 256u * 2048u ? 2 : 1;
+    const uint32_t per = 256 * items;
+    const uint32_t kb = append || k.dst ? (qh * (D / 2) + per - 1) / per : 0;
     const uint32_t vb = append ? kb : (v.dst ? (qh * (D / 8) + 255) / 256 : 0);
     const dim3 grid(kb + vb), block(256);
-#define KV4_CASE(KERNEL)                                                                       \
-    if (dt == KVC_F16) KERNEL<D, G, KVC_F16><<<grid, block, 0, s>>>(p, k, v, n, slots, kb);      \
-    else if (dt == KVC_BF16) KERNEL<D, G, KVC_BF16><<<grid, block, 0, s>>>(p, k, v, n, slots, kb); \
-    else KERNEL<D, G, KVC_F32><<<grid, block, 0, s>>>(p, k, v, n, slots, kb);
+#define KV4_ITEMS(KERNEL, DT)                                                                        \
+    if (items == 2) KERNEL<D, G, DT, 2><<<grid, block, 0, s>>>(p, k, v, n, slots, kb);               \
+    else KERNEL<D, G, DT, 1><<<grid, block, 0, s>>>(p, k, v, n, slots, kb);
+#define KV4_CASE(KERNEL)                                                                             \
+    if (dt == KVC_F16) { KV4_ITEMS(KERNEL, KVC_F16) }                                                \
+    else if (dt == KVC_BF16) { KV4_ITEMS(KERNEL, KVC_BF16) }                                         \
+    else { KV4_ITEMS(KERNEL, KVC_F32) }
     if (append) { KV4_CASE(k_kv4_append) } else { KV4_CASE(k_kv4_read) }
 #undef KV4_CASE
+#undef KV4_ITEMS
     return hipGetLastError();
 }
 

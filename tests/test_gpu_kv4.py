@@ -526,3 +526,144 @@ def test_codec_to_cache_and_back():
     kvc.decode(buf)
     torch.cuda.synchronize()
     assert int(buf.dev_status.item()) == 0
+
+
+# ----------------------------------------- blocks of 128 rows: many queries, or a long table
+
+def widen(table, keys, P):
+    """The same sequences under a table of room for `keys` keys (the launch goes by the table's width)."""
+    wide = np.full((table.shape[0], keys // P), -1, np.int32)
+    wide[:, :table.shape[1]] = table
+    return wide
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("H,D,G,P,R", [(2, 64, 32, 16, 4), (1, 64, 64, 32, 5), (2, 128, 32, 64, 3), (2, 128, 64, 16, 4),
+                                       (1, 128, 128, 32, 8), (1, 256, 64, 32, 4), (1, 256, 128, 16, 2)])
+def test_wide_blocks_split(H, D, G, P, R, dt):
+    lens, nqs = [700, 130, 0, 65, 3], [150, 130, 7, 1, 40]
+    say(f"[gpu] kv4 wide H={H} D={D} G={G} P={P} R={R} {dt}")
+    cache, ref, table, slots = build(H, D, G, P, lens, dt, 31)
+    table = widen(table, 65536, P)
+    check(cache, ref, table, slots, lens, nqs, R, dt)
+    check(cache, ref, table, slots, lens, nqs, R, dt, causal=False)
+    check(cache, ref, table, slots, lens, nqs, R, dt, softcap=20.0, scale=-0.3)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("window", [0, 2100, 4000])
+def test_wide_blocks_window_and_pages_given_away(dt, window):
+    lens, nqs, P = [5000, 2300], [64, 40], 32
+    say(f"[gpu] kv4 wide window={window} {dt}")
+    cache, ref, table, slots = build(1, 128, 64, P, lens, dt, 32)
+    for b, (l, n) in enumerate(zip(lens, nqs)):
+        if window:
+            table[b, :max(0, l - n - window + 1) // P] = -1
+    check(cache, ref, widen(table, 1 << 19, P), slots, lens, nqs, 2, dt, window=window)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_wide_blocks_unsplit(dt):
+    B = 33
+    lens = [int(x) for x in np.random.default_rng(5).integers(1, 200, B)]
+    nqs = [min(l, 32) for l in lens]
+    nqs[0], lens[0] = 32, 190
+    say(f"[gpu] kv4 wide unsplit {dt}")
+    cache, ref, table, slots = build(8, 64, 64, 16, lens, dt, 33)
+    assert kvc.kv4_work_bytes(cache, sum(nqs), 32, B, 4096 // 16, 32) >= 0
+    check(cache, ref, widen(table, 4096, 16), slots, lens, nqs, 4, dt)
+
+
+def test_wide_blocks_bad_page_and_nan():
+    import torch
+    lens, nqs, P, R = [300], [300], 16, 2
+    cache, ref, table, slots = build(1, 128, 64, P, lens, "bf16", 34)
+    wide = widen(table, 1 << 19, P)
+    q = draw((300, R, 128), "bf16", 91)
+    args = (q.cuda(), torch.from_numpy(wide).cuda(), torch.tensor(lens, dtype=torch.int32).cuda())
+    good = kvc.kv4_attention(cache, *args)
+    assert status(cache) == 0
+    bad = wide.copy()
+    bad[0, 3] = cache.n_pages
+    out = kvc.kv4_attention(cache, args[0], torch.from_numpy(bad).cuda(), args[2])
+    assert status(cache) == kvc.KVC_DEV_BAD_INDEX
+    assert torch.equal(out[:48], good[:48])  # rows before the page
+    v = torch.zeros((1, 1, 128), dtype=torch.bfloat16, device="cuda")
+    v[0, 0, 100] = math.nan
+    kvc.kv4_append(cache, torch.zeros_like(v), v, torch.from_numpy(slots[0][150:151]).cuda())
+    assert status(cache) == kvc.KVC_DEV_NONFINITE
+    out, lse = kvc.kv4_attention(cache, *args, return_lse=True)
+    nan = torch.isnan(out)
+    assert not nan[:150].any() and not nan[:, :, :64].any() and nan[150:, :, 64:].all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_tiny_and_huge_values(dt):
+    """V and K far from 1: s near the ends of fp16, q beyond its range."""
+    import torch
+    H, D, G, P = 1, 128, 64, 16
+    lens = [200]
+    for kmul, vmul, qmul in ((1.0, 1e-3, 1.0), (1.0, 6000.0, 1.0), (1000.0, 1.0, 1e-4), (1e-3, 1.0, 3e4)):
+        cache, ref = fresh(H, D, G, P, 14)
+        k, v = draw(lens + [H, D], dt, 95, kmul), draw(lens + [H, D], dt, 96, vmul)
+        slots = np.arange(lens[0])
+        kvc.kv4_append(cache, k.cuda(), v.cuda(), torch.from_numpy(slots).cuda())
+        ref.write(f32(k), f32(v), slots)
+        table = np.arange(13, dtype=np.int32)[None]
+        q = (draw((40, 4, D), "bf16", 97).float() * qmul).clamp(-6e4, 6e4).to(tdt(dt))
+        for tab in (table, widen(table, 1 << 19, P)):
+            out, lse = kvc.kv4_attention(cache, q.cuda(), torch.from_numpy(tab).cuda(),
+                                         torch.tensor(lens, dtype=torch.int32).cuda(), return_lse=True)
+            assert status(cache) == 0
+            compare(out, lse, q, ref, [slots], lens, [40], 4, dt, True, 0, 0.0, D ** -0.5)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+def test_many_tokens_equal_few_at_a_time(dt):
+    """A call that fills the chip gives the bytes and values of small calls."""
+    import torch
+    H, D, G, P, T = 5, 64, 32, 32, 14003
+    n = -(-T // P)
+    k, v = draw((T, H, D), dt, 41).cuda(), draw((T, H, D), dt, 42, 0.1).cuda()
+    slots = torch.from_numpy(np.random.default_rng(6).permutation(n * P)[:T].astype(np.int64)).cuda()
+    slots[1000:9000] = torch.arange(1000, 9000).cuda()  # runs too; a slot met twice is written last by the later call
+    slots = torch.where(torch.isin(slots, torch.arange(1000, 9000).cuda()) &
+                        ((torch.arange(T).cuda() < 1000) | (torch.arange(T).cuda() >= 9000)), -1, slots)
+    a, _ = fresh(H, D, G, P, n)
+    b, _ = fresh(H, D, G, P, n)
+    kvc.kv4_append(a, k, v, slots)
+    for t in range(0, T, 4000):
+        kvc.kv4_append(b, k[t:t + 4000], v[t:t + 4000], slots[t:t + 4000])
+    assert status(a) == 0 and status(b) == 0
+    assert torch.equal(a.codes, b.codes) and torch.equal(a.params.view(torch.int16), b.params.view(torch.int16))
+    big = kvc.kv4_read(a, slots, dtype=tdt(dt))
+    for t in range(0, T, 4000):
+        few = kvc.kv4_read(b, slots[t:t + 4000], dtype=tdt(dt))
+        for x, y in zip(big, few):
+            assert torch.equal(x[t:t + 4000], y)
+
+
+def test_every_scale_has_its_reciprocal():
+    """Codes of groups whose s takes every positive fp16 value that it can: 1/s has to be rounded correctly."""
+    import torch
+    H, D, G, P = 1, 64, 32, 256
+    bits = np.arange(1, 0x7C00, dtype=np.uint16)
+    s = bits.view(np.float16).astype(np.float32)
+    s = s[s <= 4366.0]  # 15 s within fp16
+    rng = np.random.default_rng(8)
+    x = (rng.random((len(s), 1, D)).astype(np.float32) * 15.0) * s[:, None, None]
+    x[:, 0, ::G] = 0.0
+    x[:, 0, 1::G] = (15.0 * s)[:, None]
+    T = len(s)
+    n = -(-T // P)
+    cache, _ = fresh(H, D, G, P, n)
+    t = torch.from_numpy(x)
+    slots = torch.arange(T).cuda()
+    kvc.kv4_append(cache, t.cuda(), t.cuda(), slots)
+    assert status(cache) == 0
+    got = kvc.kv4_read(cache, slots, dtype=torch.float32)
+    c, sq, lo = kv4_ref.quantise(x, G)
+    want = kv4_ref.values(c, sq, lo, G).astype(np.float32)
+    assert len(np.unique(sq)) > 0.99 * len(s)
+    for y in got:
+        assert np.array_equal(y.cpu().numpy(), want)
