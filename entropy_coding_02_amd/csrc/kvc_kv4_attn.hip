@@ -330,10 +330,10 @@ __device__ __forceinline__ u32x4 query_operand(u32x4 w, float f)
                  f16_pair(y[3] * 0.0625f, y[7] * 0.0625f)};
 }
 
-// log2 of a power of two above s (by its bits), less 7; of 2^-24 where all s are 0
-__device__ __forceinline__ float exponent_above(uint32_t s)
+// log2 of a power of two above s, less 7; of 2^-24 where all s are 0
+__device__ __forceinline__ float exponent_above(float s)
 {
-    return s ? (float)((int)(__builtin_bit_cast(uint32_t, kvc_h2f(s)) >> 23) - 126 - 7) : -31.0f;
+    return s > 0.0f ? (float)((int)(__builtin_bit_cast(uint32_t, s) >> 23) - 126 - 7) : -31.0f;
 }
 
 // c tanh(x up / c) = c - 2c / (exp(2 x up / c) + 1), in powers of 2
@@ -492,7 +492,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
                 s_top = max(s_top, s_here);
                 mx = row_max(mx);
                 if (mx > pass) m = mx * mul, pass = (m + 8.0f) / mul;
-                const float to = m + exponent_above(s_top);
+                const float to = m + exponent_above(kvc_h2f(s_top));
                 const float f = ref == -__builtin_inff() ? 1.0f : exp2_fast(ref - to);
                 ref = to;
                 mu = ref == -__builtin_inff() ? 0.0f : ref;
@@ -624,7 +624,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
     struct Turn {
         u32x4 k[NK], v[NV];
         float ks[4 * TILE], klo[4 * TILE];  // K's (s, lo), in fp32 once for all rows
-        uint32_t vp[4 * TILE];
+        float vs[4 * TILE], vlo[4 * TILE];  // and V's
     };
     extern __shared__ __align__(16) uint8_t lds_raw[];
     Turn *const turns = (Turn *)lds_raw;
@@ -680,7 +680,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
         m[ct] = pass[ct] = ref[ct] = -__builtin_inff();
         mu[ct] = l[ct] = 0.0f;
     }
-    uint32_t s_top = 0;
+    float s_top = 0.0f;
     bool bad_page = false;
 
     // this wave's tile of a turn: loaded, then laid out in LDS
@@ -718,7 +718,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
         for (int i = 0; i < NP; ++i) {
             to.ks[wave * TILE + 64 * i + lane] = in ? s_of(kp[i]) : 0.0f;
             to.klo[wave * TILE + 64 * i + lane] = in ? lo_of(kp[i]) : 0.0f;
-            to.vp[wave * TILE + 64 * i + lane] = in ? vp[i] : 0;
+            to.vs[wave * TILE + 64 * i + lane] = in ? s_of(vp[i]) : 0.0f;
+            to.vlo[wave * TILE + 64 * i + lane] = in ? lo_of(vp[i]) : 0.0f;
         }
     };
     if (turn < t_end) {
@@ -733,9 +734,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
         fetch(turn + 1);  // past the end: the last tile again
         look_up(turn + 2);
         if (turn * kKeys < any_hi && (turn + 1) * kKeys > any_lo) {
-            uint32_t s_here = 0;
+            float s_here = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4 * NP; ++i) s_here = max(s_here, now.vp[64 * i + lane] & 0xFFFFu);
+            for (int i = 0; i < 4 * NP; ++i) s_here = fmaxf(s_here, now.vs[64 * i + lane]);
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
                 const int key0 = turn * kKeys + 32 * half;
@@ -778,8 +779,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
                     for (int i = 1; i < 8; ++i) mx[ct] = fmaxf(mx[ct], x[ct][i / 4][i % 4]);
                 }
                 if (__any(mx[0] > pass[0] || mx[1] > pass[1] || s_here > s_top)) {
-                    for (int off = 32; off; off >>= 1) s_here = max(s_here, (uint32_t)__shfl_xor((int)s_here, off, 64));
-                    s_top = max(s_top, s_here);
+                    for (int off = 32; off; off >>= 1) s_here = fmaxf(s_here, __shfl_xor(s_here, off, 64));
+                    s_top = fmaxf(s_top, s_here);
 #pragma unroll
                     for (int ct = 0; ct < 2; ++ct) {
                         mx[ct] = row_max(mx[ct]);
@@ -806,24 +807,29 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
                     }
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
-                        u32x4 w[2] = {*(const u32x4 *)&now.vp[(2 * half) * TILE + 16 * g + 4 * h],
-                                      *(const u32x4 *)&now.vp[(2 * half + 1) * TILE + 16 * g + 4 * h]};
+                        f32x4 vs[2], vlo[2];
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            vs[t] = *(const f32x4 *)&now.vs[(2 * half + t) * TILE + 16 * g + 4 * h];
+                            vlo[t] = *(const f32x4 *)&now.vlo[(2 * half + t) * TILE + 16 * g + 4 * h];
+                        }
                         if (partial) {
                             // a NaN there must not reach a row that does not see it
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
-                                if (x[ct][i / 4][i % 4] == -__builtin_inff()) w[i / 4][i % 4] = 0;
+                                if (x[ct][i / 4][i % 4] == -__builtin_inff()) vlo[i / 4][i % 4] = 0.0f;
                         }
 #pragma unroll
                         for (int i = 0; i < 8; i += 2) {
-                            const uint32_t w0 = w[i / 4][i % 4], w1 = w[i / 4][i % 4 + 1];
-                            z[ct][g] = __builtin_fmaf(p[i], lo_of(w0), z[ct][g]);
-                            z[ct][g] = __builtin_fmaf(p[i + 1], lo_of(w1), z[ct][g]);
-                            const f16x2 t = {(_Float16)__builtin_fmaf(p[i], s_of(w0), 0.0f), (_Float16)__builtin_fmaf(p[i + 1], s_of(w1), 0.0f)};
+                            const float s0 = vs[i / 4][i % 4], s1 = vs[i / 4][i % 4 + 1];
+                            z[ct][g] = __builtin_fmaf(p[i], vlo[i / 4][i % 4], z[ct][g]);
+                            z[ct][g] = __builtin_fmaf(p[i + 1], vlo[i / 4][i % 4 + 1], z[ct][g]);
+                            const f32x2 a2 = {p[i] * s0, p[i + 1] * s1};
+                            const f16x2 t = __builtin_convertvector(a2, f16x2);
                             ps[ct][g][0][i / 2] = __builtin_bit_cast(uint32_t, t);
                             if (TERMS == 2) {
-                                const f16x2 u = {(_Float16)__builtin_fmaf(p[i], s_of(w0), -(float)t[0]),
-                                                 (_Float16)__builtin_fmaf(p[i + 1], s_of(w1), -(float)t[1])};
+                                const f32x2 b2 = {a2[0] - (float)t[0], a2[1] - (float)t[1]};
+                                const f16x2 u = __builtin_convertvector(b2, f16x2);
                                 ps[ct][g][TERMS - 1][i / 2] = __builtin_bit_cast(uint32_t, u);
                             }
                         }
@@ -923,7 +929,7 @@ hipError_t attend(const Kv4Attn &a, hipStream_t s)
     const int64_t blocks = (int64_t)a.ns * a.pool.H * a.B * a.tiles;
     hipError_t e;
     if (a.prompt) {
-        constexpr int lds = 2 * (4 * (D / 32) * 1024 + 2 * (D / 16) * 1024 + 3 * 4 * 64 * Stage<D, G>::NP * 4);
+        constexpr int lds = 2 * (4 * (D / 32) * 1024 + 2 * (D / 16) * 1024 + 4 * 4 * 64 * Stage<D, G>::NP * 4);
         // above 64 KB LDS has to be asked for; the attribute is per device, and cheap
         if (lds > 65536) {
             e = hipFuncSetAttribute((const void *)k_kv4_prompt<D, G, BF>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -939,7 +945,7 @@ hipError_t attend(const Kv4Attn &a, hipStream_t s)
         if (a.ns <= 8)
             k_kv4_join<D, BF, 64><<<rows, dim3(64), 0, s>>>(a);
         else
-            k_kv4_join<D, BF, 256><<<rows, dim3(256), 0, s>>>(a);
+            k_kv4_join<D, BF, 512><<<rows, dim3(512), 0, s>>>(a);  // 79 splits of 64 rows: 4.9 us, by 256 threads 6.5
         e = hipGetLastError();
     }
     return e;
@@ -966,7 +972,8 @@ hipError_t attend_dt(const Kv4Attn &a, bool bf16, hipStream_t s)
 // 169, unsplit 220, in four 181), 512 keys or more each.
 //
 // Tiles of 16 rows: a split costs a block's start and its part of the join, so
-// it gets at least 256 keys while the blocks are fewer than the compute units,
+// 512 keys or fewer are not split (1 x 300 keys 9.1 us, in two 10.4), else it
+// gets at least 256 keys while the blocks are fewer than the compute units,
 // 512 up to two blocks a unit (D = 256: a unit holds one), 1024 beyond, up to
 // eight a unit, which even out unequal sequences (us a call, this rule against
 // its neighbours: 1 x 4000 keys 11.4, at least 512: 14.4, 1024: 19.0; 1 x 16000
@@ -984,7 +991,8 @@ int64_t narrow_splits(const Kv4Pool &p, int64_t blocks, int64_t keys)
 {
     const int64_t level[3][2] = {{256, 256}, {p.D == 256 ? 256 : 512, 512}, {2048, 1024}};  // blocks, keys
     int64_t ns = 1;
-    for (int i = 0; i < 3; ++i) ns = std::max(ns, std::min(level[i][0] / blocks, (keys + level[i][1] - 1) / level[i][1]));
+    if (keys > 512)
+        for (int i = 0; i < 3; ++i) ns = std::max(ns, std::min(level[i][0] / blocks, (keys + level[i][1] - 1) / level[i][1]));
     return std::min<int64_t>(ns, 128);
 }
 
