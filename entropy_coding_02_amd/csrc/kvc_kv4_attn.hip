@@ -355,7 +355,8 @@ template <int D, int G, bool BF>
 __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2 : 3) : 4) void k_kv4_attn(Kv4Attn a)
 {
     constexpr int NW = D / 32, NG = D / G, NT = D / 16, NP = Stage<D, G>::NP, TILE = 64 * NP, NQ = (NW + kWaves - 1) / kWaves;
-    // Each wave's results; while it runs, its [K|V][tile][group][16 keys] parameters.
+    // Each wave's results; while it runs, its [K|V][tile][s|lo][group][16 keys]
+    // parameters, in fp32 (mixed-precision instructions run at half rate).
     __shared__ __align__(16) float lds_o[kWaves][16][D];
     __shared__ float lds_ml[kWaves][2][16];
     // The query operands, which as registers would cost a wave a SIMD.
@@ -364,7 +365,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
     if (!make_job<16>(a, j)) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, h = lane >> 4;  // this lane's query row, and its four keys of each tile
-    uint32_t *const prm = (uint32_t *)&lds_o[wave][0][0];
+    float *const prm = &lds_o[wave][0][0];
+    static_assert(8 * TILE <= 16 * D, "the parameters fit where the results go");
     const int row = j.row0 + col, qi = row / a.R;
     const int b_end = min(j.u1 * 4, (j.kend + 31) / 32);
     int blk = j.u0 * 4 + wave;
@@ -441,8 +443,10 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
-                    prm[t * TILE + 64 * i + lane] = cur.kp[t][i];
-                    prm[(2 + t) * TILE + 64 * i + lane] = cur.vp[t][i];
+                    prm[(2 * t) * TILE + 64 * i + lane] = s_of(cur.kp[t][i]);
+                    prm[(2 * t + 1) * TILE + 64 * i + lane] = lo_of(cur.kp[t][i]);
+                    prm[(2 * t + 4) * TILE + 64 * i + lane] = s_of(cur.vp[t][i]);
+                    prm[(2 * t + 5) * TILE + 64 * i + lane] = lo_of(cur.vp[t][i]);
                 }
             const int key0 = blk * 32;
             const bool partial = key0 + 32 > all_hi || key0 < all_lo;
@@ -456,7 +460,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
                     if (partial && (key0 + 16 * t + col < j.kbeg || key0 + 16 * t + col >= j.kend)) w = 0;
                     s_here = max(s_here, w);
                 }
-            float x[2][4] = {};
+            float x[2][4];
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 f32x4 c[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
@@ -468,10 +472,12 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
                 }
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    const u32x4 kp = *(const u32x4 *)&prm[t * TILE + 16 * g + 4 * h];
+                    const f32x4 ks = *(const f32x4 *)&prm[(2 * t) * TILE + 16 * g + 4 * h];
+                    const f32x4 klo = *(const f32x4 *)&prm[(2 * t + 1) * TILE + 16 * g + 4 * h];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        x[t][i] = __builtin_fmaf(lo_of(kp[i]), qs[g], __builtin_fmaf(s_of(kp[i]), c[t][i], x[t][i]));
+                        x[t][i] = g == 0 ? __builtin_fmaf(klo[i], qs[g], ks[i] * c[t][i])
+                                         : __builtin_fmaf(klo[i], qs[g], __builtin_fmaf(ks[i], c[t][i], x[t][i]));
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -511,24 +517,29 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 u32x4 hi, lo;
-                u32x4 vp[2] = {*(const u32x4 *)&prm[2 * TILE + 16 * g + 4 * h], *(const u32x4 *)&prm[3 * TILE + 16 * g + 4 * h]};
+                f32x4 vs[2], vlo[2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    vs[t] = *(const f32x4 *)&prm[(2 * t + 4) * TILE + 16 * g + 4 * h];
+                    vlo[t] = *(const f32x4 *)&prm[(2 * t + 5) * TILE + 16 * g + 4 * h];
+                }
                 if (partial) {
                     // what lies at a key that the row does not see may be anything, NaN too
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        if (x[i / 4][i % 4] == -__builtin_inff()) vp[i / 4][i % 4] = 0;
+                        if (x[i / 4][i % 4] == -__builtin_inff()) vs[i / 4][i % 4] = vlo[i / 4][i % 4] = 0.0f;
                 }
 #pragma unroll
                 for (int i = 0; i < 8; i += 2) {
-                    const uint32_t w0 = vp[i / 4][i % 4], w1 = vp[i / 4][i % 4 + 1];
+                    const float s0 = vs[i / 4][i % 4], s1 = vs[i / 4][i % 4 + 1];
                     const float p0 = p[i / 4][i % 4], p1 = p[i / 4][i % 4 + 1];
-                    z[g] = __builtin_fmaf(p0, lo_of(w0), z[g]);
-                    z[g] = __builtin_fmaf(p1, lo_of(w1), z[g]);
-                    const f16x2 t = {(_Float16)__builtin_fmaf(p0, s_of(w0), 0.0f), (_Float16)__builtin_fmaf(p1, s_of(w1), 0.0f)};
-                    const f16x2 u = {(_Float16)__builtin_fmaf(p0, s_of(w0), -(float)t[0]),
-                                     (_Float16)__builtin_fmaf(p1, s_of(w1), -(float)t[1])};
+                    z[g] = __builtin_fmaf(p0, vlo[i / 4][i % 4], z[g]);
+                    z[g] = __builtin_fmaf(p1, vlo[i / 4][i % 4 + 1], z[g]);
+                    const f32x2 a2 = {p0 * s0, p1 * s1};
+                    const f16x2 t = __builtin_convertvector(a2, f16x2);
+                    const f32x2 b2 = {a2[0] - (float)t[0], a2[1] - (float)t[1]};
                     hi[i / 2] = __builtin_bit_cast(uint32_t, t);
-                    lo[i / 2] = __builtin_bit_cast(uint32_t, u);
+                    lo[i / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(b2, f16x2));
                 }
 // by pairs of tiles: the two terms of one would wait for each other
 #pragma unroll
