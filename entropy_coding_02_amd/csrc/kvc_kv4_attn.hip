@@ -2,13 +2,15 @@
 //
 // A cached value is y = lo + s n, n = 0..15.  A code within the mantissa of an
 // fp16 whose exponent is zero is the subnormal n 2^-24 (or, four bits up,
-// n 2^-20), exactly, and the matrix instructions take subnormals as they are:
-// one mask turns two codes into two matrix operands, and (s, lo) never touch
-// them:
+// n 2^-20), exactly, and a packed multiplication makes it n 2^-9, two codes at
+// a time; (s, lo) never touch the matrix operands:
 //   logits   q.k = sum_g s_g (sum_{c in g} q_c n_c) + lo_g (sum_{c in g} q_c);
 //            a query row is scaled by a power of two to just under 2^15 (an
 //            fp16 then holds every bit of it that fp32 sums would), so the
 //            products are exact;
+// (The matrix instructions take the subnormals too, but align a sum's products
+// by exponent, and a subnormal's leading bits lie up to ten places below its:
+// outputs that average many keys then lost twice their last fp16 bit.)
 //   output   o_c = sum_j (p_j s_jg) n_jc + sum_j p_j lo_jg,  c in group g.
 // p_j s_jg enters the matrix product as two fp16 terms (22 bits): one would
 // be an error of the output's own size, since n s is up to twice the value it
@@ -50,14 +52,14 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c)
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// Nibble i of both halves of w as a pair of subnormals, n 2^-24 for an even i
-// and n 2^-20 for an odd one.
+// Nibble i of both halves of w as a pair of n 2^-9.
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int i)
 {
-    return (i < 2 ? w : w >> 8) & (i & 1 ? 0x00F000F0u : 0x000F000Fu);
+    const uint32_t b = (i < 2 ? w : w >> 8) & (i & 1 ? 0x00F000F0u : 0x000F000Fu);
+    const _Float16 f = i & 1 ? (_Float16)0x1p11f : (_Float16)0x1p15f;
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, b) * f16x2{f, f});
 }
-// A K dword (8 channels of a key) as 8 operands in the order 0,4,1,5,2,6,3,7,
-// of which the odd pairs count 16 times (q has 1/16 of itself there).
+// A K dword (8 channels of a key) as 8 operands in the order 0,4,1,5,2,6,3,7.
 __device__ __forceinline__ u32x4 code_octet(uint32_t w)
 {
     return u32x4{code_pair(w, 0), code_pair(w, 1), code_pair(w, 2), code_pair(w, 3)};
@@ -308,15 +310,15 @@ __device__ __forceinline__ float scale_query(const Kv4Attn &a, const u32x4 *q, f
     // 2^(14 - e) for a largest of 2^e; a row of zeros, or one with Inf or NaN, stays as it is
     const int e = big > 0.0f && big < __builtin_inff() ? max((int)(__builtin_bit_cast(uint32_t, big) >> 23) - 127, -100) : 14;
     // A scale of 0 is one too small to tell (0 times the -inf of a masked key
-    // would be NaN).  2^24 is the codes' unit.
+    // would be NaN).  2^9 undoes the codes' unit.
     up = fmaxf(__builtin_fabsf(a.scale), 1.0e-30f) * (a.softcap > 0.0f ? 1.0f : kLog2e);
-    up = fmaxf(up * __builtin_bit_cast(float, (uint32_t)(127 + min(24 - 14 + e, 127)) << 23), 1.0e-37f);
+    up = fmaxf(up * __builtin_bit_cast(float, (uint32_t)(127 + min(9 - 14 + e, 127)) << 23), 1.0e-37f);
     // a negative scale becomes a positive one of -q, so that the largest logit is found before scaling
     const float f = __builtin_bit_cast(float, (uint32_t)(127 + 14 - e) << 23);
     return a.scale < 0.0f ? -f : f;
 }
 
-// Eight channels of q, scaled, in the order and weight of code_octet.
+// Eight channels of q, scaled, in the order of code_octet.
 template <bool BF>
 __device__ __forceinline__ u32x4 query_operand(u32x4 w, float f)
 {
@@ -326,8 +328,7 @@ __device__ __forceinline__ u32x4 query_operand(u32x4 w, float f)
         const uint32_t b = w[k / 2] >> (16 * (k & 1)) & 0xFFFFu;
         y[k] = (BF ? __builtin_bit_cast(float, b << 16) : kvc_h2f(b)) * f;
     }
-    return u32x4{f16_pair(y[0], y[4]), f16_pair(y[1] * 0.0625f, y[5] * 0.0625f), f16_pair(y[2], y[6]),
-                 f16_pair(y[3] * 0.0625f, y[7] * 0.0625f)};
+    return u32x4{f16_pair(y[0], y[4]), f16_pair(y[1], y[5]), f16_pair(y[2], y[6]), f16_pair(y[3], y[7])};
 }
 
 // log2 of a power of two above s, less 7; of 2^-24 where all s are 0
@@ -413,13 +414,13 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
         // the group sums of q, in the codes' unit
         float qs[NG];
         {
-            const u32x4 ones = {0x3C003C00u, 0x4C004C00u, 0x3C003C00u, 0x4C004C00u};  // 1, 16
+            const u32x4 ones = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};  // 1
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 f32x4 c = {0, 0, 0, 0};
 #pragma unroll
                 for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) c = mfma(ones, lds_q[s][lane], c);
-                qs[g] = c[0] * 0x1p-24f;
+                qs[g] = c[0] * 0x1p-9f;
             }
         }
         uint32_t s_top = 0;  // every s so far is at most this, by its bits
@@ -571,7 +572,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
     for (int c = 0; c < NT; ++c) {
         f32x4 y;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(c & 1 ? 0x1p20f : 0x1p24f, o[c][i], z[16 * c / G]);
+        for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(512.0f, o[c][i], z[16 * c / G]);
         *(f32x4 *)&lds_o[wave][col][16 * c + 4 * h] = y;
     }
     if (h == 0) {
@@ -664,13 +665,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
         const float sign = scale_query<D, BF>(a, q[ct], up[ct]);
 #pragma unroll
         for (int s = 0; s < NW; ++s) q[ct][s] = query_operand<BF>(q[ct][s], sign);
-        const u32x4 ones = {0x3C003C00u, 0x4C004C00u, 0x3C003C00u, 0x4C004C00u};
+        const u32x4 ones = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};  // 1
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             f32x4 c = {0, 0, 0, 0};
 #pragma unroll
             for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) c = mfma(ones, q[ct][s], c);
-            qs[ct][g] = c[0] * 0x1p-24f;
+            qs[ct][g] = c[0] * 0x1p-9f;
         }
     }
     // keys that some row of the wave sees, and that every row does
@@ -878,7 +879,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
             f32x4 y;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                y[i] = __builtin_fmaf(c & 1 ? 0x1p20f : 0x1p24f, o[ct][c][i], z[ct][16 * c / G]) * inv;
+                y[i] = __builtin_fmaf(512.0f, o[ct][c][i], z[ct][16 * c / G]) * inv;
             if (a.ns > 1)
                 *(f32x4 *)(a.part_o + prow * D + 16 * c + 4 * h) = y;
             else

@@ -667,3 +667,34 @@ def test_every_scale_has_its_reciprocal():
     assert len(np.unique(sq)) > 0.99 * len(s)
     for y in got:
         assert np.array_equal(y.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_average_of_many_keys_keeps_its_last_bit(wide):
+    """20000 keys, fp16: out is a small average of large terms (lo and s n cancel).  Its relative rms error is that
+    of one rounding, at most half a step, 2^-11, uniform: 2^-11 / sqrt(3), with a tenth more for all before it."""
+    import torch
+    H, D, G, P, R, T = 2, 128, 64, 64, 8, 20000
+    n = -(-T // P)
+    cache, ref = kvc.Kv4Cache(H, D, n, page_tokens=P, group=G), kv4_ref.Pool(H, D, G, P, n)
+    k, v = draw((T, H, D), "f16", 101), torch.randn((T, H, D), generator=torch.Generator().manual_seed(102)).half()
+    slots = np.arange(T)
+    kvc.kv4_append(cache, k.cuda(), v.cuda(), torch.from_numpy(slots).cuda())
+    ref.write(f32(k), f32(v), slots)
+    nq = 32 if wide else 1
+    q = draw((nq, H * R, D), "f16", 103, 0.5)
+    table = np.arange(n, dtype=np.int32)[None]
+    tab = widen(table, 1 << 19, P) if wide else table
+    out, lse = kvc.kv4_attention(cache, q.cuda(), torch.from_numpy(tab).cuda(), torch.tensor([T], dtype=torch.int32).cuda(),
+                                 return_lse=True)
+    assert status(cache) == 0
+    got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    off, of, ol = [], [], []
+    for h in range(H):
+        hs = slice(h * R, (h + 1) * R)
+        wo, wl = kv4_ref.attention(q[:, hs].double().numpy(), ref.value(0, slots)[:, h], ref.value(1, slots)[:, h],
+                                   T - nq + np.arange(nq), T, True, 0, 0.0, D ** -0.5)
+        off.append(got[:, hs] - wo), of.append(wo), ol.append((gl[:, hs] - wl) / wl)
+    rms = lambda x: float(np.sqrt(np.mean(np.square(x))))  # noqa: E731
+    assert rms(off) <= 1.1 * 2.0 ** -11 / math.sqrt(3) * rms(of)
+    assert rms(ol) < 1e-6
