@@ -331,6 +331,36 @@ __device__ __forceinline__ u32x4 query_operand(u32x4 w, float f)
     return u32x4{f16_pair(y[0], y[4]), f16_pair(y[1], y[5]), f16_pair(y[2], y[6]), f16_pair(y[3], y[7])};
 }
 
+// The term sum_g lo_g (sum_{c in g} q_c) of the logits as a matrix product of
+// its own, which the codes' products start from: two multiply-adds fewer a
+// logit.  A lane has key r's lo of group h (and h + 4) against that group's sum
+// of q in three fp16 terms (33 bits, no coarser than 2^-25 of its 2^13 at most).
+template <int NG>
+__device__ __forceinline__ u32x4 lo_operand(const uint32_t *params, int h)
+{
+    u32x4 a = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < (NG + 3) / 4; ++i) {
+        const uint32_t lo = params[i] >> 16;
+        if (h + 4 * i < NG) a[2 * i] = lo | lo << 16, a[2 * i + 1] = lo;
+    }
+    return a;
+}
+template <int NG>
+__device__ __forceinline__ u32x4 sum_operand(const float *qs, int h)
+{
+    u32x4 b = {0, 0, 0, 0};
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        const _Float16 t1 = (_Float16)qs[g];
+        const float r1 = qs[g] - (float)t1;
+        const _Float16 t2 = (_Float16)r1;
+        const float r2 = r1 - (float)t2;
+        if (h == g % 4) b[g / 4 * 2] = f16_pair(qs[g], r1), b[g / 4 * 2 + 1] = f16_pair(r2, 0.0f);
+    }
+    return b;
+}
+
 // log2 of a power of two above s, less 7; of 2^-24 where all s are 0
 __device__ __forceinline__ float exponent_above(float s)
 {
@@ -338,17 +368,15 @@ __device__ __forceinline__ float exponent_above(float s)
 }
 
 // c tanh(x up / c) = c - 2c / (exp(2 x up / c) + 1), in powers of 2
-__device__ __forceinline__ void cap_logits(float cap, float (&x)[2][4], float &up)
+__device__ __forceinline__ void cap_logits(float cap, f32x4 (&x)[2], float &up)
 {
     // or the compiler computes this for every call
 #pragma unroll
-    for (int i = 0; i < 8; ++i) __asm__ volatile("" : "+v"(x[i / 4][i % 4]));
+    for (int t = 0; t < 2; ++t) __asm__ volatile("" : "+v"(x[t]));
     const float in = up * 2.0f * kLog2e / cap, top = cap * kLog2e;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float &y = x[i / 4][i % 4];
-        y = top - 2.0f * top * __builtin_amdgcn_rcpf(exp2_fast(y * in) + 1.0f);
-    }
+    for (int i = 0; i < 8; ++i)
+        x[i / 4][i % 4] = top - 2.0f * top * __builtin_amdgcn_rcpf(exp2_fast(x[i / 4][i % 4] * in) + 1.0f);
     up = 1.0f;
 }
 
@@ -356,8 +384,8 @@ template <int D, int G, bool BF>
 __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2 : 3) : 4) void k_kv4_attn(Kv4Attn a)
 {
     constexpr int NW = D / 32, NG = D / G, NT = D / 16, NP = Stage<D, G>::NP, TILE = 64 * NP, NQ = (NW + kWaves - 1) / kWaves;
-    // Each wave's results; while it runs, its [K|V][tile][s|lo][group][16 keys]
-    // parameters, in fp32 (mixed-precision instructions run at half rate).
+    // Each wave's results; while it runs, its parameters, [tile] K's s, then
+    // [tile][s|lo] V's, each [group][16 keys], in fp32 (mixed-precision instructions run at half rate).
     __shared__ __align__(16) float lds_o[kWaves][16][D];
     __shared__ float lds_ml[kWaves][2][16];
     // The query operands, which as registers would cost a wave a SIMD.
@@ -367,7 +395,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, h = lane >> 4;  // this lane's query row, and its four keys of each tile
     float *const prm = &lds_o[wave][0][0];
-    static_assert(8 * TILE <= 16 * D, "the parameters fit where the results go");
+    static_assert(6 * TILE <= 16 * D, "the parameters fit where the results go");
     const int row = j.row0 + col, qi = row / a.R;
     const int b_end = min(j.u1 * 4, (j.kend + 31) / 32);
     int blk = j.u0 * 4 + wave;
@@ -423,6 +451,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
                 qs[g] = c[0] * 0x1p-9f;
             }
         }
+        const u32x4 sums = sum_operand<NG>(qs, h);
         uint32_t s_top = 0;  // every s so far is at most this, by its bits
         const int pos = j.pos0 + qi;
         const int k_hi = a.causal ? min(j.len, pos + 1) : j.len;  // keys k_lo <= key < k_hi
@@ -444,10 +473,9 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
-                    prm[(2 * t) * TILE + 64 * i + lane] = s_of(cur.kp[t][i]);
-                    prm[(2 * t + 1) * TILE + 64 * i + lane] = lo_of(cur.kp[t][i]);
-                    prm[(2 * t + 4) * TILE + 64 * i + lane] = s_of(cur.vp[t][i]);
-                    prm[(2 * t + 5) * TILE + 64 * i + lane] = lo_of(cur.vp[t][i]);
+                    prm[t * TILE + 64 * i + lane] = s_of(cur.kp[t][i]);
+                    prm[(2 * t + 2) * TILE + 64 * i + lane] = s_of(cur.vp[t][i]);
+                    prm[(2 * t + 3) * TILE + 64 * i + lane] = lo_of(cur.vp[t][i]);
                 }
             const int key0 = blk * 32;
             const bool partial = key0 + 32 > all_hi || key0 < all_lo;
@@ -461,7 +489,9 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
                     if (partial && (key0 + 16 * t + col < j.kbeg || key0 + 16 * t + col >= j.kend)) w = 0;
                     s_here = max(s_here, w);
                 }
-            float x[2][4];
+            f32x4 x[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) x[t] = mfma(lo_operand<NG>(cur.kp[t], h), sums, f32x4{0, 0, 0, 0});
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 f32x4 c[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
@@ -473,12 +503,9 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
                 }
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    const f32x4 ks = *(const f32x4 *)&prm[(2 * t) * TILE + 16 * g + 4 * h];
-                    const f32x4 klo = *(const f32x4 *)&prm[(2 * t + 1) * TILE + 16 * g + 4 * h];
+                    const f32x4 ks = *(const f32x4 *)&prm[t * TILE + 16 * g + 4 * h];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[t][i] = g == 0 ? __builtin_fmaf(klo[i], qs[g], ks[i] * c[t][i])
-                                         : __builtin_fmaf(klo[i], qs[g], __builtin_fmaf(ks[i], c[t][i], x[t][i]));
+                    for (int i = 0; i < 4; ++i) x[t][i] = __builtin_fmaf(ks[i], c[t][i], x[t][i]);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -521,8 +548,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
                 f32x4 vs[2], vlo[2];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    vs[t] = *(const f32x4 *)&prm[(2 * t + 4) * TILE + 16 * g + 4 * h];
-                    vlo[t] = *(const f32x4 *)&prm[(2 * t + 5) * TILE + 16 * g + 4 * h];
+                    vs[t] = *(const f32x4 *)&prm[(2 * t + 2) * TILE + 16 * g + 4 * h];
+                    vlo[t] = *(const f32x4 *)&prm[(2 * t + 3) * TILE + 16 * g + 4 * h];
                 }
                 if (partial) {
                     // what lies at a key that the row does not see may be anything, NaN too
@@ -635,7 +662,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
     constexpr int NK = 4 * NW * 64, NV = 2 * NT * 64;  // 16-byte operands of a turn
     struct Turn {
         u32x4 k[NK], v[NV];
-        float ks[4 * TILE], klo[4 * TILE];  // K's (s, lo), in fp32 once for all rows
+        u32x4 klo[4 * 64];                  // lo_operand of K
+        float ks[4 * TILE];                 // K's s, in fp32 once for all rows
         float vs[4 * TILE], vlo[4 * TILE];  // and V's
     };
     extern __shared__ __align__(16) uint8_t lds_raw[];
@@ -652,7 +680,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
     // the wave's rows: two column tiles of 16
     const int row_w = j.row0 + 32 * wave;
     u32x4 q[2][NW];
-    float up[2], qs[2][NG];
+    u32x4 sums[2];
+    float up[2];
     int k_lo[2], k_hi[2];
 #pragma unroll
     for (int ct = 0; ct < 2; ++ct) {
@@ -666,13 +695,15 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
 #pragma unroll
         for (int s = 0; s < NW; ++s) q[ct][s] = query_operand<BF>(q[ct][s], sign);
         const u32x4 ones = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};  // 1
+        float qs[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             f32x4 c = {0, 0, 0, 0};
 #pragma unroll
             for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) c = mfma(ones, q[ct][s], c);
-            qs[ct][g] = c[0] * 0x1p-9f;
+            qs[g] = c[0] * 0x1p-9f;
         }
+        sums[ct] = sum_operand<NG>(qs, h);
     }
     // keys that some row of the wave sees, and that every row does
     const int last = min(row_w + 32, j.rows) - 1;
@@ -729,10 +760,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             to.ks[wave * TILE + 64 * i + lane] = in ? s_of(kp[i]) : 0.0f;
-            to.klo[wave * TILE + 64 * i + lane] = in ? lo_of(kp[i]) : 0.0f;
+            kp[i] = in ? kp[i] : 0;
             to.vs[wave * TILE + 64 * i + lane] = in ? s_of(vp[i]) : 0.0f;
             to.vlo[wave * TILE + 64 * i + lane] = in ? lo_of(vp[i]) : 0.0f;
         }
+        to.klo[wave * 64 + lane] = lo_operand<NG>(kp, h);
     };
     if (turn < t_end) {
         look_up(turn);
@@ -753,9 +785,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
             for (int half = 0; half < 2; ++half) {
                 const int key0 = turn * kKeys + 32 * half;
                 const bool partial = key0 + 32 > all_hi || key0 < all_lo;
-                float x[2][2][4];
+                f32x4 x[2][2];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
+                    const u32x4 klo = now.klo[(2 * half + t) * 64 + lane];
+#pragma unroll
+                    for (int ct = 0; ct < 2; ++ct) x[ct][t] = mfma(klo, sums[ct], f32x4{0, 0, 0, 0});
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
                         f32x4 c[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
@@ -766,13 +801,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
                             c[1] = mfma(k, q[1][s], c[1]);
                         }
                         const f32x4 ks = *(const f32x4 *)&now.ks[(2 * half + t) * TILE + 16 * g + 4 * h];
-                        const f32x4 klo = *(const f32x4 *)&now.klo[(2 * half + t) * TILE + 16 * g + 4 * h];
 #pragma unroll
                         for (int ct = 0; ct < 2; ++ct)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                x[ct][t][i] = g == 0 ? __builtin_fmaf(klo[i], qs[ct][g], ks[i] * c[ct][i])
-                                                     : __builtin_fmaf(klo[i], qs[ct][g], __builtin_fmaf(ks[i], c[ct][i], x[ct][t][i]));
+                                x[ct][t][i] = __builtin_fmaf(ks[i], c[ct][i], x[ct][t][i]);
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);
@@ -941,7 +974,7 @@ hipError_t attend(const Kv4Attn &a, hipStream_t s)
     const int64_t blocks = (int64_t)a.ns * a.pool.H * a.B * a.tiles;
     hipError_t e;
     if (a.prompt) {
-        constexpr int lds = 2 * (4 * (D / 32) * 1024 + 2 * (D / 16) * 1024 + 4 * 4 * 64 * Stage<D, G>::NP * 4);
+        constexpr int lds = 2 * (4 * (D / 32) * 1024 + 2 * (D / 16) * 1024 + 4 * 1024 + 3 * 4 * 64 * Stage<D, G>::NP * 4);
         // above 64 KB LDS has to be asked for; the attribute is per device, and cheap
         if (lds > 65536) {
             e = hipFuncSetAttribute((const void *)k_kv4_prompt<D, G, BF>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
