@@ -1009,21 +1009,21 @@ hipError_t attend_dt(const Kv4Attn &a, bool bf16, hipStream_t s)
 // Blocks of 128 rows unpack a key once for all of them, but are few and long:
 // they are taken where every sequence may fill one, the keys are 2048 or more
 // and blocks and thousands of keys together occupy the chip (8 kv heads of
-// 128, R = 4, us a call, this kernel against tiles of 16 rows: 2048 queries
-// over 8192 keys 415 : 576, 2 x 512 over 4096 169 : 174, 8 x 32 over 4096
-// 45 : 51, 128 over 16000 82 : 108; not for 1 x 64 over 4096 32 : 25, 1024
-// over 1024 49 : 40, nor D = 256 with G = 32, whose 512 registers do not
-// hold it, 310 : 242).  Split: two blocks a compute unit (2 x 512 over 4096
-// 169, unsplit 220, in four 181), 512 keys or more each.
+// 128, R = 4, us a call with its join, this kernel : tiles of 16 rows: 2048
+// queries over 8192 keys 406 : 638, 2 x 512 over 4096 160 : 195, 8 x 32 over
+// 4096 46 : 54, 128 over 16000 89 : 116, 512 over 4096 with 4 heads of 256
+// 136 : 200, in groups of 32 231 : 246; not for 1 x 64 over 4096 38 : 27, nor
+// 1024 over 1024 50 : 42).  Split: two blocks a compute unit (2 x 512 over 4096
+// 160, unsplit 219, in four 175), 512 keys or more each.
 //
 // Tiles of 16 rows: a split costs a block's start and its part of the join, so
-// 512 keys or fewer are not split (1 x 300 keys 9.1 us, in two 10.4), else it
+// 512 keys or fewer are not split (1 x 300 keys 9.7 us, in two 11.0), else it
 // gets at least 256 keys while the blocks are fewer than the compute units,
 // 512 up to two blocks a unit (D = 256: a unit holds one), 1024 beyond, up to
 // eight a unit, which even out unequal sequences (us a call, this rule against
-// its neighbours: 1 x 4000 keys 11.4, at least 512: 14.4, 1024: 19.0; 1 x 16000
-// 15.4, 256: 18.5, 1024: 19.5; 64 x up to 8192 100, 1024 blocks 114, 4096 108;
-// 64 x up to 1000 21, split in two 27.5).
+// its neighbours: 1 x 4000 keys 11.7, in 8 14.8, in 64 14.3; 1 x 16000 15.4, in
+// 16 19.5, in 64 16.8; 64 x up to 8192 102, unsplit 110, in 8 112; 64 x up to
+// 1000 21, in two 28).
 namespace {
 
 int64_t prompt_splits(const Kv4Pool &p, int64_t blocks, int64_t keys)
@@ -1051,7 +1051,7 @@ Kv4Plan kv4_plan(const Kv4Pool &p, int64_t n_seqs, int R, int64_t max_q, int64_t
     const int64_t wide_tiles = (max_q * R + kRows - 1) / kRows, tiles = (max_q * R + 15) / 16;
     const int64_t wide = std::max<int64_t>(n_seqs * p.H * wide_tiles, 1), narrow = std::max<int64_t>(n_seqs * p.H * tiles, 1);
     const int64_t keys = keys_of(kRows);
-    plan.prompt = max_q * R >= kRows && (p.D < 256 || p.G >= 64) && keys >= 2048 && wide * ((keys + 1023) / 1024) >= 256;
+    plan.prompt = max_q * R >= kRows && keys >= 2048 && wide * ((keys + 1023) / 1024) >= 256;
     plan.tiles = (int32_t)(plan.prompt ? wide_tiles : tiles);
     plan.ns = (int32_t)(plan.prompt ? prompt_splits(p, wide, keys) : narrow_splits(p, narrow, keys_of(16)));
     // either kernel's splits grow with the keys, so no window takes more than these

@@ -698,3 +698,20 @@ def test_average_of_many_keys_keeps_its_last_bit(wide):
     rms = lambda x: float(np.sqrt(np.mean(np.square(x))))  # noqa: E731
     assert rms(off) <= 1.1 * 2.0 ** -11 / math.sqrt(3) * rms(of)
     assert rms(ol) < 1e-6
+
+
+def test_example_runs_them_together():
+    import os
+    import sys
+    import torch
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    sys.path.insert(0, os.path.join(root, "examples"))
+    try:
+        import resident_cache
+    finally:
+        sys.path.pop(0)
+    r = resident_cache.main(n_tokens=300, n_steps=70)  # the steps pass the end of a page
+    assert r["status"] == 0 and torch.isfinite(r["out"]).all() and r["out"].abs().sum() > 0
+    # 4 bits a channel, 16 levels over a group's range: half a step of 1/15 of it, uniform, against the rms of what
+    # lies in it (at least an eighth of its range for 64 values of any smooth density)
+    assert r["rms_error"] <= 8 / 15 / math.sqrt(12)
