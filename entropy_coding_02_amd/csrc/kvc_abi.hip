@@ -107,13 +107,15 @@ bool make_rows(Kv4Rows &r, const void *src, void *dst, int64_t ts, int64_t hs, i
     return true;
 }
 
-// Sizes an attention call may have: tiles and positions are counted in 32 bits.
+// Sizes an attention call may have: rows and positions are counted in 32 bits,
+// and a launch holds fewer than 2^32 threads (2^24 blocks of 256).
 bool kv4_attn_sizes(const Kv4Pool &p, int64_t n_q, int64_t n_seqs, int64_t n_q_heads, int64_t max_pages, int64_t max_q)
 {
-    return n_q >= 0 && n_q <= INT32_MAX && n_seqs >= 0 && max_q >= 0 && max_pages >= 0 && n_q_heads >= p.H &&
-           n_q_heads % p.H == 0 && (max_pages << p.pshift) <= ((int64_t)1 << 30) &&
-           max_q * (n_q_heads / p.H) <= ((int64_t)1 << 30) && n_q * n_q_heads <= ((int64_t)1 << 32) &&
-           n_seqs * p.H * ((max_q * (n_q_heads / p.H) + 15) / 16) < ((int64_t)1 << 30);
+    if (n_q < 0 || n_q > INT32_MAX || n_seqs < 0 || max_q < 0 || max_pages < 0 || n_q_heads < p.H || n_q_heads % p.H != 0)
+        return false;
+    const int64_t most = (int64_t)1 << 30, rows = max_q * (n_q_heads / p.H);
+    return (max_pages << p.pshift) <= most && rows <= most && n_q * n_q_heads <= most && n_seqs * p.H < (1 << 24) &&
+           n_seqs * p.H * ((rows + 15) / 16) < (1 << 24);
 }
 
 // The tensor as the CDF producers see it: its tables as chunks of S * Tc

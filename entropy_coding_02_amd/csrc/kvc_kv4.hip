@@ -399,12 +399,12 @@ Kv4Rows rows_from(Kv4Rows r, int64_t t, int dt)
     return r;
 }
 
-// A launch counts its items (at most n/4 * H * D/2) in 32 bits; more tokens
-// than that take several.
+// A launch holds fewer than 2^32 threads, n/4 * H * D/2 for K and as many for V;
+// more tokens than that take several.
 hipError_t move_any(bool append, const Kv4Pool &p, const Kv4Rows &k, const Kv4Rows &v, int64_t n, int dt,
                     const int64_t *slots, hipStream_t s)
 {
-    const int64_t most = ((int64_t)1 << 31) / ((int64_t)p.H * (p.D / 2)) * 4;
+    const int64_t most = ((int64_t)1 << 30) / ((int64_t)p.H * (p.D / 2)) * 4;
     for (int64_t t = 0; t < n; t += most) {
         const hipError_t e = move_piece(append, p, rows_from(k, t, dt), rows_from(v, t, dt),
                                         n - t < most ? n - t : most, dt, slots + t, s);

@@ -185,9 +185,10 @@ __device__ __forceinline__ bool make_job(const Kv4Attn &a, Job &j)
         j.kbeg = j.kend = j.u0 = j.u1 = 0;
         return true;
     }
-    const int f = j.kbeg / 128, n = (j.kend + 127) / 128 - f;
-    j.u0 = f + (int)((int64_t)n * j.split / a.ns);
-    j.u1 = f + (int)((int64_t)n * (j.split + 1) / a.ns);
+    // at most 2^23 units (2^30 keys) times 128 splits
+    const uint32_t f = (uint32_t)j.kbeg / 128, n = (uint32_t)(j.kend + 127) / 128 - f, ns = (uint32_t)a.ns;
+    j.u0 = (int)(f + n * (uint32_t)j.split / ns);
+    j.u1 = (int)(f + n * ((uint32_t)j.split + 1) / ns);
     return true;
 }
 

@@ -715,3 +715,39 @@ def test_example_runs_them_together():
     # 4 bits a channel, 16 levels over a group's range: half a step of 1/15 of it, uniform, against the rms of what
     # lies in it (at least an eighth of its range for 64 values of any smooth density)
     assert r["rms_error"] <= 8 / 15 / math.sqrt(12)
+
+
+def test_wide_blocks_in_a_graph():
+    """A prompt piece captured, replayed with other queries and lengths, each replay against the eager call."""
+    import torch
+    lens, nq, R, P = [260, 90], 64, 4, 16
+    cache, ref, table, slots = build(2, 128, 64, P, lens, "bf16", 35)
+    tab = torch.from_numpy(widen(table, 65536, P)).cuda()
+    q = draw((2 * nq, 2 * R, 128), "bf16", 111).cuda()
+    length = torch.tensor(lens, dtype=torch.int32).cuda()
+    work = torch.empty(kvc.kv4_work_bytes(cache, 2 * nq, 2 * R, 2, tab.shape[1], nq), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], dtype=torch.float32, device="cuda")
+
+    def step():
+        kvc.kv4_attention(cache, q, tab, length, out=out, lse=lse, work=work)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i in range(3):
+        q.copy_(draw(tuple(q.shape), "bf16", 112 + i))
+        length.copy_(torch.tensor([l - 13 * i for l in lens], dtype=torch.int32))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        again, lse2 = kvc.kv4_attention(cache, q, tab, length, return_lse=True)
+        assert torch.equal(again, out) and torch.equal(lse2, lse)
+        now = [l - 13 * i for l in lens]
+        compare(out, lse, q.cpu(), ref, [s[:n] for s, n in zip(slots, now)], now, [nq] * 2, R, "bf16", True, 0, 0.0, 128 ** -0.5)
+    assert status(cache) == 0

@@ -165,3 +165,13 @@ def test_workspace_covers_every_window(D, G):
             a = attn(cu_q=None, n_q=B * max_q, n_seqs=B, n_q_heads=H * R, max_pages=pages, max_q=max_q, window=window,
                      work=OK if need else None, work_bytes=need)
             assert lib.kvc_kv4_attention(d, ctypes.byref(a), OK, OK, None, None) == kvc.KVC_ERR_HIP
+
+
+def test_launch_limits():
+    """Sizes whose launches would pass 2^24 blocks are refused, the largest products without overflow."""
+    d, lib = desc(H=1024, D=64, G=64, n=10), kvc.lib()
+    big = (1 << 31) - 1
+    for n_q, n_seqs, heads, pages, max_q in ((big, big, 1024 * 2000000, big, big), (1 << 20, 1 << 14, 1024, 4, 64),
+                                            (1, 1, 1024, 4, 1 << 18), (1 << 21, 1, 1024, 4, 1)):
+        assert lib.kvc_kv4_work_bytes(d, n_q, n_seqs, heads, pages, max_q) == kvc.KVC_ERR_ARG
+    assert lib.kvc_kv4_work_bytes(d, 1 << 13, 1 << 13, 1024, 4, 1) == 0
