@@ -991,7 +991,7 @@ hipError_t attend(const Kv4Attn &a, hipStream_t s)
         if (a.ns <= 8)
             k_kv4_join<D, BF, 64><<<rows, dim3(64), 0, s>>>(a);
         else
-            k_kv4_join<D, BF, 512><<<rows, dim3(512), 0, s>>>(a);  // 79 splits of 64 rows: 4.9 us, by 256 threads 6.5
+            k_kv4_join<D, BF, 512><<<rows, dim3(512), 0, s>>>(a);  // 64 splits of 64 rows: 4.2 us; 79, 4.9, by 256 threads 6.5
         e = hipGetLastError();
     }
     return e;
@@ -1024,7 +1024,9 @@ hipError_t attend_dt(const Kv4Attn &a, bool bf16, hipStream_t s)
 // eight a unit, which even out unequal sequences (us a call, this rule against
 // its neighbours: 1 x 4000 keys 11.7, in 8 14.8, in 64 14.3; 1 x 16000 15.4, in
 // 16 19.5, in 64 16.8; 64 x up to 8192 102, unsplit 110, in 8 112; 64 x up to
-// 1000 21, in two 28).
+// 1000 21, in two 28).  Fewer than four blocks a unit are rounded down to as
+// many on every unit where that takes no more than a quarter of them (1 x 80000
+// on 8 heads, 79 ways 36, 64 ways 32).
 namespace {
 
 int64_t prompt_splits(const Kv4Pool &p, int64_t blocks, int64_t keys)
@@ -1039,7 +1041,9 @@ int64_t narrow_splits(const Kv4Pool &p, int64_t blocks, int64_t keys)
     int64_t ns = 1;
     if (keys > 512)
         for (int i = 0; i < 3; ++i) ns = std::max(ns, std::min(level[i][0] / blocks, (keys + level[i][1] - 1) / level[i][1]));
-    return std::min<int64_t>(ns, 128);
+    ns = std::min<int64_t>(ns, 128);
+    const int64_t even = ns * blocks / 256 * 256 / blocks;
+    return ns * blocks < 1024 && even * 4 >= ns * 3 ? even : ns;
 }
 
 }  // namespace
