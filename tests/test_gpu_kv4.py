@@ -751,3 +751,13 @@ def test_wide_blocks_in_a_graph():
         now = [l - 13 * i for l in lens]
         compare(out, lse, q.cpu(), ref, [s[:n] for s, n in zip(slots, now)], now, [nq] * 2, R, "bf16", True, 0, 0.0, 128 ** -0.5)
     assert status(cache) == 0
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_wide_blocks_of_256_channels_in_fine_groups(dt):
+    lens, nqs = [333, 64, 0], [140, 64, 9]
+    say(f"[gpu] kv4 wide D=256 G=32 {dt}")
+    cache, ref, table, slots = build(2, 256, 32, 16, lens, dt, 36)
+    table = widen(table, 65536, 16)
+    check(cache, ref, table, slots, lens, nqs, 2, dt)
+    check(cache, ref, table, slots, lens, nqs, 2, dt, causal=False, softcap=15.0)
