@@ -654,13 +654,21 @@ constexpr int kKeys = 64;    // keys a turn
 // Each wave unpacks a tile of 16 of a turn's 64 keys into LDS, as the matrix
 // operands that all of them read (in the order in which lanes read them: 16
 // bytes a lane, no conflicts), while the codes of the next turn are on their
-// way.  The terms are those of k_kv4_attn; with bf16 outputs p s is one fp16
-// term: its 2^-12 is an eighth of the output's own rounding, doubled by n s.
+// way.  The terms are those of k_kv4_attn, with bf16 outputs too: one fp16 term of
+// p s is off by 2^-12 of s n, which in a group with an outlier channel is many
+// times its other channels' values (one channel in 32 offset by 30: outputs off
+// by 5e-3, where the rounding to bf16 is 1.7e-3).  The second term costs a fifth
+// (2048 queries over 8192 keys 494 us, with one term 412); it is the residual of
+// the exact product, by a mixed multiply-add (as a difference of fp32: 520).
 template <int D, int G, bool BF>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
 {
-    constexpr int NW = D / 32, NG = D / G, NT = D / 16, NP = Stage<D, G>::NP, TILE = 64 * NP, TERMS = BF ? 1 : 2;
+    constexpr int NW = D / 32, NG = D / G, NT = D / 16, NP = Stage<D, G>::NP, TILE = 64 * NP;
     constexpr int NK = 4 * NW * 64, NV = 2 * NT * 64;  // 16-byte operands of a turn
+    // Groups whose p s are held at once: one, or the registers spill (in groups
+    // of 32, 2 x 512 queries over 4096 keys 211 us, all at once 327); heads of 256 have the
+    // accumulators' half of the file for it (512 over 4096 152 us, one by one 196).
+    constexpr int GS = D == 256 ? NG : 1;
     struct Turn {
         u32x4 k[NK], v[NV];
         u32x4 klo[4 * 64];                  // lo_operand of K
@@ -842,17 +850,20 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
                         for (int c = 0; c < NT; ++c) o[ct][c] *= f;
                     }
                 }
-                u32x4 ps[2][NG][TERMS];
+                float p[2][8];
 #pragma unroll
-                for (int ct = 0; ct < 2; ++ct) {
-                    float p[8];
+                for (int ct = 0; ct < 2; ++ct)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        p[i] = exp2_fast(__builtin_fmaf(x[ct][i / 4][i % 4], mul[ct], -mu[ct]));
-                        l[ct] += p[i];
+                        p[ct][i] = exp2_fast(__builtin_fmaf(x[ct][i / 4][i % 4], mul[ct], -mu[ct]));
+                        l[ct] += p[ct][i];
                     }
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) {
+                for (int g0 = 0; g0 < NG; g0 += GS) {
+                    u32x4 hi[GS][2], lo[GS][2];
+#pragma unroll
+                    for (int j = 0; j < 2 * GS; ++j) {
+                        const int g = g0 + j % GS, ct = j / GS;
                         f32x4 vs[2], vlo[2];
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
@@ -868,27 +879,25 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
 #pragma unroll
                         for (int i = 0; i < 8; i += 2) {
                             const float s0 = vs[i / 4][i % 4], s1 = vs[i / 4][i % 4 + 1];
-                            z[ct][g] = __builtin_fmaf(p[i], vlo[i / 4][i % 4], z[ct][g]);
-                            z[ct][g] = __builtin_fmaf(p[i + 1], vlo[i / 4][i % 4 + 1], z[ct][g]);
-                            const f32x2 a2 = {p[i] * s0, p[i + 1] * s1};
+                            z[ct][g] = __builtin_fmaf(p[ct][i], vlo[i / 4][i % 4], z[ct][g]);
+                            z[ct][g] = __builtin_fmaf(p[ct][i + 1], vlo[i / 4][i % 4 + 1], z[ct][g]);
+                            const f32x2 a2 = {p[ct][i] * s0, p[ct][i + 1] * s1};
                             const f16x2 t = __builtin_convertvector(a2, f16x2);
-                            ps[ct][g][0][i / 2] = __builtin_bit_cast(uint32_t, t);
-                            if (TERMS == 2) {
-                                const f32x2 b2 = {a2[0] - (float)t[0], a2[1] - (float)t[1]};
-                                const f16x2 u = __builtin_convertvector(b2, f16x2);
-                                ps[ct][g][TERMS - 1][i / 2] = __builtin_bit_cast(uint32_t, u);
-                            }
+                            const f16x2 r = {(_Float16)__builtin_fmaf(p[ct][i], s0, -(float)t[0]),
+                                             (_Float16)__builtin_fmaf(p[ct][i + 1], s1, -(float)t[1])};
+                            hi[g - g0][ct][i / 2] = __builtin_bit_cast(uint32_t, t);
+                            lo[g - g0][ct][i / 2] = __builtin_bit_cast(uint32_t, r);
                         }
                     }
-                }
 #pragma unroll
-                for (int c = 0; c < NT; ++c) {
-                    if (c % 2 == 0) __builtin_amdgcn_sched_barrier(0);
-                    const u32x4 v = now.v[(half * NT + c) * 64 + lane];
-#pragma unroll
-                    for (int e = 0; e < TERMS; ++e) {
-                        o[0][c] = mfma(v, ps[0][16 * c / G][e], o[0][c]);
-                        o[1][c] = mfma(v, ps[1][16 * c / G][e], o[1][c]);
+                    for (int c = g0 * (G / 16); c < (g0 + GS) * (G / 16); ++c) {
+                        if (c % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+                        const u32x4 v = now.v[(half * NT + c) * 64 + lane];
+                        const int g = 16 * c / G - g0;
+                        o[0][c] = mfma(v, hi[g][0], o[0][c]);
+                        o[1][c] = mfma(v, hi[g][1], o[1][c]);
+                        o[0][c] = mfma(v, lo[g][0], o[0][c]);
+                        o[1][c] = mfma(v, lo[g][1], o[1][c]);
                     }
                 }
             }
@@ -969,12 +978,19 @@ __global__ __launch_bounds__(THREADS) void k_kv4_join(Kv4Attn a)
     if (a.lse && part == 0) a.lse[row] = lse_of(M, L);
 }
 
+// Heads of 256 in groups of 32 have no blocks of 128 rows: those spilled 226
+// registers a lane (512 queries over 4096 keys, 4 heads: 254 us, tiles of 16 rows
+// 248; 1024 over 8192, 8 heads: 1730 : 1338).
+constexpr bool has_prompt(int D, int G) { return D != 256 || G != 32; }
+
 template <int D, int G, bool BF>
 hipError_t attend(const Kv4Attn &a, hipStream_t s)
 {
     const int64_t blocks = (int64_t)a.ns * a.pool.H * a.B * a.tiles;
     hipError_t e;
-    if (a.prompt) {
+    if (!a.prompt) {
+        k_kv4_attn<D, G, BF><<<dim3((uint32_t)blocks), dim3(64 * kWaves), 0, s>>>(a);
+    } else if constexpr (has_prompt(D, G)) {
         constexpr int lds = 2 * (4 * (D / 32) * 1024 + 2 * (D / 16) * 1024 + 4 * 1024 + 3 * 4 * 64 * Stage<D, G>::NP * 4);
         // above 64 KB LDS has to be asked for; the attribute is per device, and cheap
         if (lds > 65536) {
@@ -982,8 +998,6 @@ hipError_t attend(const Kv4Attn &a, hipStream_t s)
             if (e != hipSuccess) return e;
         }
         k_kv4_prompt<D, G, BF><<<dim3((uint32_t)blocks), dim3(256), lds, s>>>(a);
-    } else {
-        k_kv4_attn<D, G, BF><<<dim3((uint32_t)blocks), dim3(64 * kWaves), 0, s>>>(a);
     }
     e = hipGetLastError();
     if (e == hipSuccess && a.ns > 1) {
@@ -1011,11 +1025,11 @@ hipError_t attend_dt(const Kv4Attn &a, bool bf16, hipStream_t s)
 // they are taken where every sequence may fill one, the keys are 2048 or more
 // and blocks and thousands of keys together occupy the chip (8 kv heads of
 // 128, R = 4, us a call with its join, this kernel : tiles of 16 rows: 2048
-// queries over 8192 keys 406 : 638, 2 x 512 over 4096 160 : 195, 8 x 32 over
-// 4096 46 : 54, 128 over 16000 89 : 116, 512 over 4096 with 4 heads of 256
-// 136 : 200, in groups of 32 231 : 246; not for 1 x 64 over 4096 38 : 27, nor
-// 1024 over 1024 50 : 42).  Split: two blocks a compute unit (2 x 512 over 4096
-// 160, unsplit 219, in four 175), 512 keys or more each.
+// queries over 8192 keys 494 : 640, 2 x 512 over 4096 154 : 188, 8 x 32 over
+// 4096 58 : 73, 128 over 16000 100 : 117, 512 over 4096 with 4 heads of 256
+// 152 : 203; not for 1 x 64 over 4096 38 : 27, nor 1024 over 1024 50 : 42).
+// Split: two blocks a compute unit (2 x up to 512 over up to 4096, fp16, 160,
+// unsplit 219, in four 175), 512 keys or more each.
 //
 // Tiles of 16 rows: a split costs a block's start and its part of the join, so
 // 512 keys or fewer are not split (1 x 300 keys 9.7 us, in two 11.0), else it
@@ -1056,7 +1070,7 @@ Kv4Plan kv4_plan(const Kv4Pool &p, int64_t n_seqs, int R, int64_t max_q, int64_t
     const int64_t wide_tiles = (max_q * R + kRows - 1) / kRows, tiles = (max_q * R + 15) / 16;
     const int64_t wide = std::max<int64_t>(n_seqs * p.H * wide_tiles, 1), narrow = std::max<int64_t>(n_seqs * p.H * tiles, 1);
     const int64_t keys = keys_of(kRows);
-    plan.prompt = max_q * R >= kRows && keys >= 2048 && wide * ((keys + 1023) / 1024) >= 256;
+    plan.prompt = has_prompt(p.D, p.G) && max_q * R >= kRows && keys >= 2048 && wide * ((keys + 1023) / 1024) >= 256;
     plan.tiles = (int32_t)(plan.prompt ? wide_tiles : tiles);
     plan.ns = (int32_t)(plan.prompt ? prompt_splits(p, wide, keys) : narrow_splits(p, narrow, keys_of(16)));
     // either kernel's splits grow with the keys, so no window takes more than these

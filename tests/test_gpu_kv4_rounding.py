@@ -1,0 +1,104 @@
+"""What the attention over the 4-bit cache loses beyond the one rounding of its
+output: inputs on which a step carried in too few bits shows.
+
+p s enters the matrix product as two fp16 terms, off by 2^-22 of itself, and is
+multiplied by codes up to 15, whatever the value lo + s n that they make up.
+"""
+import math
+
+import numpy as np
+import pytest
+
+import entropy_coding_02_amd as kvc
+import kv4_ref
+from gpu_util import say
+from test_gpu_kv4 import EPS, draw, f32, fresh, status, tdt, widen
+
+pytestmark = pytest.mark.gpu
+
+# heads, channels, groups, page
+SHAPES = [(2, 64, 32, 16), (1, 64, 64, 32), (2, 128, 32, 16), (2, 128, 64, 64), (1, 128, 128, 32), (1, 256, 64, 16),
+          (1, 256, 128, 16), (1, 256, 32, 16)]
+
+
+def hold(k, v, G, P, seed=0):
+    """One sequence's k, v [T][H][D] in shuffled pages: the pool, its reference, the table, the slots."""
+    import torch
+    T, H, D = k.shape
+    n = -(-T // P)
+    cache, ref = fresh(H, D, G, P, n)
+    table = np.random.default_rng(seed).permutation(n).astype(np.int32)[None]
+    t = np.arange(T)
+    slots = table[0, t // P].astype(np.int64) * P + t % P
+    kvc.kv4_append(cache, k.cuda(), v.cuda(), torch.from_numpy(slots).cuda())
+    ref.write(f32(k), f32(v), slots)
+    assert status(cache) == 0
+    return cache, ref, table, slots
+
+
+def attend(cache, table, q, T, wide, **call):
+    """wide: a table of room for many more keys, under which many query rows go by blocks of 128."""
+    import torch
+    tab = widen(table, 1 << 19, cache.page_tokens) if wide else table
+    out, lse = kvc.kv4_attention(cache, q.cuda(), torch.from_numpy(tab).cuda(), torch.tensor([T], dtype=torch.int32).cuda(),
+                                 return_lse=True, **call)
+    assert status(cache) == 0
+    return out.double().cpu().numpy(), lse.double().cpu().numpy()
+
+
+def exact(ref, slots, q, scale, causal=True, window=0, softcap=0.0):
+    n, Hq, _ = q.shape
+    R, T = Hq // ref.H, len(slots)
+    q64 = q.double().numpy()
+    parts = [kv4_ref.attention(q64[:, h * R:(h + 1) * R], ref.value(0, slots)[:, h], ref.value(1, slots)[:, h],
+                               T - n + np.arange(n), T, causal, window, softcap, scale) for h in range(ref.H)]
+    return np.concatenate([o for o, _ in parts], 1), np.concatenate([l for _, l in parts], 1)
+
+
+def rms(x):
+    return float(np.sqrt(np.mean(np.square(x))))
+
+
+@pytest.mark.parametrize("H,D,G,P", SHAPES)
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("wide", [False, True])
+def test_outlier_channels_leave_the_others_their_bits(H, D, G, P, dt, wide):
+    """V with one channel in 32 far off: s is that channel's, and the others' values are small differences of lo and
+    s n.  Their relative rms error is that of one rounding, at most half a step, uniform: eps / 2 / sqrt(3), with a
+    tenth more for all before it.  (One fp16 term of p s makes it 2^-12 / sqrt(3) of about 30 / 15 * 14 for values of
+    1: 4e-3 where bf16 has 2.3e-3 and fp16 2.8e-4.)"""
+    import torch
+    T, nq, R = 1500, 32, 4
+    say(f"[gpu] kv4 outlier channels H={H} D={D} G={G} {dt} wide={wide}")
+    k, v = draw((T, H, D), dt, 1, 0.3), torch.randn((T, H, D), generator=torch.Generator().manual_seed(2))
+    v[..., ::32] -= 30.0
+    cache, ref, table, slots = hold(k, v.to(tdt(dt)), G, P)
+    q = draw((nq, H * R, D), dt, 3, 0.3)
+    got, gl = attend(cache, table, q, T, wide)
+    wo, wl = exact(ref, slots, q, D ** -0.5)
+    others = np.arange(D) % 32 != 0
+    assert rms((got - wo)[..., others]) <= 1.1 * EPS[dt] / 2 / math.sqrt(3) * rms(wo[..., others])
+    assert np.abs(gl - wl).max() <= 2.0 ** -16 * np.abs(wl).max()
+
+
+@pytest.mark.parametrize("H,D,G,P", SHAPES)
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("wide", [False, True])
+def test_one_dominant_key(H, D, G, P, dt, wide):
+    """A key with 0.99 of the weight, 60 after one of 2^-7.2 of it (p goes by that one, and is no power of two): out is
+    about its value, and where that is next to 0 the error is a share of s.  Half a step of the output, 2^-22 of p s
+    times 15 and the fp32 steps of p s n and p lo, of at most 31 s and a dozen: 2^-18 s."""
+    import torch
+    T, nq, R = 1100, 32, 4
+    say(f"[gpu] kv4 dominant key H={H} D={D} G={G} {dt} wide={wide}")
+    c = torch.full((T,), -60.0)
+    c[640], c[700] = 0.0, 5.0
+    k = c.view(T, 1, 1).expand(T, H, D).contiguous().to(tdt(dt))  # the same in every channel: s = 0, lo = c
+    v = torch.randn((T, H, D), generator=torch.Generator().manual_seed(5)).to(tdt(dt))
+    cache, ref, table, slots = hold(k, v, G, P)
+    q = torch.ones((nq, H * R, D), dtype=tdt(dt))
+    got, gl = attend(cache, table, q, T, wide, scale=1.0 / D)
+    wo, wl = exact(ref, slots, q, 1.0 / D)
+    smax = np.repeat(ref.s[1, slots].astype(np.float64).max((0, 2)), R)[None, :, None]
+    assert (np.abs(got - wo) <= EPS[dt] / 2 * np.abs(wo) + 2.0 ** -18 * smax).all()
+    assert np.abs(gl - wl).max() <= 2.0 ** -20 * 5
