@@ -516,6 +516,18 @@ def _kv4_stream(stream, t):
     return _RAW_STREAM(t.get_device())
 
 
+def _kv4_empty(stream, like, shape, dtype):
+    """A tensor for the kernels of a call on `stream`, of that stream's memory: the current stream's could be in use
+    there still, or be given away before the kernels are done with it."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, like.device) if stream else torch.cuda.default_stream(like.device)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _rows(name: str, t, shape):
     """Pointer and strides of a device tensor [n][heads][D] whose channels are contiguous."""
     if t.shape != shape or t.dim() != 3:
@@ -551,15 +563,16 @@ def kv4_append(cache: Kv4Cache, k, v, slots, stream=None):
 
 def kv4_read(cache: Kv4Cache, slots, dtype=None, k=None, v=None, stream=None):
     """The values at slots int64 [T], as (k, v) [T][H][D] of `dtype` (float16
-    unless given) or written into k and v (one dtype, channels contiguous)."""
+    unless given) or written into k and v (one dtype, channels contiguous).
+    What is allocated here belongs to `stream` (the current one if not given)."""
     if slots.dim() != 1:
         raise ValueError("kvc: slots must be int64 [T]")
     n = slots.shape[0]
     if dtype is None:
         dtype = cache.params.dtype if k is None and v is None else (v if k is None else k).dtype
     shape = (n, cache.n_kv_heads, cache.head_dim)
-    k = slots.new_empty(shape, dtype=dtype) if k is None else k
-    v = slots.new_empty(shape, dtype=dtype) if v is None else v
+    k = _kv4_empty(stream, slots, shape, dtype) if k is None else k
+    v = _kv4_empty(stream, slots, shape, dtype) if v is None else v
     if k.dtype != dtype or v.dtype != dtype:
         raise ValueError("kvc: k and v must have one dtype")
     kp, kts, khs = _rows("k", k, shape)
@@ -587,7 +600,8 @@ def kv4_attention(cache: Kv4Cache, q, page_table, kv_len, cu_q=None, max_q: Opti
     [B][max_pages], kv_len int32 [B]; cu_q int32 [B + 1] bounds each
     sequence's queries (at most max_q; n_q if not given), without it every
     sequence has n_q / B.  `work`: uint8 of kv4_work_bytes, allocated if not
-    given.  Returns out, or (out, lse float32 [n_q][Hq])."""
+    given.  What is allocated here belongs to `stream` (the current one if not
+    given).  Returns out, or (out, lse float32 [n_q][Hq])."""
     if q.dim() != 3 or page_table.dim() != 2:
         raise ValueError("kvc: q must be [n_q][Hq][D], page_table [B][max_pages]")
     n_q, n_heads, _ = q.shape
@@ -605,7 +619,7 @@ def kv4_attention(cache: Kv4Cache, q, page_table, kv_len, cu_q=None, max_q: Opti
     elif max_q is None:
         max_q = n_q
     if out is None:
-        out = q.new_empty(shape)
+        out = _kv4_empty(stream, q, shape, dtype)
     elif out.dtype != dtype:
         raise ValueError("kvc: out must have q's dtype")
     if lse is not None:
@@ -613,10 +627,10 @@ def kv4_attention(cache: Kv4Cache, q, page_table, kv_len, cu_q=None, max_q: Opti
         if lse.dtype != cache.float32 or lse.shape != shape[:2]:
             raise ValueError("kvc: lse must be float32 [n_q][Hq]")
     elif return_lse:
-        lse = q.new_empty(shape[:2], dtype=cache.float32)
+        lse = _kv4_empty(stream, q, shape[:2], cache.float32)
     if work is None:
         nb = kv4_work_bytes(cache, n_q, n_heads, B, max_pages, max_q)
-        work = q.new_empty(nb, dtype=cache.codes.dtype) if nb else None
+        work = _kv4_empty(stream, q, (nb,), cache.codes.dtype) if nb else None
     qp, qts, qhs = _rows("q", q, shape)
     op, ots, ohs = _rows("out", out, shape)
     args = _ATTN.pack(

@@ -1,0 +1,104 @@
+"""The Python side of the 4-bit cache without a GPU: stand-ins for device tensors, a library that records its calls."""
+import contextlib
+import math
+import types
+
+import pytest
+import torch
+
+import entropy_coding_02_amd as kvc
+
+STREAMS = []  # what torch.cuda.stream has entered, innermost last
+
+
+class Fake:
+    """What the binding asks of a device tensor.  `home`: the stream that was current when it was made."""
+    made = 0
+
+    def __init__(self, shape, dtype, device=0, strides=None):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, torch.device("cuda", device)
+        if strides is None:
+            strides = [math.prod(shape[i + 1:]) for i in range(len(shape))]
+        self.strides, self.is_cuda = tuple(strides), True
+        Fake.made += 1
+        self.address = Fake.made << 32
+        self.home = STREAMS[-1] if STREAMS else None
+
+    def dim(self): return len(self.shape)
+    def numel(self): return self.shape.numel()
+    def element_size(self): return torch.empty(0, dtype=self.dtype).element_size()
+    def stride(self, i=None): return self.strides if i is None else self.strides[i]
+    def data_ptr(self): return self.address
+    def get_device(self): return self.device.index
+
+    def is_contiguous(self):
+        return self.strides == Fake(self.shape, self.dtype).strides
+
+    def new_empty(self, shape, dtype=None):
+        t = Fake(shape if isinstance(shape, (tuple, torch.Size)) else (shape,), dtype or self.dtype, self.device.index)
+        ALLOCATED.append(t)
+        return t
+
+
+ALLOCATED = []
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The launches of the library, as (name, arguments); sizes come from the library itself."""
+    real, made = kvc._load(), []
+
+    def record(name):
+        return lambda *a: made.append((name, a)) or kvc.KVC_OK
+
+    lib = types.SimpleNamespace(**{n: getattr(real, n) for n in kvc.EXPORTED})
+    for n in ("kvc_kv4_append", "kvc_kv4_read", "kvc_kv4_attention"):
+        setattr(lib, n, record(n))
+
+    @contextlib.contextmanager
+    def stream(s):
+        STREAMS.append(s)
+        yield
+        STREAMS.pop()
+
+    monkeypatch.setattr(kvc, "_load", lambda: lib)
+    monkeypatch.setattr(kvc, "_RAW_STREAM", lambda i: 77)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: types.SimpleNamespace(cuda_stream=h))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: types.SimpleNamespace(cuda_stream=0))
+    ALLOCATED.clear()
+    return made
+
+
+def pool(H=2, D=64, P=64, n=200, G=64, device=0):
+    return kvc.Kv4Cache(H, D, n, page_tokens=P, group=G,
+                        codes=Fake((n, 2, H, P * D // 2), torch.uint8, device),
+                        params=Fake((n, 2, H, D // G, P, 2), torch.float16, device),
+                        dev_status=Fake((1,), torch.int32, device))
+
+
+def attention(cache, **kw):
+    """One query over a table of 200 pages: split, so that a workspace is wanted."""
+    a = dict(q=Fake((1, 4, cache.head_dim), torch.float16), page_table=Fake((1, 200), torch.int32),
+             kv_len=Fake((1,), torch.int32))
+    a.update(kw)
+    return kvc.kv4_attention(cache, a.pop("q"), a.pop("page_table"), a.pop("kv_len"), **a)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_what_a_call_allocates_belongs_to_its_stream(calls, handle):
+    s = types.SimpleNamespace(cuda_stream=1234)
+    attention(pool(), return_lse=True, stream=1234 if handle else s)
+    kvc.kv4_read(pool(), Fake((5,), torch.int64), stream=1234 if handle else s)
+    assert len(ALLOCATED) == 5  # out, lse, workspace; k, v
+    assert all(t.home is not None and t.home.cuda_stream == 1234 for t in ALLOCATED)
+    assert all(a[-1] == 1234 for _, a in calls)
+
+
+def test_without_a_stream_the_current_one_is_used(calls):
+    attention(pool(), return_lse=True)
+    kvc.kv4_read(pool(), Fake((5,), torch.int64))
+    assert len(ALLOCATED) == 5 and all(t.home is None for t in ALLOCATED)
+    assert all(a[-1] == 77 for _, a in calls)
+    attention(pool(), stream=0)  # the default stream's handle
+    assert calls[-1][1][-1] == 0 and ALLOCATED[-1].home.cuda_stream == 0
