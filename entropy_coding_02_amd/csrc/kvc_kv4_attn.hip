@@ -368,16 +368,41 @@ __device__ __forceinline__ float exponent_above(float s)
     return s > 0.0f ? (float)((int)(__builtin_bit_cast(uint32_t, s) >> 23) - 126 - 7) : -31.0f;
 }
 
-// c tanh(x up / c) = c - 2c / (exp(2 x up / c) + 1), in powers of 2
+// c tanh(u), u = x up / c, in powers of 2.  Its error has to be a share of the
+// logit, whatever the cap: up to 5/8, u Q(u^2) with Q the minimax polynomial of
+// tanh(u)/u there that is 1 at 0 (2^-27.8; fitted by weighted least squares), so
+// that a cap far above the logits leaves them as they are; beyond,
+// 1 - 2 / (exp(2u) + 1), which for small u would be a difference of near equals.
+// Logits past 5/8 of their cap are few, and the branch is a wave's.
 __device__ __forceinline__ void cap_logits(float cap, f32x4 (&x)[2], float &up)
 {
     // or the compiler computes this for every call
 #pragma unroll
     for (int t = 0; t < 2; ++t) __asm__ volatile("" : "+v"(x[t]));
-    const float in = up * 2.0f * kLog2e / cap, top = cap * kLog2e;
+    constexpr float kNear = 0.625f;
+    const float in = fminf(up / cap, 1.0e30f), unit = up * kLog2e;  // 0 times infinity would be NaN
+    float u[8], far = 0.0f;
+    f32x4 y[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        x[i / 4][i % 4] = top - 2.0f * top * __builtin_amdgcn_rcpf(exp2_fast(x[i / 4][i % 4] * in) + 1.0f);
+    for (int i = 0; i < 8; ++i) {
+        u[i] = x[i / 4][i % 4] * in;
+        const float w = u[i] * u[i];
+        float q = __builtin_fmaf(w, -0.00570498686f, 0.020639088f);
+        q = __builtin_fmaf(w, q, -0.0537397154f);
+        q = __builtin_fmaf(w, q, 0.133314416f);
+        q = __builtin_fmaf(w, q, -0.333332807f);
+        y[i / 4][i % 4] = x[i / 4][i % 4] * unit * __builtin_fmaf(w, q, 1.0f);
+        far = fmaxf(far, __builtin_fabsf(u[i]));
+    }
+    if (__any(far > kNear)) {
+        const float top = fminf(cap * kLog2e, 3.0e38f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float r = __builtin_amdgcn_rcpf(exp2_fast(u[i] * (2.0f * kLog2e)) + 1.0f);
+            if (__builtin_fabsf(u[i]) > kNear) y[i / 4][i % 4] = top * __builtin_fmaf(-2.0f, r, 1.0f);
+        }
+    }
+    x[0] = y[0], x[1] = y[1];
     up = 1.0f;
 }
 

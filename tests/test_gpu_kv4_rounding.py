@@ -102,3 +102,27 @@ def test_one_dominant_key(H, D, G, P, dt, wide):
     smax = np.repeat(ref.s[1, slots].astype(np.float64).max((0, 2)), R)[None, :, None]
     assert (np.abs(got - wo) <= EPS[dt] / 2 * np.abs(wo) + 2.0 ** -18 * smax).all()
     assert np.abs(gl - wl).max() <= 2.0 ** -20 * 5
+
+
+@pytest.mark.parametrize("cap", [1e-30, 1e-3, 1.0, 5.0, 30.0, 1e3, 1e4, 1e5, 1e7, 1e15, 1e30, 2.9e38])
+@pytest.mark.parametrize("H,D,G,P", [(2, 64, 32, 16), (2, 128, 64, 16), (1, 256, 128, 16)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_soft_cap_of_any_size(cap, H, D, G, P, wide):
+    """A capped logit is off by a share of itself: 32 half steps of fp32 of the largest logit before the cap (its sums
+    over D channels and groups, the cap's ten operations, exp2's argument), and so is lse; out by twice that of the
+    largest value, beside its own rounding and the terms of p s."""
+    T, nq, R = 40, 32, 4
+    say(f"[gpu] kv4 softcap={cap} D={D} wide={wide}")
+    k, v = draw((T, H, D), "f16", 7, 0.5), draw((T, H, D), "f16", 8, 0.5)
+    k[..., :3] -= 3.0  # draw's offset, of which a logit would be nine times
+    cache, ref, table, slots = hold(k, v, G, P)
+    q = draw((nq, H * R, D), "f16", 9, 2.0)
+    for scale in (D ** -0.5, -2.0 * D ** -0.5):
+        got, gl = attend(cache, table, q, T, wide, softcap=cap, scale=scale)
+        wo, wl = exact(ref, slots, q, scale, softcap=cap)
+        k64 = ref.value(0, slots)
+        most = max(np.abs(q.double().numpy()[:, h * R:(h + 1) * R] @ k64[:, h].T).max() for h in range(H)) * abs(scale)
+        off = 32 * 2.0 ** -24 * most
+        assert np.abs(gl - wl).max() <= off + 2.0 ** -22 * np.abs(wl).max()
+        vmax, smax = np.abs(ref.value(1, slots)).max(), float(ref.s[1].max())
+        assert (np.abs(got - wo) <= EPS["f16"] / 2 * np.abs(wo) + 2 * off * vmax + 2.0 ** -18 * smax).all()
