@@ -15,10 +15,13 @@
 // p_j s_jg enters the matrix product as two fp16 terms (22 bits): one would
 // be an error of the output's own size, since n s is up to twice the value it
 // belongs to.  They keep those bits because p is taken relative not to the
-// row's maximum alone but also to a power of two above every s met so far: p s
-// is at most 2^7.  The maximum is let be until a logit passes it by 8 (in
-// powers of 2): the sums are rescaled a few times a row rather than at every
-// new maximum of any of a wave's rows, and p s stays below 2^15.
+// row's largest logit but to the largest p_j s_j, s_j the largest s of key j's
+// groups, of which the product is 2^7: neither a token far larger than the others
+// that the row hardly looks at, nor one far smaller that it looks at alone, takes
+// the others' bits.  (Within a token a group whose s is 2^-k of the largest
+// keeps 22 bits up to k = 10, and one fewer for each more.)  That maximum is let be
+// until a p s passes it by 2^8: the sums are rescaled a few times a row rather
+// than at every new maximum of any of a wave's rows, and p s stays below 2^15.
 //
 // Orientation: S^T = K q^T (16 keys x 16 query rows), so a lane holds one
 // query row and four keys of a tile, which is just what P^T needs as the
@@ -362,10 +365,39 @@ __device__ __forceinline__ u32x4 sum_operand(const float *qs, int h)
     return b;
 }
 
-// log2 of a power of two above s, less 7; of 2^-24 where all s are 0
-__device__ __forceinline__ float exponent_above(float s)
+// log2 of the largest s of a key's groups, of which this lane holds `s`, and the
+// lanes of the same key 16 apart the others; at least -24, the smallest s there
+// is (what lies at a key that no row sees may be anything: NaN becomes -24).
+template <int NG>
+__device__ __forceinline__ float log2_top(float s)
 {
-    return s > 0.0f ? (float)((int)(__builtin_bit_cast(uint32_t, s) >> 23) - 126 - 7) : -31.0f;
+    if (NG > 1) {
+        const uint32_t b = __builtin_bit_cast(uint32_t, s);
+        const auto x = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+        const uint32_t x0 = x[0], x1 = x[1];
+        s = fmaxf(__builtin_bit_cast(float, x0), __builtin_bit_cast(float, x1));
+    }
+    if (NG > 2) {
+        const uint32_t b = __builtin_bit_cast(uint32_t, s);
+        const auto x = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+        const uint32_t x0 = x[0], x1 = x[1];
+        s = fmaxf(__builtin_bit_cast(float, x0), __builtin_bit_cast(float, x1));
+    }
+    return fmaxf(__builtin_amdgcn_logf(s), -24.0f);
+}
+
+// Rows of which some p s passes the largest so far by 2^8 take the new one.
+// top: the largest x + log2 s of the row's new keys, by lane; ref: what p is
+// relative to (-inf: no key yet).  Returns what the sums are to be multiplied by.
+__device__ __forceinline__ float rescale(float top, float &pass, float &ref, float &mu)
+{
+    top = row_max(top);
+    const float to = top > pass ? top - 7.0f : ref;
+    const float f = ref == -__builtin_inff() ? 1.0f : exp2_fast(ref - to);
+    pass = top > pass ? top + 8.0f : pass;
+    ref = to;
+    mu = ref == -__builtin_inff() ? 0.0f : ref;
+    return f;
 }
 
 // c tanh(u), u = x up / c, in powers of 2.  Its error has to be a share of the
@@ -411,7 +443,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
 {
     constexpr int NW = D / 32, NG = D / G, NT = D / 16, NP = Stage<D, G>::NP, TILE = 64 * NP, NQ = (NW + kWaves - 1) / kWaves;
     // Each wave's results; while it runs, its parameters, [tile] K's s, then
-    // [tile][s|lo] V's, each [group][16 keys], in fp32 (mixed-precision instructions run at half rate).
+    // [tile][s|lo] V's, each [group][16 keys], in fp32 (mixed-precision instructions run at half
+    // rate), then [tile] log2 of each key's largest s of V.
     __shared__ __align__(16) float lds_o[kWaves][16][D];
     __shared__ float lds_ml[kWaves][2][16];
     // The query operands, which as registers would cost a wave a SIMD.
@@ -421,7 +454,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, h = lane >> 4;  // this lane's query row, and its four keys of each tile
     float *const prm = &lds_o[wave][0][0];
-    static_assert(6 * TILE <= 16 * D, "the parameters fit where the results go");
+    static_assert(6 * TILE + 32 <= 16 * D, "the parameters fit where the results go");
     const int row = j.row0 + col, qi = row / a.R;
     const int b_end = min(j.u1 * 4, (j.kend + 31) / 32);
     int blk = j.u0 * 4 + wave;
@@ -452,9 +485,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
     }
 
     f32x4 o[NT];
-    // In powers of 2: m, a logit that no later one passes by more than 8 (pass:
-    // that bound, in the unit of x), and ref, what p is relative to.
-    float z[NG], m = -__builtin_inff(), pass = -__builtin_inff(), ref = -__builtin_inff(), mu = 0.0f, l = 0.0f;
+    // In powers of 2: pass, the p s at which the sums are rescaled, and ref, what p is relative to.
+    float z[NG], pass = -__builtin_inff(), ref = -__builtin_inff(), mu = 0.0f, l = 0.0f;
 #pragma unroll
     for (int c = 0; c < NT; ++c) o[c] = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -478,7 +510,6 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
             }
         }
         const u32x4 sums = sum_operand<NG>(qs, h);
-        uint32_t s_top = 0;  // every s so far is at most this, by its bits
         const int pos = j.pos0 + qi;
         const int k_hi = a.causal ? min(j.len, pos + 1) : j.len;  // keys k_lo <= key < k_hi
         const int k_lo = a.window ? max(0, pos - a.window + 1) : 0;
@@ -503,18 +534,15 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
                     prm[(2 * t + 2) * TILE + 64 * i + lane] = s_of(cur.vp[t][i]);
                     prm[(2 * t + 3) * TILE + 64 * i + lane] = lo_of(cur.vp[t][i]);
                 }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                float s = s_of(cur.vp[t][0]);
+#pragma unroll
+                for (int i = 1; i < NP; ++i) s = fmaxf(s, s_of(cur.vp[t][i]));
+                prm[6 * TILE + 16 * t + col] = log2_top<NG>(s);
+            }
             const int key0 = blk * 32;
             const bool partial = key0 + 32 > all_hi || key0 < all_lo;
-            // the largest s of the block: of this lane's share of the parameters
-            uint32_t s_here = 0;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    uint32_t w = cur.vp[t][i] & 0xFFFFu;
-                    if (partial && (key0 + 16 * t + col < j.kbeg || key0 + 16 * t + col >= j.kend)) w = 0;
-                    s_here = max(s_here, w);
-                }
             f32x4 x[2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) x[t] = mfma(lo_operand<NG>(cur.kp[t], h), sums, f32x4{0, 0, 0, 0});
@@ -543,19 +571,15 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
                     const int key = key0 + 16 * (i / 4) + 4 * h + i % 4;
                     if (key < k_lo || key >= k_hi) x[i / 4][i % 4] = -__builtin_inff();
                 }
-            float mx = x[0][0];
+            float top = -__builtin_inff();
 #pragma unroll
-            for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[i / 4][i % 4]);
-            if (__any(mx > pass || s_here > s_top)) {
-                // the bound of s is the wave's: its rows share the keys
-                for (int off = 32; off; off >>= 1) s_here = max(s_here, (uint32_t)__shfl_xor((int)s_here, off, 64));
-                s_top = max(s_top, s_here);
-                mx = row_max(mx);
-                if (mx > pass) m = mx * mul, pass = (m + 8.0f) / mul;
-                const float to = m + exponent_above(kvc_h2f(s_top));
-                const float f = ref == -__builtin_inff() ? 1.0f : exp2_fast(ref - to);
-                ref = to;
-                mu = ref == -__builtin_inff() ? 0.0f : ref;
+            for (int t = 0; t < 2; ++t) {
+                const f32x4 ls = *(const f32x4 *)&prm[6 * TILE + 16 * t + 4 * h];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, __builtin_fmaf(x[t][i], mul, ls[i]));
+            }
+            if (__any(top > pass)) {
+                const float f = rescale(top, pass, ref, mu);
                 l *= f;
 #pragma unroll
                 for (int g = 0; g < NG; ++g) z[g] *= f;
@@ -699,6 +723,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
         u32x4 klo[4 * 64];                  // lo_operand of K
         float ks[4 * TILE];                 // K's s, in fp32 once for all rows
         float vs[4 * TILE], vlo[4 * TILE];  // and V's
+        float vtop[kKeys];                  // log2 of each key's largest s of V
     };
     extern __shared__ __align__(16) uint8_t lds_raw[];
     Turn *const turns = (Turn *)lds_raw;
@@ -747,17 +772,16 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
     const int all_lo = a.window ? j.pos0 + last / a.R - a.window + 1 : 0;
 
     f32x4 o[2][NT];
-    float z[2][NG], m[2], pass[2], ref[2], mu[2], l[2];
+    float z[2][NG], pass[2], ref[2], mu[2], l[2];
 #pragma unroll
     for (int ct = 0; ct < 2; ++ct) {
 #pragma unroll
         for (int c = 0; c < NT; ++c) o[ct][c] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int g = 0; g < NG; ++g) z[ct][g] = 0.0f;
-        m[ct] = pass[ct] = ref[ct] = -__builtin_inff();
+        pass[ct] = ref[ct] = -__builtin_inff();
         mu[ct] = l[ct] = 0.0f;
     }
-    float s_top = 0.0f;
     bool bad_page = false;
 
     // this wave's tile of a turn: loaded, then laid out in LDS
@@ -791,14 +815,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
         // what lies at keys that no row sees may be anything
         const int key = t * kKeys + 16 * wave + col;
         const bool in = key >= j.kbeg && key < j.kend;
+        float s_top = 0.0f;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             to.ks[wave * TILE + 64 * i + lane] = in ? s_of(kp[i]) : 0.0f;
             kp[i] = in ? kp[i] : 0;
-            to.vs[wave * TILE + 64 * i + lane] = in ? s_of(vp[i]) : 0.0f;
+            const float s = in ? s_of(vp[i]) : 0.0f;
+            s_top = fmaxf(s_top, s);
+            to.vs[wave * TILE + 64 * i + lane] = s;
             to.vlo[wave * TILE + 64 * i + lane] = in ? lo_of(vp[i]) : 0.0f;
         }
         to.klo[wave * 64 + lane] = lo_operand<NG>(kp, h);
+        to.vtop[16 * wave + col] = log2_top<NG>(s_top);
     };
     if (turn < t_end) {
         look_up(turn);
@@ -812,9 +840,6 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
         fetch(turn + 1);  // past the end: the last tile again
         look_up(turn + 2);
         if (turn * kKeys < any_hi && (turn + 1) * kKeys > any_lo) {
-            float s_here = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4 * NP; ++i) s_here = fmaxf(s_here, now.vs[64 * i + lane]);
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
                 const int key0 = turn * kKeys + 32 * half;
@@ -843,7 +868,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);
-                float mul[2] = {up[0], up[1]}, mx[2];
+                float mul[2] = {up[0], up[1]}, top[2];
 #pragma unroll
                 for (int ct = 0; ct < 2; ++ct) {
                     if (a.softcap > 0.0f) cap_logits(a.softcap, x[ct], mul[ct]);
@@ -853,21 +878,23 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
                             const int key = key0 + 16 * (i / 4) + 4 * h + i % 4;
                             if (key < k_lo[ct] || key >= k_hi[ct]) x[ct][i / 4][i % 4] = -__builtin_inff();
                         }
-                    mx[ct] = x[ct][0][0];
+                    top[ct] = x[ct][0][0];
 #pragma unroll
-                    for (int i = 1; i < 8; ++i) mx[ct] = fmaxf(mx[ct], x[ct][i / 4][i % 4]);
+                    for (int i = 1; i < 8; ++i) top[ct] = fmaxf(top[ct], x[ct][i / 4][i % 4]);
                 }
-                if (__any(mx[0] > pass[0] || mx[1] > pass[1] || s_here > s_top)) {
-                    for (int off = 32; off; off >>= 1) s_here = fmaxf(s_here, __shfl_xor(s_here, off, 64));
-                    s_top = fmaxf(s_top, s_here);
+                const f32x4 ls[2] = {*(const f32x4 *)&now.vtop[32 * half + 4 * h], *(const f32x4 *)&now.vtop[32 * half + 16 + 4 * h]};
+                float most = ls[0][0];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) most = fmaxf(most, ls[i / 4][i % 4]);
+                // the largest logit with the largest s: a bound, and rarely past (2048 queries over
+                // 8192 keys 504 us, with each logit's own s 512)
+                if (__any(__builtin_fmaf(top[0], mul[0], most) > pass[0] || __builtin_fmaf(top[1], mul[1], most) > pass[1])) {
 #pragma unroll
                     for (int ct = 0; ct < 2; ++ct) {
-                        mx[ct] = row_max(mx[ct]);
-                        if (mx[ct] > pass[ct]) m[ct] = mx[ct] * mul[ct], pass[ct] = (m[ct] + 8.0f) / mul[ct];
-                        const float to = m[ct] + exponent_above(s_top);
-                        const float f = ref[ct] == -__builtin_inff() ? 1.0f : exp2_fast(ref[ct] - to);
-                        ref[ct] = to;
-                        mu[ct] = ref[ct] == -__builtin_inff() ? 0.0f : ref[ct];
+                        float t = -__builtin_inff();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) t = fmaxf(t, __builtin_fmaf(x[ct][i / 4][i % 4], mul[ct], ls[i / 4][i % 4]));
+                        const float f = rescale(t, pass[ct], ref[ct], mu[ct]);
                         l[ct] *= f;
 #pragma unroll
                         for (int g = 0; g < NG; ++g) z[ct][g] *= f;
@@ -1016,7 +1043,7 @@ hipError_t attend(const Kv4Attn &a, hipStream_t s)
     if (!a.prompt) {
         k_kv4_attn<D, G, BF><<<dim3((uint32_t)blocks), dim3(64 * kWaves), 0, s>>>(a);
     } else if constexpr (has_prompt(D, G)) {
-        constexpr int lds = 2 * (4 * (D / 32) * 1024 + 2 * (D / 16) * 1024 + 4 * 1024 + 3 * 4 * 64 * Stage<D, G>::NP * 4);
+        constexpr int lds = 2 * (4 * (D / 32) * 1024 + 2 * (D / 16) * 1024 + 4 * 1024 + 3 * 4 * 64 * Stage<D, G>::NP * 4 + kKeys * 4);
         // above 64 KB LDS has to be asked for; the attribute is per device, and cheap
         if (lds > 65536) {
             e = hipFuncSetAttribute((const void *)k_kv4_prompt<D, G, BF>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);

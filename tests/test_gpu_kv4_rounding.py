@@ -126,3 +126,47 @@ def test_soft_cap_of_any_size(cap, H, D, G, P, wide):
         assert np.abs(gl - wl).max() <= off + 2.0 ** -22 * np.abs(wl).max()
         vmax, smax = np.abs(ref.value(1, slots)).max(), float(ref.s[1].max())
         assert (np.abs(got - wo) <= EPS["f16"] / 2 * np.abs(wo) + 2 * off * vmax + 2.0 ** -18 * smax).all()
+
+
+@pytest.mark.parametrize("H,D,G,P", SHAPES)
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("wide", [False, True])
+def test_a_huge_token_that_no_row_looks_at(H, D, G, P, dt, wide):
+    """One token's V is 2^25 times the others', with e^-40 of their weight: the others' average keeps the bits of one
+    rounding (as in test_outlier_channels; that token's own share is 1e-10 of it)."""
+    import torch
+    T, nq, R = 300, 32, 4
+    say(f"[gpu] kv4 huge token H={H} D={D} G={G} {dt} wide={wide}")
+    c = torch.zeros(T)
+    c[140] = -40.0
+    k = c.view(T, 1, 1).expand(T, H, D).contiguous().to(tdt(dt))
+    v = torch.randn((T, H, D), generator=torch.Generator().manual_seed(11)) * 1e-3 + 1e-3
+    v[140] *= 3e7 / 2
+    cache, ref, table, slots = hold(k, v.clamp(-6e4, 6e4).to(tdt(dt)), G, P)
+    q = torch.ones((nq, H * R, D), dtype=tdt(dt))
+    got, gl = attend(cache, table, q, T, wide, scale=1.0 / D)
+    wo, wl = exact(ref, slots, q, 1.0 / D)
+    # an average near 1e-3 may lie among fp16's subnormals, whose step is 2^-24 everywhere
+    least = 2.0 ** -25 / math.sqrt(3) if dt == "f16" else 0.0
+    assert rms(got - wo) <= 1.1 * max(EPS[dt] / 2 / math.sqrt(3) * rms(wo), least)
+    assert np.abs(gl - wl).max() <= 2.0 ** -20 * 6
+
+
+@pytest.mark.parametrize("H,D,G,P", SHAPES)
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("wide", [False, True])
+def test_tokens_of_very_different_sizes(H, D, G, P, dt, wide):
+    """V of sizes from 2^-9 to 2^12, each token with a weight that makes its share the same, in an order that goes up and
+    down: one rounding (as in test_outlier_channels)."""
+    import torch
+    T, nq, R = 600, 32, 4
+    say(f"[gpu] kv4 sizes H={H} D={D} G={G} {dt} wide={wide}")
+    size = 2.0 ** (torch.rand(T, generator=torch.Generator().manual_seed(13)) * 21.0 - 9.0)
+    k = (-size.log()).view(T, 1, 1).expand(T, H, D).contiguous().to(tdt(dt))
+    v = (torch.randn((T, H, D), generator=torch.Generator().manual_seed(14)).clamp(-4, 4) * size.view(T, 1, 1)).to(tdt(dt))
+    cache, ref, table, slots = hold(k, v, G, P)
+    q = torch.ones((nq, H * R, D), dtype=tdt(dt))
+    got, gl = attend(cache, table, q, T, wide, scale=1.0 / D)
+    wo, wl = exact(ref, slots, q, 1.0 / D)
+    assert rms(got - wo) <= 1.1 * EPS[dt] / 2 / math.sqrt(3) * rms(wo)
+    assert np.abs(gl - wl).max() <= 2.0 ** -19 * np.abs(wl).max()
