@@ -598,8 +598,8 @@ def kv4_attention(cache: Kv4Cache, q, page_table, kv_len, cu_q=None, max_q: Opti
     """Attention of q [n_q][Hq][D] (float16 or bfloat16) over the cached keys:
     the last query of sequence b stands at its last key.  page_table int32
     [B][max_pages], kv_len int32 [B]; cu_q int32 [B + 1] bounds each
-    sequence's queries (at most max_q; n_q if not given), without it every
-    sequence has n_q / B.  `work`: uint8 of kv4_work_bytes, allocated if not
+    sequence's queries (at most max_q; n_q if not given; rows outside all of
+    them are not written), without it every sequence has n_q / B.  `work`: uint8 of kv4_work_bytes, allocated if not
     given.  What is allocated here belongs to `stream` (the current one if not
     given).  Returns out, or (out, lse float32 [n_q][Hq])."""
     if q.dim() != 3 or page_table.dim() != 2:

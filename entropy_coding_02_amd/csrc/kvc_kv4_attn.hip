@@ -992,14 +992,17 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
 }
 
 // Joins the splits of a row: D/4 lanes a split, as many splits at a time as
-// fill the block, then their sums through LDS.
+// fill the block, then their sums through LDS.  Rows that no sequence has were
+// not written by any split, and are left alone here too.
 template <int D, bool BF, int THREADS>
 __global__ __launch_bounds__(THREADS) void k_kv4_join(Kv4Attn a)
 {
     constexpr int LANES = D / 4, AT_ONCE = THREADS / LANES;
     __shared__ f32x4 lds_y[AT_ONCE][LANES];
     __shared__ float lds_l[AT_ONCE];
-    const int64_t rows = a.n_q * a.Hq, row = blockIdx.x;
+    const int64_t rows = a.n_q * a.Hq;
+    const int64_t row = (a.cu_q ? (int64_t)max(scalar_load(a.cu_q, 0), 0) * a.Hq : 0) + blockIdx.x;
+    if (row >= (a.cu_q ? min((int64_t)scalar_load(a.cu_q, a.B), a.n_q) * a.Hq : rows)) return;
     const int part = threadIdx.x % LANES, first = threadIdx.x / LANES;
     float M = -__builtin_inff();
     for (int s = threadIdx.x & 63; s < a.ns; s += 64) M = fmaxf(M, a.part_ml[(s * rows + row) * 2]);
@@ -1053,7 +1056,7 @@ hipError_t attend(const Kv4Attn &a, hipStream_t s)
     }
     e = hipGetLastError();
     if (e == hipSuccess && a.ns > 1) {
-        const dim3 rows((uint32_t)(a.n_q * a.Hq));
+        const dim3 rows((uint32_t)(std::min(a.n_q, (int64_t)a.B * a.max_q) * a.Hq));  // as many as sequences may have
         if (a.ns <= 8)
             k_kv4_join<D, BF, 64><<<rows, dim3(64), 0, s>>>(a);
         else

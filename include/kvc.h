@@ -512,7 +512,9 @@ typedef struct kvc_kv4_attn {
                                   each P tokens of a sequence; entries past its length are not read */
     int64_t table_stride;
     const int32_t *kv_len;     /* [n_seqs]; below 0 is taken as 0 */
-    const int32_t *cu_q;       /* [n_seqs + 1] rising from 0 to n_q, or NULL: max_q queries each */
+    const int32_t *cu_q;       /* [n_seqs + 1] rising within 0..n_q, or NULL: max_q queries each.  Query tokens
+                                  before the first or from the last on are no sequence's (the padding of a
+                                  captured batch): their rows of out and lse are not written */
     int64_t n_q;               /* query tokens in all */
     int32_t n_seqs, n_q_heads, max_pages;
     int32_t max_q;             /* the most queries of one sequence */
