@@ -105,8 +105,12 @@ __device__ __forceinline__ GroupScale group_scale(float hi, float nlo)
     return g;
 }
 
+// WIDE: x may lie past the fp16 range and counts as its border, as in the
+// extremes (lo may have been rounded up to 65504 from a smaller minimum).
+template <bool WIDE>
 __device__ __forceinline__ uint32_t code4(float x, const GroupScale &g)
 {
+    if (WIDE) x = __builtin_amdgcn_fmed3f(x, -65504.0f, 65504.0f);
     const float r = __builtin_rintf((x - g.lo) * g.inv);
     return (uint32_t)fminf(fmaxf(r, 0.0f), 15.0f);
 }
@@ -192,7 +196,7 @@ __device__ __forceinline__ void append_rows(const Kv4Pool &p, const Kv4Rows &r, 
         e.close();
         const GroupScale g = group_scale(run_max<G / 8>(e.hi), run_max<G / 8>(e.nlo));
         uint32_t w = 0;
-        for (int j = 0; j < 8; ++j) w |= code4(x[u].at(j), g) << (4 * j);
+        for (int j = 0; j < 8; ++j) w |= code4<DT != KVC_F16>(x[u].at(j), g) << (4 * j);
         const int P = 1 << p.pshift, off = (int)(slot[u] & (P - 1));
         const int64_t blk = kv4_block(p, slot[u] >> p.pshift, V, head[u]);
         uint8_t *dst = p.codes + blk * (P * (D / 2));
