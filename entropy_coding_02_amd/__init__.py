@@ -455,7 +455,8 @@ def decode(buf: Buffers, out_dtype=KVC_F16, stream=None, payload=None, payload_b
 class Kv4Cache:
     """One layer's paged 4-bit K/V pool: a kvc_kv4_desc, its two device buffers
     and a status word.  Layouts as in kvc.h: codes uint8
-    [n_pages][2][H][P * D/2], params float16 [n_pages][2][H][D/G][P][2] (s, lo)."""
+    [n_pages][2][H][P * D/2], params float16 [n_pages][2][H][D/G][P][2] (s, lo).
+    Another tensor may be assigned to any of the three; it is checked as the first was."""
 
     def __init__(self, n_kv_heads: int, head_dim: int, n_pages: int, page_tokens: int = 64, group: int = 64,
                  codes=None, params=None, dev_status=None, device="cuda"):
@@ -464,27 +465,54 @@ class Kv4Cache:
         self.ref = ctypes.byref(self.c)
         self.n_kv_heads, self.head_dim, self.group = n_kv_heads, head_dim, group
         self.page_tokens, self.n_pages = page_tokens, n_pages
-        sizes = []
-        for fn in ("kvc_kv4_codes_bytes", "kvc_kv4_params_bytes"):
-            v = int(getattr(_load(), fn)(self.ref))
+        self.int32, self.int64, self.float32 = torch.int32, torch.int64, torch.float32
+        self._want = {}  # type and bytes of a buffer
+        for name, dt in (("codes", torch.uint8), ("params", torch.float16)):
+            v = int(getattr(_load(), f"kvc_kv4_{name}_bytes")(self.ref))
             if v < 0:
-                raise KvcError(fn, v)
-            sizes.append(v)
+                raise KvcError(f"kvc_kv4_{name}_bytes", v)
+            self._want[name] = dt, v
         if codes is None:
             codes = torch.empty((n_pages, 2, n_kv_heads, page_tokens * head_dim // 2), dtype=torch.uint8, device=device)
         if params is None:
             params = torch.empty((n_pages, 2, n_kv_heads, head_dim // group, page_tokens, 2), dtype=torch.float16,
                                  device=device)
-        for name, t, dt, nb in (("codes", codes, torch.uint8, sizes[0]), ("params", params, torch.float16, sizes[1])):
-            if t.dtype != dt or t.numel() * t.element_size() != nb:
-                raise ValueError(f"kvc: {name} must be {dt} of {nb} bytes")
-            _ptr(t)
-        if dev_status is None:
-            dev_status = torch.zeros(1, dtype=torch.int32, device=codes.device)
-        self.codes, self.params, self.dev_status = codes, params, dev_status
-        # what every call needs of them
-        self.codes_ptr, self.params_ptr, self.status_ptr = codes.data_ptr(), params.data_ptr(), dev_status.data_ptr()
-        self.int32, self.int64, self.float32 = torch.int32, torch.int64, torch.float32
+        self.codes, self.params = codes, params
+        self.dev_status = torch.zeros(1, dtype=torch.int32, device=codes.device) if dev_status is None else dev_status
+
+    # The calls take the address of each, kept beside it.
+
+    @property
+    def codes(self):
+        return self._codes
+
+    @codes.setter
+    def codes(self, t):
+        self._codes, self.codes_ptr = t, self._checked("codes", t)
+
+    @property
+    def params(self):
+        return self._params
+
+    @params.setter
+    def params(self, t):
+        self._params, self.params_ptr = t, self._checked("params", t)
+
+    @property
+    def dev_status(self):
+        return self._status
+
+    @dev_status.setter
+    def dev_status(self, t):
+        if t.dtype != self.int32 or t.numel() < 1:
+            raise ValueError("kvc: dev_status must be torch.int32")
+        self._status, self.status_ptr = t, _ptr(t)
+
+    def _checked(self, name, t):
+        dt, nb = self._want[name]
+        if t.dtype != dt or t.numel() * t.element_size() != nb:
+            raise ValueError(f"kvc: {name} must be {dt} of {nb} bytes")
+        return _ptr(t)
 
 
 _KV4_DTYPES = {}  # torch.dtype -> KVC_* (filled on first use: torch is imported late)

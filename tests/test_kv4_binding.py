@@ -102,3 +102,36 @@ def test_without_a_stream_the_current_one_is_used(calls):
     assert all(a[-1] == 77 for _, a in calls)
     attention(pool(), stream=0)  # the default stream's handle
     assert calls[-1][1][-1] == 0 and ALLOCATED[-1].home.cuda_stream == 0
+
+
+def launched(calls, n=1):
+    return [a for _, a in calls[-n:]]
+
+
+def test_an_assigned_buffer_is_the_one_used(calls):
+    cache = pool()
+    new = Fake(cache.codes.shape, torch.uint8), Fake(cache.params.shape, torch.float16), Fake((1,), torch.int32)
+    cache.codes, cache.params, cache.dev_status = new
+    assert (cache.codes, cache.params, cache.dev_status) == new
+    slots, rows = Fake((5,), torch.int64), (Fake((5, 2, 64), torch.float16), Fake((5, 2, 64), torch.float16))
+    kvc.kv4_append(cache, *rows, slots)
+    kvc.kv4_read(cache, slots)
+    attention(cache)
+    for args in launched(calls, 3):
+        for t in new:
+            assert t.data_ptr() in args
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("codes", lambda c: Fake((1,), torch.uint8)), ("codes", lambda c: Fake(c.codes.shape, torch.int8)),
+    ("codes", lambda c: Fake(c.codes.shape, torch.uint8, strides=(1, 1, 1, 1))),
+    ("params", lambda c: Fake((1,), torch.float16)), ("params", lambda c: Fake(c.params.shape, torch.bfloat16)),
+    ("codes", lambda c: torch.empty(c.codes.shape, dtype=torch.uint8)),
+    ("dev_status", lambda c: Fake((1,), torch.int64)), ("dev_status", lambda c: Fake((0,), torch.int32)),
+    ("dev_status", lambda c: torch.zeros(1, dtype=torch.int32))])
+def test_an_assigned_buffer_is_checked(calls, name, bad):
+    cache = pool()
+    kept = getattr(cache, name)
+    with pytest.raises(ValueError):
+        setattr(cache, name, bad(cache))
+    assert getattr(cache, name) is kept and kept.data_ptr() in (cache.codes_ptr, cache.params_ptr, cache.status_ptr)
