@@ -556,8 +556,9 @@ def _kv4_empty(stream, like, shape, dtype):
         return like.new_empty(shape, dtype=dtype)
 
 
-def _rows(name: str, t, shape):
-    """Pointer and strides of a device tensor [n][heads][D] whose channels are contiguous."""
+def _rows(name: str, t, shape, written=False):
+    """Pointer and strides of a device tensor [n][heads][D] whose channels are contiguous; one that is written
+    may not have rows in each other's place (an expanded tensor)."""
     if t.shape != shape or t.dim() != 3:
         raise ValueError(f"kvc: {name} must be {list(shape)}, not {list(t.shape)}")
     if not t.is_cuda:
@@ -565,6 +566,8 @@ def _rows(name: str, t, shape):
     ts, hs, cs = t.stride()
     if cs != 1:
         raise ValueError(f"kvc: the channels of {name} must be contiguous")
+    if written and (-shape[2] < ts < shape[2] and shape[0] > 1 or -shape[2] < hs < shape[2] and shape[1] > 1):
+        raise ValueError(f"kvc: the rows of {name} overlap")
     return t.data_ptr(), ts, hs
 
 
@@ -603,8 +606,8 @@ def kv4_read(cache: Kv4Cache, slots, dtype=None, k=None, v=None, stream=None):
     v = _kv4_empty(stream, slots, shape, dtype) if v is None else v
     if k.dtype != dtype or v.dtype != dtype:
         raise ValueError("kvc: k and v must have one dtype")
-    kp, kts, khs = _rows("k", k, shape)
-    vp, vts, vhs = _rows("v", v, shape)
+    kp, kts, khs = _rows("k", k, shape, True)
+    vp, vts, vhs = _rows("v", v, shape, True)
     rc = _load().kvc_kv4_read(cache.ref, cache.codes_ptr, cache.params_ptr, _ints("slots", slots, cache.int64, (n,)), n,
                               kp, vp, kts, khs, vts, vhs, _kv4_dtype(dtype), cache.status_ptr, _kv4_stream(stream, k))
     _check("kvc_kv4_read", rc)
@@ -660,7 +663,7 @@ def kv4_attention(cache: Kv4Cache, q, page_table, kv_len, cu_q=None, max_q: Opti
         nb = kv4_work_bytes(cache, n_q, n_heads, B, max_pages, max_q)
         work = _kv4_empty(stream, q, (nb,), cache.codes.dtype) if nb else None
     qp, qts, qhs = _rows("q", q, shape)
-    op, ots, ohs = _rows("out", out, shape)
+    op, ots, ohs = _rows("out", out, shape, True)
     args = _ATTN.pack(
         qp, op, 0 if lse is None else _ptr(lse), qts, qhs, ots, ohs, page_table.data_ptr(), page_table.stride(0),
         _ints("kv_len", kv_len, i32, (B,)), 0 if cu_q is None else _ints("cu_q", cu_q, i32, (B + 1,)),

@@ -484,7 +484,7 @@ int kvc_kv4_append(const kvc_kv4_desc *desc, const void *k, const void *v, int64
  * KVC_F16 clamped to +-65504 first: a value can pass its group's largest by
  * the rounding of s).
  *   k, v    [n_tokens][H][D] of out_dtype (KVC_F16, KVC_F32 or KVC_BF16; device, written),
- *           strides as kvc_kv4_append; either may be NULL
+ *           strides as kvc_kv4_append (no two rows in one place); either may be NULL
  *   slots   as kvc_kv4_append; the rows of a negative or bad slot are written as zeros
  */
 int kvc_kv4_read(const kvc_kv4_desc *desc, const uint8_t *codes, const uint16_t *params,
@@ -505,7 +505,7 @@ int kvc_kv4_read(const kvc_kv4_desc *desc, const uint8_t *codes, const uint16_t 
  */
 typedef struct kvc_kv4_attn {
     const void *q;             /* [n_q][n_q_heads][D] of dtype (KVC_F16 or KVC_BF16), channels contiguous */
-    void *out;                 /* as q (written); must not overlap q */
+    void *out;                 /* as q (written); must not overlap q, nor its rows each other */
     float *lse;                /* NULL, or [n_q][n_q_heads] (written) */
     int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride; /* elements */
     const int32_t *page_table; /* [n_seqs][max_pages], rows table_stride entries apart: the page of

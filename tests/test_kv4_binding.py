@@ -135,3 +135,28 @@ def test_an_assigned_buffer_is_checked(calls, name, bad):
     with pytest.raises(ValueError):
         setattr(cache, name, bad(cache))
     assert getattr(cache, name) is kept and kept.data_ptr() in (cache.codes_ptr, cache.params_ptr, cache.status_ptr)
+
+
+@pytest.mark.parametrize("strides", [(0, 64, 1), (128, 0, 1), (128, 63, 1), (-63, 640, 1), (0, 0, 1)])
+def test_written_rows_may_not_overlap(calls, strides):
+    cache = pool()
+    ok = Fake((2, 2, 64), torch.float16)
+    bad = Fake((2, 2, 64), torch.float16, strides=strides)
+    for kw in (dict(k=bad, v=ok), dict(k=ok, v=bad)):
+        with pytest.raises(ValueError):
+            kvc.kv4_read(cache, Fake((2,), torch.int64), **kw)
+    with pytest.raises(ValueError):
+        attention(cache, q=ok, page_table=Fake((2, 9), torch.int32), kv_len=Fake((2,), torch.int32), out=bad)
+    assert not calls
+    kvc.kv4_append(cache, bad, bad, Fake((2,), torch.int64))  # what is only read may be broadcast
+    attention(cache, q=bad, page_table=Fake((2, 9), torch.int32), kv_len=Fake((2,), torch.int32), out=ok)
+    assert len(calls) == 2
+
+
+def test_strides_that_no_row_uses_and_negative_ones(calls):
+    cache = pool(H=1)
+    kvc.kv4_read(cache, Fake((3,), torch.int64), k=Fake((3, 1, 64), torch.float16, strides=(-64, 0, 1)),
+                 v=Fake((3, 1, 64), torch.float16, strides=(64, 1, 1)))
+    kvc.kv4_read(cache, Fake((1,), torch.int64), k=Fake((1, 1, 64), torch.float16, strides=(0, 0, 1)),
+                 v=Fake((1, 1, 64), torch.float16, strides=(1, 64, 1)))
+    assert len(calls) == 2
