@@ -472,11 +472,14 @@ class Kv4Cache:
             if v < 0:
                 raise KvcError(f"kvc_kv4_{name}_bytes", v)
             self._want[name] = dt, v
+        given = [t for t in (codes, params, dev_status) if t is not None]
+        device = given[0].device if given else device
         if codes is None:
             codes = torch.empty((n_pages, 2, n_kv_heads, page_tokens * head_dim // 2), dtype=torch.uint8, device=device)
         if params is None:
             params = torch.empty((n_pages, 2, n_kv_heads, head_dim // group, page_tokens, 2), dtype=torch.float16,
                                  device=device)
+        self.device_index = codes.get_device()
         self.codes, self.params = codes, params
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=codes.device) if dev_status is None else dev_status
 
@@ -506,18 +509,22 @@ class Kv4Cache:
     def dev_status(self, t):
         if t.dtype != self.int32 or t.numel() < 1:
             raise ValueError("kvc: dev_status must be torch.int32")
+        if t.get_device() != self.device_index:
+            raise _wrong_device("dev_status", t)
         self._status, self.status_ptr = t, _ptr(t)
 
     def _checked(self, name, t):
         dt, nb = self._want[name]
         if t.dtype != dt or t.numel() * t.element_size() != nb:
             raise ValueError(f"kvc: {name} must be {dt} of {nb} bytes")
+        if t.get_device() != self.device_index:
+            raise _wrong_device(name, t)
         return _ptr(t)
 
 
 _KV4_DTYPES = {}  # torch.dtype -> KVC_* (filled on first use: torch is imported late)
 _ATTN = struct.Struct("@PPPqqqqPqPPqiiiiiiiffPq")  # kvc_kv4_attn, field by field as KvcKv4Attn
-_RAW_STREAM = None
+_RAW_STREAM = _CURRENT_DEVICE = None
 
 
 def _kv4_dtype(dt):
@@ -531,17 +538,27 @@ def _kv4_dtype(dt):
     return v
 
 
-def _kv4_stream(stream, t):
-    """The caller's stream, or the current one of t's device (without building
-    a torch.cuda.Stream: these calls are a few microseconds long)."""
-    global _RAW_STREAM
-    if stream is not None:
-        return _stream(stream)
+def _wrong_device(name, t):
+    return ValueError(f"kvc: {name} must be on the cache's device" if t.is_cuda else
+                      "kvc: device tensors only (there is no CPU path)")
+
+
+def _kv4_call(fn, cache, stream, *args):
+    """Launches on the caller's stream, or the current one of the cache's device (without building a
+    torch.cuda.Stream: these calls are a few microseconds long), with that device current."""
+    global _RAW_STREAM, _CURRENT_DEVICE
     if _RAW_STREAM is None:
         import torch
         _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda i: torch.cuda.current_stream(i).cuda_stream)
-    return _RAW_STREAM(t.get_device())
+        _CURRENT_DEVICE = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    dev = cache.device_index
+    stream = _RAW_STREAM(dev) if stream is None else _stream(stream)
+    if _CURRENT_DEVICE() == dev:
+        return fn(cache.ref, *args, stream)
+    import torch
+    with torch.cuda.device(dev):
+        return fn(cache.ref, *args, stream)
 
 
 def _kv4_empty(stream, like, shape, dtype):
@@ -556,13 +573,13 @@ def _kv4_empty(stream, like, shape, dtype):
         return like.new_empty(shape, dtype=dtype)
 
 
-def _rows(name: str, t, shape, written=False):
+def _rows(name: str, t, shape, dev: int, written=False):
     """Pointer and strides of a device tensor [n][heads][D] whose channels are contiguous; one that is written
     may not have rows in each other's place (an expanded tensor)."""
-    if t.shape != shape or t.dim() != 3:
+    if t.shape != shape:
         raise ValueError(f"kvc: {name} must be {list(shape)}, not {list(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError("kvc: device tensors only (there is no CPU path)")
+    if t.get_device() != dev:
+        raise _wrong_device(name, t)
     ts, hs, cs = t.stride()
     if cs != 1:
         raise ValueError(f"kvc: the channels of {name} must be contiguous")
@@ -571,25 +588,29 @@ def _rows(name: str, t, shape, written=False):
     return t.data_ptr(), ts, hs
 
 
-def _ints(name: str, t, dt, shape):
+def _ints(name: str, t, dt, shape, dev: int):
     if t.dtype != dt or t.shape != shape:
         raise ValueError(f"kvc: {name} must be {dt} of shape {list(shape)}, not {t.dtype} {list(t.shape)}")
-    return _ptr(t)
+    if t.get_device() != dev:
+        raise _wrong_device(name, t)
+    if not t.is_contiguous():
+        raise ValueError("kvc: tensors must be contiguous")
+    return t.data_ptr()
 
 
 def kv4_append(cache: Kv4Cache, k, v, slots, stream=None):
     """Quantise k, v [T][H][D] (float16, bfloat16 or float32) into the slots
     int64 [T] (page * page_tokens + token in page; negative: skipped)."""
-    n = k.shape[0]
+    n, dev = k.shape[0], cache.device_index
     if v.dtype != k.dtype:
         raise ValueError("kvc: k and v must have one dtype")
     shape = (n, cache.n_kv_heads, cache.head_dim)
-    kp, kts, khs = _rows("k", k, shape)
-    vp, vts, vhs = _rows("v", v, shape)
-    rc = _load().kvc_kv4_append(cache.ref, kp, vp, n, kts, khs, vts, vhs, _kv4_dtype(k.dtype),
-                                _ints("slots", slots, cache.int64, (n,)), cache.codes_ptr, cache.params_ptr,
-                                cache.status_ptr, _kv4_stream(stream, k))
-    _check("kvc_kv4_append", rc)
+    kp, kts, khs = _rows("k", k, shape, dev)
+    vp, vts, vhs = _rows("v", v, shape, dev)
+    rc = _kv4_call(_load().kvc_kv4_append, cache, stream, kp, vp, n, kts, khs, vts, vhs, _kv4_dtype(k.dtype),
+                   _ints("slots", slots, cache.int64, (n,), dev), cache.codes_ptr, cache.params_ptr, cache.status_ptr)
+    if rc:
+        raise KvcError("kvc_kv4_append", rc)
 
 
 def kv4_read(cache: Kv4Cache, slots, dtype=None, k=None, v=None, stream=None):
@@ -598,19 +619,23 @@ def kv4_read(cache: Kv4Cache, slots, dtype=None, k=None, v=None, stream=None):
     What is allocated here belongs to `stream` (the current one if not given)."""
     if slots.dim() != 1:
         raise ValueError("kvc: slots must be int64 [T]")
-    n = slots.shape[0]
+    n, dev = slots.shape[0], cache.device_index
     if dtype is None:
         dtype = cache.params.dtype if k is None and v is None else (v if k is None else k).dtype
     shape = (n, cache.n_kv_heads, cache.head_dim)
-    k = _kv4_empty(stream, slots, shape, dtype) if k is None else k
-    v = _kv4_empty(stream, slots, shape, dtype) if v is None else v
+    if k is None:
+        k = slots.new_empty(shape, dtype=dtype) if stream is None else _kv4_empty(stream, slots, shape, dtype)
+    if v is None:
+        v = slots.new_empty(shape, dtype=dtype) if stream is None else _kv4_empty(stream, slots, shape, dtype)
     if k.dtype != dtype or v.dtype != dtype:
         raise ValueError("kvc: k and v must have one dtype")
-    kp, kts, khs = _rows("k", k, shape, True)
-    vp, vts, vhs = _rows("v", v, shape, True)
-    rc = _load().kvc_kv4_read(cache.ref, cache.codes_ptr, cache.params_ptr, _ints("slots", slots, cache.int64, (n,)), n,
-                              kp, vp, kts, khs, vts, vhs, _kv4_dtype(dtype), cache.status_ptr, _kv4_stream(stream, k))
-    _check("kvc_kv4_read", rc)
+    kp, kts, khs = _rows("k", k, shape, dev, True)
+    vp, vts, vhs = _rows("v", v, shape, dev, True)
+    rc = _kv4_call(_load().kvc_kv4_read, cache, stream, cache.codes_ptr, cache.params_ptr,
+                   _ints("slots", slots, cache.int64, (n,), dev), n, kp, vp, kts, khs, vts, vhs, _kv4_dtype(dtype),
+                   cache.status_ptr)
+    if rc:
+        raise KvcError("kvc_kv4_read", rc)
     return k, v
 
 
@@ -629,8 +654,9 @@ def kv4_attention(cache: Kv4Cache, q, page_table, kv_len, cu_q=None, max_q: Opti
     """Attention of q [n_q][Hq][D] (float16 or bfloat16) over the cached keys:
     the last query of sequence b stands at its last key.  page_table int32
     [B][max_pages], kv_len int32 [B]; cu_q int32 [B + 1] bounds each
-    sequence's queries (at most max_q; n_q if not given; rows outside all of
-    them are not written), without it every sequence has n_q / B.  `work`: uint8 of kv4_work_bytes, allocated if not
+    sequence's queries (at most max_q, by which the launch is planned; n_q if
+    not given; rows outside all of them are not written), without it every
+    sequence has n_q / B.  `work`: uint8 of kv4_work_bytes, allocated if not
     given.  What is allocated here belongs to `stream` (the current one if not
     given).  Returns out, or (out, lse float32 [n_q][Hq])."""
     if q.dim() != 3 or page_table.dim() != 2:
@@ -638,9 +664,11 @@ def kv4_attention(cache: Kv4Cache, q, page_table, kv_len, cu_q=None, max_q: Opti
     n_q, n_heads, _ = q.shape
     shape = (n_q, n_heads, cache.head_dim)
     B, max_pages = page_table.shape
-    i32, dtype = cache.int32, q.dtype
-    if page_table.dtype != i32 or not page_table.is_cuda or (max_pages > 1 and page_table.stride(1) != 1):
+    i32, f32, dtype, dev = cache.int32, cache.float32, q.dtype, cache.device_index
+    if page_table.dtype != i32 or (max_pages > 1 and page_table.stride(1) != 1):
         raise ValueError("kvc: page_table must be a device int32 tensor with contiguous rows")
+    if page_table.get_device() != dev:
+        raise _wrong_device("page_table", page_table)
     if cu_q is None:
         if B == 0 or n_q % B:
             raise ValueError("kvc: without cu_q every sequence has the same number of queries")
@@ -650,27 +678,28 @@ def kv4_attention(cache: Kv4Cache, q, page_table, kv_len, cu_q=None, max_q: Opti
     elif max_q is None:
         max_q = n_q
     if out is None:
-        out = _kv4_empty(stream, q, shape, dtype)
+        out = q.new_empty(shape) if stream is None else _kv4_empty(stream, q, shape, dtype)
     elif out.dtype != dtype:
         raise ValueError("kvc: out must have q's dtype")
     if lse is not None:
         return_lse = True
-        if lse.dtype != cache.float32 or lse.shape != shape[:2]:
-            raise ValueError("kvc: lse must be float32 [n_q][Hq]")
     elif return_lse:
-        lse = _kv4_empty(stream, q, shape[:2], cache.float32)
+        lse = q.new_empty(shape[:2], dtype=f32) if stream is None else _kv4_empty(stream, q, shape[:2], f32)
     if work is None:
         nb = kv4_work_bytes(cache, n_q, n_heads, B, max_pages, max_q)
         work = _kv4_empty(stream, q, (nb,), cache.codes.dtype) if nb else None
-    qp, qts, qhs = _rows("q", q, shape)
-    op, ots, ohs = _rows("out", out, shape, True)
+    elif work.get_device() != dev:
+        raise _wrong_device("work", work)
+    qp, qts, qhs = _rows("q", q, shape, dev)
+    op, ots, ohs = _rows("out", out, shape, dev, True)
     args = _ATTN.pack(
-        qp, op, 0 if lse is None else _ptr(lse), qts, qhs, ots, ohs, page_table.data_ptr(), page_table.stride(0),
-        _ints("kv_len", kv_len, i32, (B,)), 0 if cu_q is None else _ints("cu_q", cu_q, i32, (B + 1,)),
+        qp, op, 0 if lse is None else _ints("lse", lse, f32, shape[:2], dev), qts, qhs, ots, ohs,
+        page_table.data_ptr(), page_table.stride(0),
+        _ints("kv_len", kv_len, i32, (B,), dev), 0 if cu_q is None else _ints("cu_q", cu_q, i32, (B + 1,), dev),
         n_q, B, n_heads, max_pages, max_q, _kv4_dtype(dtype), bool(causal), window, softcap,
         cache.head_dim ** -0.5 if scale is None else scale, 0 if work is None else _ptr(work),
         0 if work is None else work.numel() * work.element_size())
-    rc = _load().kvc_kv4_attention(cache.ref, args, cache.codes_ptr, cache.params_ptr, cache.status_ptr,
-                                   _kv4_stream(stream, q))
-    _check("kvc_kv4_attention", rc)
+    rc = _kv4_call(_load().kvc_kv4_attention, cache, stream, args, cache.codes_ptr, cache.params_ptr, cache.status_ptr)
+    if rc:
+        raise KvcError("kvc_kv4_attention", rc)
     return (out, lse) if return_lse else out

@@ -62,7 +62,8 @@ def calls(monkeypatch):
         STREAMS.pop()
 
     monkeypatch.setattr(kvc, "_load", lambda: lib)
-    monkeypatch.setattr(kvc, "_RAW_STREAM", lambda i: 77)
+    monkeypatch.setattr(kvc, "_RAW_STREAM", lambda i: 77 + i)
+    monkeypatch.setattr(kvc, "_CURRENT_DEVICE", lambda: 0, raising=False)
     monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: types.SimpleNamespace(cuda_stream=h))
     monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: types.SimpleNamespace(cuda_stream=0))
@@ -160,3 +161,45 @@ def test_strides_that_no_row_uses_and_negative_ones(calls):
     kvc.kv4_read(cache, Fake((1,), torch.int64), k=Fake((1, 1, 64), torch.float16, strides=(0, 0, 1)),
                  v=Fake((1, 1, 64), torch.float16, strides=(1, 64, 1)))
     assert len(calls) == 2
+
+
+def test_tensors_of_another_device_are_refused(calls):
+    cache, f16, i32, i64 = pool(), torch.float16, torch.int32, torch.int64
+    here, there = Fake((2, 2, 64), f16), Fake((2, 2, 64), f16, device=1)
+    for call in (lambda: kvc.kv4_append(cache, there, here, Fake((2,), i64)),
+                 lambda: kvc.kv4_append(cache, here, there, Fake((2,), i64)),
+                 lambda: kvc.kv4_append(cache, here, here, Fake((2,), i64, device=1)),
+                 lambda: kvc.kv4_read(cache, Fake((2,), i64, device=1)),
+                 lambda: kvc.kv4_read(cache, Fake((2,), i64), k=there, v=here),
+                 lambda: attention(cache, q=Fake((1, 4, 64), f16, device=1)),
+                 lambda: attention(cache, out=Fake((1, 4, 64), f16, device=1)),
+                 lambda: attention(cache, lse=Fake((1, 4), torch.float32, device=1)),
+                 lambda: attention(cache, page_table=Fake((1, 200), i32, device=1)),
+                 lambda: attention(cache, kv_len=Fake((1,), i32, device=1)),
+                 lambda: attention(cache, cu_q=Fake((2,), i32, device=1), max_q=1),
+                 lambda: attention(cache, work=Fake((1 << 20,), torch.uint8, device=1)),
+                 lambda: setattr(cache, "codes", Fake(cache.codes.shape, torch.uint8, device=1)),
+                 lambda: setattr(cache, "params", Fake(cache.params.shape, f16, device=1)),
+                 lambda: setattr(cache, "dev_status", Fake((1,), i32, device=1))):
+        with pytest.raises(ValueError):
+            call()
+    assert not calls
+
+
+def test_the_cache_s_device_is_current_at_the_launch(calls, monkeypatch):
+    entered = []
+
+    @contextlib.contextmanager
+    def device(i):
+        entered.append(i)
+        n = len(calls)
+        yield
+        assert len(calls) == n + 1
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    cache = pool(device=1)
+    rows = Fake((2, 2, 64), torch.float16, device=1)
+    kvc.kv4_append(cache, rows, rows, Fake((2,), torch.int64, device=1))
+    assert entered == [1] and calls[-1][1][-1] == 78  # the current stream of that device
+    kvc.kv4_append(pool(), Fake((2, 2, 64), torch.float16), Fake((2, 2, 64), torch.float16), Fake((2,), torch.int64))
+    assert entered == [1] and calls[-1][1][-1] == 77
