@@ -11,7 +11,11 @@
 // (The matrix instructions take the subnormals too, but align a sum's products
 // by exponent, and a subnormal's leading bits lie up to ten places below its:
 // outputs that average many keys then lost twice their last fp16 bit.)
-//   output   o_c = sum_j (p_j s_jg) n_jc + sum_j p_j lo_jg,  c in group g.
+//   output   o_c = sum_j (p_j s_jg) (n_jc - 7.5) + sum_j p_j mid_jg,  c in group g,
+//            mid = lo + 7.5 s.  Sums of n itself are all positive and cancel
+//            against lo; what they rounded off added up (2048 queries over 8192
+//            keys of values of either sign: outputs off by 8e-5 in the mean,
+//            centred by 8e-7, in the same time).
 // p_j s_jg enters the matrix product as two fp16 terms (22 bits): one would
 // be an error of the output's own size, since n s is up to twice the value it
 // belongs to.  They keep those bits because p is taken relative not to the
@@ -26,7 +30,7 @@
 // Orientation: S^T = K q^T (16 keys x 16 query rows), so a lane holds one
 // query row and four keys of a tile, which is just what P^T needs as the
 // right operand of O^T = V^T P^T (keys 4h .. 4h+3 of two tiles are its eight
-// k indices): probabilities never cross lanes, the terms with lo and the row
+// k indices): probabilities never cross lanes, the terms with mid and the row
 // sums are plain fp32 sums per lane, added over the four lanes of a row once
 // at the end.
 #include <algorithm>
@@ -62,6 +66,13 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w, int i)
     const _Float16 f = i & 1 ? (_Float16)0x1p11f : (_Float16)0x1p15f;
     return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, b) * f16x2{f, f});
 }
+// The same less 7.5, exactly, for V.
+__device__ __forceinline__ uint32_t centred_pair(uint32_t w, int i)
+{
+    const uint32_t b = (i < 2 ? w : w >> 8) & (i & 1 ? 0x00F000F0u : 0x000F000Fu);
+    const _Float16 f = i & 1 ? (_Float16)0x1p11f : (_Float16)0x1p15f, c = (_Float16)(-7.5f * 0x1p-9f);
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(f16x2, b), f16x2{f, f}, f16x2{c, c}));
+}
 // A K dword (8 channels of a key) as 8 operands in the order 0,4,1,5,2,6,3,7.
 __device__ __forceinline__ u32x4 code_octet(uint32_t w)
 {
@@ -70,6 +81,7 @@ __device__ __forceinline__ u32x4 code_octet(uint32_t w)
 
 __device__ __forceinline__ float s_of(uint32_t w) { return kvc_h2f(w & 0xFFFF); }
 __device__ __forceinline__ float lo_of(uint32_t w) { return kvc_h2f(w >> 16); }
+__device__ __forceinline__ float mid_of(uint32_t w) { return __builtin_fmaf(7.5f, s_of(w), lo_of(w)); }  // of a group's range
 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b)
 {
@@ -443,7 +455,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
 {
     constexpr int NW = D / 32, NG = D / G, NT = D / 16, NP = Stage<D, G>::NP, TILE = 64 * NP, NQ = (NW + kWaves - 1) / kWaves;
     // Each wave's results; while it runs, its parameters, [tile] K's s, then
-    // [tile][s|lo] V's, each [group][16 keys], in fp32 (mixed-precision instructions run at half
+    // [tile][s|mid] V's, each [group][16 keys], in fp32 (mixed-precision instructions run at half
     // rate), then [tile] log2 of each key's largest s of V.
     __shared__ __align__(16) float lds_o[kWaves][16][D];
     __shared__ float lds_ml[kWaves][2][16];
@@ -532,7 +544,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
                 for (int i = 0; i < NP; ++i) {
                     prm[t * TILE + 64 * i + lane] = s_of(cur.kp[t][i]);
                     prm[(2 * t + 2) * TILE + 64 * i + lane] = s_of(cur.vp[t][i]);
-                    prm[(2 * t + 3) * TILE + 64 * i + lane] = lo_of(cur.vp[t][i]);
+                    prm[(2 * t + 3) * TILE + 64 * i + lane] = mid_of(cur.vp[t][i]);
                 }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -595,24 +607,24 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 u32x4 hi, lo;
-                f32x4 vs[2], vlo[2];
+                f32x4 vs[2], vmid[2];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     vs[t] = *(const f32x4 *)&prm[(2 * t + 2) * TILE + 16 * g + 4 * h];
-                    vlo[t] = *(const f32x4 *)&prm[(2 * t + 3) * TILE + 16 * g + 4 * h];
+                    vmid[t] = *(const f32x4 *)&prm[(2 * t + 3) * TILE + 16 * g + 4 * h];
                 }
                 if (partial) {
                     // what lies at a key that the row does not see may be anything, NaN too
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        if (x[i / 4][i % 4] == -__builtin_inff()) vs[i / 4][i % 4] = vlo[i / 4][i % 4] = 0.0f;
+                        if (x[i / 4][i % 4] == -__builtin_inff()) vs[i / 4][i % 4] = vmid[i / 4][i % 4] = 0.0f;
                 }
 #pragma unroll
                 for (int i = 0; i < 8; i += 2) {
                     const float s0 = vs[i / 4][i % 4], s1 = vs[i / 4][i % 4 + 1];
                     const float p0 = p[i / 4][i % 4], p1 = p[i / 4][i % 4 + 1];
-                    z[g] = __builtin_fmaf(p0, vlo[i / 4][i % 4], z[g]);
-                    z[g] = __builtin_fmaf(p1, vlo[i / 4][i % 4 + 1], z[g]);
+                    z[g] = __builtin_fmaf(p0, vmid[i / 4][i % 4], z[g]);
+                    z[g] = __builtin_fmaf(p1, vmid[i / 4][i % 4 + 1], z[g]);
                     const f32x2 a2 = {p0 * s0, p1 * s1};
                     const f16x2 t = __builtin_convertvector(a2, f16x2);
                     const f32x2 b2 = {a2[0] - (float)t[0], a2[1] - (float)t[1]};
@@ -627,8 +639,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? (G == 32 ? 2
                     u32x4 va[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
-                        va[k] = u32x4{code_pair(cur.v[0][w], (c & 3) + k), code_pair(cur.v[0][w + 1], (c & 3) + k),
-                                      code_pair(cur.v[1][w], (c & 3) + k), code_pair(cur.v[1][w + 1], (c & 3) + k)};
+                        va[k] = u32x4{centred_pair(cur.v[0][w], (c & 3) + k), centred_pair(cur.v[0][w + 1], (c & 3) + k),
+                                      centred_pair(cur.v[1][w], (c & 3) + k), centred_pair(cur.v[1][w + 1], (c & 3) + k)};
                     o[c] = mfma(va[0], hi, o[c]);
                     o[c + 1] = mfma(va[1], hi, o[c + 1]);
                     o[c] = mfma(va[0], lo, o[c]);
@@ -707,8 +719,10 @@ constexpr int kKeys = 64;    // keys a turn
 // p s is off by 2^-12 of s n, which in a group with an outlier channel is many
 // times its other channels' values (one channel in 32 offset by 30: outputs off
 // by 5e-3, where the rounding to bf16 is 1.7e-3).  The second term costs a fifth
-// (2048 queries over 8192 keys 494 us, with one term 412); it is the residual of
-// the exact product, by a mixed multiply-add (as a difference of fp32: 520).
+// of the time (2048 queries over 8192 keys, all else alike: 494 us, with one term
+// 412); it is the residual of the exact product, by a mixed multiply-add (as a
+// difference of fp32: 520).  That call takes 505 us, 470 TFLOP/s: the vector units
+// are 61% busy, the matrix units 30%, LDS 42%, with two waves a SIMD.
 template <int D, int G, bool BF>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
 {
@@ -722,7 +736,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
         u32x4 k[NK], v[NV];
         u32x4 klo[4 * 64];                  // lo_operand of K
         float ks[4 * TILE];                 // K's s, in fp32 once for all rows
-        float vs[4 * TILE], vlo[4 * TILE];  // and V's
+        float vs[4 * TILE], vmid[4 * TILE];  // and V's
         float vtop[kKeys];                  // log2 of each key's largest s of V
     };
     extern __shared__ __align__(16) uint8_t lds_raw[];
@@ -809,7 +823,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
             const int w = 2 * (c / 4);
-            const u32x2 d = {code_pair(vw[w], c & 3), code_pair(vw[w + 1], c & 3)};
+            const u32x2 d = {centred_pair(vw[w], c & 3), centred_pair(vw[w + 1], c & 3)};
             *(u32x2 *)((uint8_t *)&to.v[((wave >> 1) * NT + c) * 64 + lane] + 8 * (wave & 1)) = d;
         }
         // what lies at keys that no row sees may be anything
@@ -823,7 +837,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
             const float s = in ? s_of(vp[i]) : 0.0f;
             s_top = fmaxf(s_top, s);
             to.vs[wave * TILE + 64 * i + lane] = s;
-            to.vlo[wave * TILE + 64 * i + lane] = in ? lo_of(vp[i]) : 0.0f;
+            to.vmid[wave * TILE + 64 * i + lane] = in ? mid_of(vp[i]) : 0.0f;
         }
         to.klo[wave * 64 + lane] = lo_operand<NG>(kp, h);
         to.vtop[16 * wave + col] = log2_top<NG>(s_top);
@@ -916,23 +930,23 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
 #pragma unroll
                     for (int j = 0; j < 2 * GS; ++j) {
                         const int g = g0 + j % GS, ct = j / GS;
-                        f32x4 vs[2], vlo[2];
+                        f32x4 vs[2], vmid[2];
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             vs[t] = *(const f32x4 *)&now.vs[(2 * half + t) * TILE + 16 * g + 4 * h];
-                            vlo[t] = *(const f32x4 *)&now.vlo[(2 * half + t) * TILE + 16 * g + 4 * h];
+                            vmid[t] = *(const f32x4 *)&now.vmid[(2 * half + t) * TILE + 16 * g + 4 * h];
                         }
                         if (partial) {
                             // a NaN there must not reach a row that does not see it
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
-                                if (x[ct][i / 4][i % 4] == -__builtin_inff()) vlo[i / 4][i % 4] = 0.0f;
+                                if (x[ct][i / 4][i % 4] == -__builtin_inff()) vmid[i / 4][i % 4] = 0.0f;
                         }
 #pragma unroll
                         for (int i = 0; i < 8; i += 2) {
                             const float s0 = vs[i / 4][i % 4], s1 = vs[i / 4][i % 4 + 1];
-                            z[ct][g] = __builtin_fmaf(p[ct][i], vlo[i / 4][i % 4], z[ct][g]);
-                            z[ct][g] = __builtin_fmaf(p[ct][i + 1], vlo[i / 4][i % 4 + 1], z[ct][g]);
+                            z[ct][g] = __builtin_fmaf(p[ct][i], vmid[i / 4][i % 4], z[ct][g]);
+                            z[ct][g] = __builtin_fmaf(p[ct][i + 1], vmid[i / 4][i % 4 + 1], z[ct][g]);
                             const f32x2 a2 = {p[ct][i] * s0, p[ct][i + 1] * s1};
                             const f16x2 t = __builtin_convertvector(a2, f16x2);
                             const f16x2 r = {(_Float16)__builtin_fmaf(p[ct][i], s0, -(float)t[0]),
@@ -1035,7 +1049,7 @@ __global__ __launch_bounds__(THREADS) void k_kv4_join(Kv4Attn a)
 
 // Heads of 256 in groups of 32 have no blocks of 128 rows: those spilled 226
 // registers a lane (512 queries over 4096 keys, 4 heads: 254 us, tiles of 16 rows
-// 248; 1024 over 8192, 8 heads: 1730 : 1338).
+// 246; 1024 over 8192, 8 heads: 1730 : 1361).
 constexpr bool has_prompt(int D, int G) { return D != 256 || G != 32; }
 
 template <int D, int G, bool BF>
@@ -1080,20 +1094,20 @@ hipError_t attend_dt(const Kv4Attn &a, bool bf16, hipStream_t s)
 // they are taken where every sequence may fill one, the keys are 2048 or more
 // and blocks and thousands of keys together occupy the chip (8 kv heads of
 // 128, R = 4, us a call with its join, this kernel : tiles of 16 rows: 2048
-// queries over 8192 keys 494 : 640, 2 x 512 over 4096 154 : 188, 8 x 32 over
-// 4096 58 : 73, 128 over 16000 100 : 117, 512 over 4096 with 4 heads of 256
-// 152 : 203; not for 1 x 64 over 4096 38 : 27, nor 1024 over 1024 50 : 42).
-// Split: two blocks a compute unit (2 x up to 512 over up to 4096, fp16, 160,
-// unsplit 219, in four 175), 512 keys or more each.
+// queries over 8192 keys 505 : 662, 2 x 512 over 4096 156 : 193, 8 x 32 over
+// 4096 57 : 73, 128 over 16000 101 : 118, 512 over 4096 with 4 heads of 256
+// 149 : 196; not for 1 x 64 over 4096 41 : 28, nor 1024 over 1024 55 : 43).
+// Split: two blocks a compute unit (2 x up to 512 over up to 4096, fp16, in two
+// 155, unsplit 212, in eight 187), 512 keys or more each.
 //
 // Tiles of 16 rows: a split costs a block's start and its part of the join, so
-// 512 keys or fewer are not split (1 x 300 keys 9.7 us, in two 11.0), else it
+// 512 keys or fewer are not split (1 x 300 keys 9.2 us, in two 10.9), else it
 // gets at least 256 keys while the blocks are fewer than the compute units,
 // 512 up to two blocks a unit (D = 256: a unit holds one), 1024 beyond, up to
 // eight a unit, which even out unequal sequences (us a call, this rule against
-// its neighbours: 1 x 4000 keys 11.7, in 8 14.8, in 64 14.3; 1 x 16000 15.4, in
-// 16 19.5, in 64 16.8; 64 x up to 8192 102, unsplit 110, in 8 112; 64 x up to
-// 1000 21, in two 28).  Fewer than four blocks a unit are rounded down to as
+// its neighbours: 1 x 4000 keys 11.7, in 8 14.7, in 64 14.2; 1 x 16000 15.2, in
+// 16 18.8, in 64 16.5; 64 x up to 8192 93, unsplit 106, in 8 99; 64 x up to
+// 1000 20, in two 27).  Fewer than four blocks a unit are rounded down to as
 // many on every unit where that takes no more than a quarter of them (1 x 80000
 // on 8 heads, 79 ways 36, 64 ways 32).
 namespace {

@@ -501,7 +501,9 @@ int kvc_kv4_read(const kvc_kv4_desc *desc, const uint8_t *codes, const uint16_t 
  *   x_j = scale * q.k_j  (softcap > 0: softcap * tanh(x_j / softcap)),
  *   out = sum_j softmax(x)_j v_j,  lse = ln sum_j exp(x_j).
  * A row without a key gives out = 0, lse = -inf.  Logits, maxima, sums and
- * accumulators are fp32; out is rounded once.
+ * accumulators are fp32; a probability times a group's s has 22 bits of the
+ * row's largest such product (in a token with groups whose s differ by more
+ * than 2^10, fewer for the smaller ones by as much); out is rounded once.
  */
 typedef struct kvc_kv4_attn {
     const void *q;             /* [n_q][n_q_heads][D] of dtype (KVC_F16 or KVC_BF16), channels contiguous */

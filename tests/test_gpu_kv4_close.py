@@ -118,3 +118,39 @@ def test_one_key_a_row(H, D, G, P, dt, room):
     got, gl, wo, wl, smax = run(H, D, G, P, [333, 64, 1], [150, 64, 1], 3, dt, room, window=1)
     assert (np.abs(got - wo) <= kv4_close.STEP[dt] / 2 * np.abs(wo) + 2.0 ** -18 * smax).all()
     assert kv4_close.lse_off(gl, wl) <= 1
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("D,G", [(64, 64), (128, 64), (256, 128)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_rounding_errors_do_not_add_up_over_many_keys(dt, D, G, wide):
+    """20000 keys in one split, V of either sign: outputs are averages a hundred times smaller than what is summed.  A
+    sum of N terms of either sign, rounded to fp32 at every step of 32, is off by about 2^-24 sqrt(N / 32) of itself,
+    2^-19.4; with the logits' share and the two terms' as in kv4_close, of which most averages out: 2^-16 of |out|, in
+    the mean, beyond the rounding, and four steps."""
+    import torch
+    say(f"[gpu] kv4 close 20000 keys {dt} D={D} G={G} wide={wide}")
+    T, P, H, R, B, nq = 20000, 64, 8, 4, 64 if wide else 256, 32 if wide else 1
+    n = -(-T // P)
+    cache, ref = kvc.Kv4Cache(H, D, n, page_tokens=P, group=G), kv4_ref.Pool(2, D, G, P, n)  # two heads are looked at
+    g = torch.Generator().manual_seed(21)
+    t = {"bf16": torch.bfloat16, "f16": torch.float16}[dt]
+    k, v, q = (torch.randn(s, generator=g).to(t) for s in ((T, H, D), (T, H, D), (nq, H * R, D)))
+    slots = np.arange(T)
+    kvc.kv4_append(cache, k.cuda(), v.cuda(), torch.from_numpy(slots).cuda())
+    # as many sequences as leave no call for splits, all over the same pages with the same queries
+    table = torch.arange(n, dtype=torch.int32).repeat(B, 1).cuda()
+    lens = torch.full((B,), T, dtype=torch.int32).cuda()
+    assert kvc.kv4_work_bytes(cache, B * nq, H * R, B, n, nq) == 0
+    out, lse = kvc.kv4_attention(cache, q.repeat(B, 1, 1).cuda(), table, lens, return_lse=True)
+    assert status(cache) == 0
+    ref.write(f32(k[:, :2]), f32(v[:, :2]), slots)
+    got, gl = out[:nq, :2 * R].double().cpu().numpy(), lse[:nq, :2 * R].double().cpu().numpy()
+    wo, wl = np.zeros_like(got), np.zeros_like(gl)
+    for h in range(2):
+        hs = slice(h * R, (h + 1) * R)
+        wo[:, hs], wl[:, hs] = kv4_ref.attention(q[:, hs].double().numpy(), ref.value(0, slots)[:, h], ref.value(1, slots)[:, h],
+                                                 T - nq + np.arange(nq), T, True, 0, 0.0, D ** -0.5)
+    off = np.abs(got - kv4_close.rounded(wo, dt)).sum()
+    assert off <= 2.0 ** -16 * np.abs(wo).sum() + 4 * kv4_close.STEP[dt] * np.abs(wo).max()
+    assert kv4_close.lse_off(gl, wl) <= 1
