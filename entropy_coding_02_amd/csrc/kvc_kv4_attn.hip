@@ -721,8 +721,8 @@ constexpr int kKeys = 64;    // keys a turn
 // by 5e-3, where the rounding to bf16 is 1.7e-3).  The second term costs a fifth
 // of the time (2048 queries over 8192 keys, all else alike: 494 us, with one term
 // 412); it is the residual of the exact product, by a mixed multiply-add (as a
-// difference of fp32: 520).  That call takes 505 us, 470 TFLOP/s: the vector units
-// are 61% busy, the matrix units 30%, LDS 42%, with two waves a SIMD.
+// difference of fp32: 520).  That call takes 504 us, 475 TFLOP/s: the vector units
+// are 60% busy, the matrix units 30%, LDS 42%, with two waves a SIMD.
 template <int D, int G, bool BF>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
 {
@@ -1074,7 +1074,7 @@ hipError_t attend(const Kv4Attn &a, hipStream_t s)
         if (a.ns <= 8)
             k_kv4_join<D, BF, 64><<<rows, dim3(64), 0, s>>>(a);
         else
-            k_kv4_join<D, BF, 512><<<rows, dim3(512), 0, s>>>(a);  // 64 splits of 64 rows: 4.2 us; 79, 4.9, by 256 threads 6.5
+            k_kv4_join<D, BF, 512><<<rows, dim3(512), 0, s>>>(a);  // 64 splits of 64 rows: 4.7 us; 79 by 256 threads a third longer
         e = hipGetLastError();
     }
     return e;
@@ -1108,8 +1108,9 @@ hipError_t attend_dt(const Kv4Attn &a, bool bf16, hipStream_t s)
 // its neighbours: 1 x 4000 keys 11.7, in 8 14.7, in 64 14.2; 1 x 16000 15.2, in
 // 16 18.8, in 64 16.5; 64 x up to 8192 93, unsplit 106, in 8 99; 64 x up to
 // 1000 20, in two 27).  Fewer than four blocks a unit are rounded down to as
-// many on every unit where that takes no more than a quarter of them (1 x 80000
-// on 8 heads, 79 ways 36, 64 ways 32).
+// many on every unit where that takes no more than a quarter of them (on 8
+// heads 1 x 80000, 79 ways 35, 64 ways 32; 1 x 100000, 98 ways 43, 96 ways 37;
+// 2 x 40000, 40 ways 33, 32 ways 30).
 namespace {
 
 int64_t prompt_splits(const Kv4Pool &p, int64_t blocks, int64_t keys)
