@@ -34,6 +34,7 @@ EXPORTED = (
     "kvc_stream_work_bytes", "kvc_stream_encode",
     "kvc_kv4_codes_bytes", "kvc_kv4_params_bytes", "kvc_kv4_append", "kvc_kv4_read",
     "kvc_kv4_work_bytes", "kvc_kv4_attention",
+    "kvc_kv4_append_rotated", "kvc_kv4_tree_work_bytes", "kvc_kv4_tree_attention", "kvc_kv4_keep",
 )
 KVC_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -73,6 +74,14 @@ class KvcKv4Attn(ctypes.Structure):
         ("softcap", ctypes.c_float), ("scale", ctypes.c_float),
         ("work", ctypes.c_void_p), ("work_bytes", ctypes.c_int64),
     ]
+
+
+class KvcKv4Rotated(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "q", "q_out")] +
+                [(f"{n}_{x}_stride", ctypes.c_int64) for n in ("k", "v", "q", "q_out") for x in ("token", "head")] +
+                [(n, ctypes.c_void_p) for n in ("slots", "positions", "table")] +
+                [(n, ctypes.c_int64) for n in ("n_tokens", "n_positions")] +
+                [(n, ctypes.c_int32) for n in ("n_q_heads", "rot", "interleaved", "dtype")])
 
 
 # void on_chunk(void *user, int64_t chunk, int32_t level, const uint8_t *container, int64_t n_bytes)
@@ -161,6 +170,14 @@ def _load():
         lib.kvc_kv4_work_bytes.argtypes = [K, I64, I32, I32, I32, I32]
         lib.kvc_kv4_attention.restype = ctypes.c_int
         lib.kvc_kv4_attention.argtypes = [K, P, P, P, P, P]  # the kvc_kv4_attn as bytes or a reference
+        lib.kvc_kv4_append_rotated.restype = ctypes.c_int
+        lib.kvc_kv4_append_rotated.argtypes = [K, P, P, P, P, P]  # the kvc_kv4_rotated as bytes or a reference
+        lib.kvc_kv4_tree_work_bytes.restype = I64
+        lib.kvc_kv4_tree_work_bytes.argtypes = [K, I64, I32, I32, I32, I32]
+        lib.kvc_kv4_tree_attention.restype = ctypes.c_int
+        lib.kvc_kv4_tree_attention.argtypes = [K, P, P, P, P, P, P]
+        lib.kvc_kv4_keep.restype = ctypes.c_int
+        lib.kvc_kv4_keep.argtypes = [K, P, I32, P, I64, I32, P, P, I64, I32, P, I32, P, P]
         _lib = lib
     return _lib
 
@@ -465,6 +482,7 @@ class Kv4Cache:
         self.ref = ctypes.byref(self.c)
         self.n_kv_heads, self.head_dim, self.group = n_kv_heads, head_dim, group
         self.page_tokens, self.n_pages = page_tokens, n_pages
+        self.geometry = n_kv_heads, head_dim, group, page_tokens, n_pages
         self.int32, self.int64, self.float32 = torch.int32, torch.int64, torch.float32
         self._want = {}  # type and bytes of a buffer
         for name, dt in (("codes", torch.uint8), ("params", torch.float16)):
@@ -524,6 +542,7 @@ class Kv4Cache:
 
 _KV4_DTYPES = {}  # torch.dtype -> KVC_* (filled on first use: torch is imported late)
 _ATTN = struct.Struct("@PPPqqqqPqPPqiiiiiiiffPq")  # kvc_kv4_attn, field by field as KvcKv4Attn
+_ROTATED = struct.Struct("@PPPPqqqqqqqqPPPqqiiii")  # kvc_kv4_rotated, as KvcKv4Rotated
 _RAW_STREAM = _CURRENT_DEVICE = None
 
 
@@ -639,13 +658,17 @@ def kv4_read(cache: Kv4Cache, slots, dtype=None, k=None, v=None, stream=None):
     return k, v
 
 
+def _work_bytes(name, cache, n_q, n_q_heads, n_seqs, max_pages, max_q):
+    v = int(getattr(_load(), name)(cache.ref, n_q, n_seqs, n_q_heads, max_pages, max_q))
+    if v < 0:
+        raise KvcError(name, v)
+    return v
+
+
 def kv4_work_bytes(cache: Kv4Cache, n_q: int, n_q_heads: int, n_seqs: int, max_pages: int, max_q: int) -> int:
     """Workspace of a kv4_attention call: n_q query tokens in all, at most
     max_q of one sequence, page tables of max_pages entries."""
-    v = int(_load().kvc_kv4_work_bytes(cache.ref, n_q, n_seqs, n_q_heads, max_pages, max_q))
-    if v < 0:
-        raise KvcError("kvc_kv4_work_bytes", v)
-    return v
+    return _work_bytes("kvc_kv4_work_bytes", cache, n_q, n_q_heads, n_seqs, max_pages, max_q)
 
 
 def kv4_attention(cache: Kv4Cache, q, page_table, kv_len, cu_q=None, max_q: Optional[int] = None, causal: bool = True,
@@ -659,6 +682,13 @@ def kv4_attention(cache: Kv4Cache, q, page_table, kv_len, cu_q=None, max_q: Opti
     sequence has n_q / B.  `work`: uint8 of kv4_work_bytes, allocated if not
     given.  What is allocated here belongs to `stream` (the current one if not
     given).  Returns out, or (out, lse float32 [n_q][Hq])."""
+    return _attend("kvc_kv4_attention", "kvc_kv4_work_bytes", cache, q, page_table, kv_len, cu_q, max_q, causal, window,
+                   softcap, scale, out, return_lse, lse, work, stream, None)
+
+
+def _attend(name, work_name, cache, q, page_table, kv_len, cu_q, max_q, causal, window, softcap, scale, out, return_lse,
+            lse, work, stream, parents):
+    """A call of kvc_kv4_attention, or with parents of kvc_kv4_tree_attention."""
     if q.dim() != 3 or page_table.dim() != 2:
         raise ValueError("kvc: q must be [n_q][Hq][D], page_table [B][max_pages]")
     n_q, n_heads, _ = q.shape
@@ -686,7 +716,7 @@ def kv4_attention(cache: Kv4Cache, q, page_table, kv_len, cu_q=None, max_q: Opti
     elif return_lse:
         lse = q.new_empty(shape[:2], dtype=f32) if stream is None else _kv4_empty(stream, q, shape[:2], f32)
     if work is None:
-        nb = kv4_work_bytes(cache, n_q, n_heads, B, max_pages, max_q)
+        nb = _work_bytes(work_name, cache, n_q, n_heads, B, max_pages, max_q)
         work = _kv4_empty(stream, q, (nb,), cache.codes.dtype) if nb else None
     elif work.get_device() != dev:
         raise _wrong_device("work", work)
@@ -699,7 +729,108 @@ def kv4_attention(cache: Kv4Cache, q, page_table, kv_len, cu_q=None, max_q: Opti
         n_q, B, n_heads, max_pages, max_q, _kv4_dtype(dtype), bool(causal), window, softcap,
         cache.head_dim ** -0.5 if scale is None else scale, 0 if work is None else _ptr(work),
         0 if work is None else work.numel() * work.element_size())
-    rc = _kv4_call(_load().kvc_kv4_attention, cache, stream, args, cache.codes_ptr, cache.params_ptr, cache.status_ptr)
+    tree = () if parents is None else (_ints("parents", parents, i32, (n_q,), dev),)
+    rc = _kv4_call(getattr(_load(), name), cache, stream, args, *tree, cache.codes_ptr, cache.params_ptr, cache.status_ptr)
     if rc:
-        raise KvcError("kvc_kv4_attention", rc)
+        raise KvcError(name, rc)
     return (out, lse) if return_lse else out
+
+
+# ------------------------------------------- speculative decoding from the cache
+
+def kv4_append_rotated(cache: Kv4Cache, k, v, slots, positions, table, q=None, q_out=None, interleaved: bool = False,
+                       stream=None):
+    """kv4_append with k turned by the rotation of its tokens' positions on the
+    way, and q [T][Hq][D] too, into q_out (allocated if not given; q itself: in
+    place).  positions int64 [T] (negative: the token is skipped); table float32
+    [n_positions][rot]: rot/2 cosines, then rot/2 sines of each position's angles, usually
+    position * base ** (-2 i / rot) computed in 64 bits; the first rot channels of a head
+    are turned, as pairs (i, i + rot/2), or (2i, 2i + 1) if interleaved.  What is
+    allocated here belongs to `stream` (the current one if not given).
+    Returns q_out (None without q)."""
+    n, dev, dtype = k.shape[0], cache.device_index, k.dtype
+    if v.dtype != dtype or (q is not None and q.dtype != dtype) or (q_out is not None and q_out.dtype != dtype):
+        raise ValueError("kvc: k, v, q and q_out must have one dtype")
+    if q is None and q_out is not None:
+        raise ValueError("kvc: q_out without q")
+    shape = (n, cache.n_kv_heads, cache.head_dim)
+    kp, kts, khs = _rows("k", k, shape, dev)
+    vp, vts, vhs = _rows("v", v, shape, dev)
+    if table.dim() != 2:
+        raise ValueError("kvc: table must be float32 [n_positions][rot]")
+    qp = qts = qhs = op = ots = ohs = heads = 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("kvc: q must be [T][Hq][D]")
+        heads = q.shape[1]
+        shape = (n, heads, cache.head_dim)
+        qp, qts, qhs = _rows("q", q, shape, dev)
+        if q_out is None:
+            q_out = q.new_empty(shape) if stream is None else _kv4_empty(stream, q, shape, dtype)
+        op, ots, ohs = _rows("q_out", q_out, shape, dev, True)
+        if not heads or not n:
+            qp = op = 0  # nothing to turn
+    args = _ROTATED.pack(kp, vp, qp, op, kts, khs, vts, vhs, qts, qhs, ots, ohs,
+                         _ints("slots", slots, cache.int64, (n,), dev), _ints("positions", positions, cache.int64, (n,), dev),
+                         _ints("table", table, cache.float32, table.shape, dev), n, table.shape[0], heads, table.shape[1],
+                         bool(interleaved), _kv4_dtype(dtype))
+    rc = _kv4_call(_load().kvc_kv4_append_rotated, cache, stream, args, cache.codes_ptr, cache.params_ptr, cache.status_ptr)
+    if rc:
+        raise KvcError("kvc_kv4_append_rotated", rc)
+    return q_out
+
+
+def kv4_tree_work_bytes(cache: Kv4Cache, n_q: int, n_q_heads: int, n_seqs: int, max_pages: int, max_q: int) -> int:
+    """Workspace of a kv4_tree_attention call, as kv4_work_bytes."""
+    return _work_bytes("kvc_kv4_tree_work_bytes", cache, n_q, n_q_heads, n_seqs, max_pages, max_q)
+
+
+def kv4_tree_attention(cache: Kv4Cache, q, page_table, kv_len, parents, cu_q=None, max_q: Optional[int] = None,
+                       window: int = 0, softcap: float = 0.0, scale: Optional[float] = None, out=None,
+                       return_lse: bool = False, lse=None, work=None, stream=None):
+    """Attention of a tree of drafted tokens: q [n_q][Hq][D] are the queries of
+    the tokens whose keys are each sequence's last cached ones (kv_len counts them),
+    parents int32 [n_q] the drafted token that each follows (its index within
+    its own sequence's, smaller than the token's; -1: the last token before the tree).  A token sees
+    the keys before the tree, its ancestors and itself.  At most 1024 tokens a
+    tree (max_q, which has to be given where n_q is more); workspace of
+    kv4_tree_work_bytes; all else as kv4_attention."""
+    return _attend("kvc_kv4_tree_attention", "kvc_kv4_tree_work_bytes", cache, q, page_table, kv_len, cu_q, max_q, True, window,
+                   softcap, scale, out, return_lse, lse, work, stream, parents)
+
+
+def kv4_keep(caches, page_table, base, path, n_keep, stream=None):
+    """Keep the accepted path of each sequence's tree in `caches` (a Kv4Cache, or
+    the layers' caches of one geometry, which share the page table): token
+    base[b] + i becomes what token base[b] + path[b][i] was, for i < n_keep[b].
+    page_table int32 [B][max_pages]; base and n_keep int32 [B]; path int32
+    [B][max_path], rising.  Device findings go to the first cache's dev_status."""
+    if isinstance(caches, Kv4Cache):
+        caches = (caches,)
+    if not caches:
+        raise ValueError("kvc: no cache to keep tokens in")
+    first = caches[0]
+    dev, i32 = first.device_index, first.int32
+    pools = []
+    for c in caches:
+        if c.geometry != first.geometry:
+            raise ValueError("kvc: the caches must be of one geometry")
+        if c.device_index != dev:
+            raise ValueError("kvc: the caches must be on one device")
+        pools += c.codes_ptr, c.params_ptr
+    if len(set(pools)) != len(pools):
+        raise ValueError("kvc: a cache is given twice")
+    if page_table.dim() != 2 or path.dim() != 2:
+        raise ValueError("kvc: page_table must be [B][max_pages], path [B][max_path]")
+    B, max_pages = page_table.shape
+    max_path = path.shape[1]
+    for name, t in (("page_table", page_table), ("path", path)):
+        if t.dtype != i32 or t.shape[0] != B or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"kvc: {name} must be a device int32 tensor with a contiguous row for each sequence")
+        if t.get_device() != dev:
+            raise _wrong_device(name, t)
+    rc = _kv4_call(_load().kvc_kv4_keep, first, stream, struct.pack(f"@{len(pools)}P", *pools), len(caches),
+                   page_table.data_ptr(), page_table.stride(0), max_pages, _ints("base", base, i32, (B,), dev),
+                   path.data_ptr(), path.stride(0), max_path, _ints("n_keep", n_keep, i32, (B,), dev), B, first.status_ptr)
+    if rc:
+        raise KvcError("kvc_kv4_keep", rc)

@@ -235,6 +235,84 @@ bool host_pinned(const void *ptr)
 
 int launch_status(hipError_t e) { return e == hipSuccess ? KVC_OK : KVC_ERR_HIP; }
 
+// Workspace of a call that is planned by `plan_of`.
+int64_t kv4_work(const kvc_kv4_desc *desc, decltype(&kv4_plan) plan_of, int64_t n_q, int32_t n_seqs, int32_t n_q_heads,
+                 int32_t max_pages, int32_t max_q)
+{
+    Kv4Pool p;
+    const int rc = make_pool(desc, p);
+    if (rc != KVC_OK) return rc;
+    if (!kv4_attn_sizes(p, n_q, n_seqs, n_q_heads, max_pages, max_q)) return KVC_ERR_ARG;
+    const Kv4Plan plan = plan_of(p, n_seqs, n_q_heads / p.H, max_q, (int64_t)max_pages << p.pshift, 0);
+    return plan.most_ns > 1 ? plan.most_ns * n_q * n_q_heads * (p.D + 2) * 4 : 0;
+}
+
+// kvc_kv4_attention, and with `tree` kvc_kv4_tree_attention.
+int kv4_attend(const kvc_kv4_desc *desc, const kvc_kv4_attn *args, bool tree, const int32_t *parents, const uint8_t *codes,
+               const uint16_t *params, int32_t *dev_status, void *stream)
+{
+    Kv4Attn a;
+    memset(&a, 0, sizeof(a));
+    const int rc = make_pool(desc, a.pool);
+    if (rc != KVC_OK) return rc;
+    if (!args || !kv4_attn_sizes(a.pool, args->n_q, args->n_seqs, args->n_q_heads, args->max_pages, args->max_q))
+        return KVC_ERR_ARG;
+    if ((args->dtype != KVC_F16 && args->dtype != KVC_BF16) || args->window < 0 || (args->window && !args->causal) ||
+        !(args->softcap >= 0.0f) || args->softcap > 3.0e38f || !(args->scale == args->scale) ||
+        args->scale > 1.0e37f || args->scale < -1.0e37f)
+        return KVC_ERR_ARG;
+    if (tree && (args->causal != 1 || args->max_q > kTreeMost)) return KVC_ERR_ARG;
+    if (args->n_q == 0 || args->n_seqs == 0 || args->max_q == 0) return KVC_OK;
+    if (!args->q || !args->out || !args->kv_len || !codes || !params || (!args->page_table && args->max_pages) ||
+        !aligned(args->q, 2) || !aligned(args->out, 2) || !aligned(args->lse, 4) || !aligned(args->kv_len, 4) ||
+        !aligned(args->page_table, 4) || !aligned(args->cu_q, 4) || !aligned(codes, 16) || !aligned(params, 16) ||
+        (dev_status && !aligned(dev_status, 4)) || (tree && (!parents || !aligned(parents, 4))))
+        return KVC_ERR_ARG;
+    if (!args->cu_q && (int64_t)args->n_seqs * args->max_q != args->n_q) return KVC_ERR_ARG;
+    const int64_t most_keys = (int64_t)args->max_pages << a.pool.pshift;
+    a.window = args->window >= most_keys ? 0 : args->window;  // one that reaches past every key is none
+    const auto plan_of = tree ? kv4_tree_plan : kv4_plan;
+    const Kv4Plan plan = plan_of(a.pool, args->n_seqs, args->n_q_heads / a.pool.H, args->max_q, most_keys, a.window);
+    const int64_t part = plan.ns > 1 ? plan.ns * args->n_q * args->n_q_heads : 0;
+    if (part) {
+        if (!args->work || !aligned(args->work, 16)) return KVC_ERR_ARG;
+        if (args->work_bytes < part * (a.pool.D + 2) * 4) return KVC_ERR_CAPACITY;
+        a.part_o = (float *)args->work;
+        a.part_ml = a.part_o + part * a.pool.D;
+    }
+    a.pool.codes = (uint8_t *)codes;
+    a.pool.params = (uint32_t *)params;
+    a.pool.status = dev_status;
+    a.q = (const uint16_t *)args->q;
+    a.out = (uint16_t *)args->out;
+    a.lse = args->lse;
+    a.q_ts = args->q_token_stride;
+    a.q_hs = args->q_head_stride;
+    a.o_ts = args->out_token_stride;
+    a.o_hs = args->out_head_stride;
+    a.q_vec = aligned(a.q, 16) && a.q_ts % 8 == 0 && a.q_hs % 8 == 0;
+    a.o_vec = aligned(a.out, 8) && a.o_ts % 4 == 0 && a.o_hs % 4 == 0;
+    a.table = args->page_table;
+    a.table_stride = args->table_stride;
+    a.kv_len = args->kv_len;
+    a.cu_q = args->cu_q;
+    a.n_q = args->n_q;
+    a.B = args->n_seqs;
+    a.Hq = args->n_q_heads;
+    a.R = args->n_q_heads / a.pool.H;
+    a.max_pages = args->max_pages;
+    a.max_q = args->max_q;
+    a.causal = args->causal != 0;
+    a.softcap = args->softcap;
+    a.scale = args->scale;
+    a.ns = plan.ns;
+    a.tiles = plan.tiles;
+    a.prompt = plan.prompt;
+    a.parents = parents;
+    const auto launch = tree ? launch_kv4_tree : launch_kv4_attention;
+    return launch_status(launch(a, args->dtype == KVC_BF16, (hipStream_t)stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -779,6 +857,91 @@ int kvc_kv4_append(const kvc_kv4_desc *desc, const void *k, const void *v, int64
     return launch_status(launch_kv4_append(p, kr, vr, n_tokens, dtype, slots, (hipStream_t)stream));
 }
 
+int kvc_kv4_append_rotated(const kvc_kv4_desc *desc, const kvc_kv4_rotated *args, uint8_t *codes, uint16_t *params,
+                           int32_t *dev_status, void *stream)
+{
+    Kv4Pool p;
+    const int rc = make_pool(desc, p);
+    if (rc != KVC_OK) return rc;
+    if (!args || !kv4_dtype(args->dtype) || args->n_tokens < 0 || args->n_tokens > ((int64_t)1 << 40) || args->rot < 16 ||
+        args->rot > p.D || args->rot % 16 || args->n_positions < 0 || args->n_positions > ((int64_t)1 << 40) ||
+        (args->q && (args->n_q_heads < 1 || args->n_q_heads > 65536)))
+        return KVC_ERR_ARG;
+    if (args->n_tokens == 0) return KVC_OK;
+    Kv4Rows kr, vr;
+    Kv4Turn turn;
+    memset(&turn, 0, sizeof(turn));
+    const int32_t dt = args->dtype;
+    if (!args->k || !args->v || !args->slots || !args->positions || (!args->table && args->n_positions) || !codes || !params ||
+        !aligned(args->slots, 8) || !aligned(args->positions, 8) || !aligned(args->table, 16) || !aligned(codes, 16) ||
+        !aligned(params, 16) || (dev_status && !aligned(dev_status, 4)) || !args->q != !args->q_out ||
+        !make_rows(kr, args->k, nullptr, args->k_token_stride, args->k_head_stride, dt) ||
+        !make_rows(vr, args->v, nullptr, args->v_token_stride, args->v_head_stride, dt))
+        return KVC_ERR_ARG;
+    if (args->q) {
+        Kv4Rows out;
+        if (!make_rows(turn.q, args->q, nullptr, args->q_token_stride, args->q_head_stride, dt) ||
+            !make_rows(out, nullptr, args->q_out, args->q_out_token_stride, args->q_out_head_stride, dt))
+            return KVC_ERR_ARG;
+        // in place or apart
+        if (args->q == args->q_out && (out.token_stride != turn.q.token_stride || out.head_stride != turn.q.head_stride))
+            return KVC_ERR_ARG;
+        turn.q.dst = args->q_out;
+        turn.out_token_stride = out.token_stride;
+        turn.out_head_stride = out.head_stride;
+        turn.out_vec = out.vec;
+        turn.Hq = args->n_q_heads;
+    }
+    turn.table = args->table;
+    turn.positions = args->positions;
+    turn.n_positions = args->n_positions;
+    turn.rot = args->rot;
+    turn.interleaved = args->interleaved != 0;
+    p.codes = codes;
+    p.params = (uint32_t *)params;
+    p.status = dev_status;
+    return launch_status(launch_kv4_append_rotated(p, kr, vr, turn, args->n_tokens, dt, args->slots, (hipStream_t)stream));
+}
+
+int kvc_kv4_keep(const kvc_kv4_desc *desc, const kvc_kv4_pool *pools, int32_t n_pools, const int32_t *page_table,
+                 int64_t table_stride, int32_t max_pages, const int32_t *base, const int32_t *path, int64_t path_stride,
+                 int32_t max_path, const int32_t *n_keep, int32_t n_seqs, int32_t *dev_status, void *stream)
+{
+    Kv4Keep a;
+    memset(&a, 0, sizeof(a));
+    const int rc = make_pool(desc, a.pool);
+    if (rc != KVC_OK) return rc;
+    const int64_t rows = (int64_t)n_seqs * a.pool.H;  // a wave each in every pool
+    if (n_pools < 0 || n_seqs < 0 || rows >= (1 << 24) || max_pages < 0 || max_path < 0 ||
+        ((int64_t)max_pages << a.pool.pshift) > ((int64_t)1 << 30) || max_path > (1 << 30))
+        return KVC_ERR_ARG;
+    if (n_pools == 0 || n_seqs == 0) return KVC_OK;
+    if (!pools || !base || !n_keep || (!path && max_path) || (!page_table && max_pages) || !aligned(base, 4) ||
+        !aligned(n_keep, 4) || !aligned(path, 4) || !aligned(page_table, 4) || (dev_status && !aligned(dev_status, 4)))
+        return KVC_ERR_ARG;
+    for (int i = 0; i < n_pools; ++i)
+        if (!pools[i].codes || !pools[i].params || !aligned(pools[i].codes, 16) || !aligned(pools[i].params, 16))
+            return KVC_ERR_ARG;
+    a.pool.status = dev_status;
+    a.table = page_table;
+    a.table_stride = table_stride;
+    a.base = base;
+    a.path = path;
+    a.n_keep = n_keep;
+    a.path_stride = path_stride;
+    a.B = n_seqs;
+    a.max_path = max_path;
+    a.max_pages = max_pages;
+    const int32_t most = (int32_t)std::min<int64_t>(kKeepPools, (1 << 25) / rows);  // fewer than 2^32 threads a launch
+    for (int32_t i = 0; i < n_pools; i += most) {
+        a.n_pools = std::min(n_pools - i, most);
+        for (int j = 0; j < a.n_pools; ++j) a.pools[j] = pools[i + j];
+        const int st = launch_status(launch_kv4_keep(a, (hipStream_t)stream));
+        if (st != KVC_OK) return st;
+    }
+    return KVC_OK;
+}
+
 int kvc_kv4_read(const kvc_kv4_desc *desc, const uint8_t *codes, const uint16_t *params,
                  const int64_t *slots, int64_t n_tokens, void *k, void *v, int64_t k_token_stride,
                  int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
@@ -804,73 +967,26 @@ int kvc_kv4_read(const kvc_kv4_desc *desc, const uint8_t *codes, const uint16_t 
 int64_t kvc_kv4_work_bytes(const kvc_kv4_desc *desc, int64_t n_q, int32_t n_seqs, int32_t n_q_heads,
                            int32_t max_pages, int32_t max_q)
 {
-    Kv4Pool p;
-    const int rc = make_pool(desc, p);
-    if (rc != KVC_OK) return rc;
-    if (!kv4_attn_sizes(p, n_q, n_seqs, n_q_heads, max_pages, max_q)) return KVC_ERR_ARG;
-    const Kv4Plan plan = kv4_plan(p, n_seqs, n_q_heads / p.H, max_q, (int64_t)max_pages << p.pshift, 0);
-    return plan.most_ns > 1 ? plan.most_ns * n_q * n_q_heads * (p.D + 2) * 4 : 0;
+    return kv4_work(desc, kv4_plan, n_q, n_seqs, n_q_heads, max_pages, max_q);
 }
 
 int kvc_kv4_attention(const kvc_kv4_desc *desc, const kvc_kv4_attn *args, const uint8_t *codes,
                       const uint16_t *params, int32_t *dev_status, void *stream)
 {
-    Kv4Attn a;
-    memset(&a, 0, sizeof(a));
-    const int rc = make_pool(desc, a.pool);
-    if (rc != KVC_OK) return rc;
-    if (!args || !kv4_attn_sizes(a.pool, args->n_q, args->n_seqs, args->n_q_heads, args->max_pages, args->max_q))
-        return KVC_ERR_ARG;
-    if ((args->dtype != KVC_F16 && args->dtype != KVC_BF16) || args->window < 0 || (args->window && !args->causal) ||
-        !(args->softcap >= 0.0f) || args->softcap > 3.0e38f || !(args->scale == args->scale) ||
-        args->scale > 1.0e37f || args->scale < -1.0e37f)
-        return KVC_ERR_ARG;
-    if (args->n_q == 0 || args->n_seqs == 0 || args->max_q == 0) return KVC_OK;
-    if (!args->q || !args->out || !args->kv_len || !codes || !params || (!args->page_table && args->max_pages) ||
-        !aligned(args->q, 2) || !aligned(args->out, 2) || !aligned(args->lse, 4) || !aligned(args->kv_len, 4) ||
-        !aligned(args->page_table, 4) || !aligned(args->cu_q, 4) || !aligned(codes, 16) || !aligned(params, 16) ||
-        (dev_status && !aligned(dev_status, 4)))
-        return KVC_ERR_ARG;
-    if (!args->cu_q && (int64_t)args->n_seqs * args->max_q != args->n_q) return KVC_ERR_ARG;
-    const int64_t most_keys = (int64_t)args->max_pages << a.pool.pshift;
-    a.window = args->window >= most_keys ? 0 : args->window;  // one that reaches past every key is none
-    const Kv4Plan plan = kv4_plan(a.pool, args->n_seqs, args->n_q_heads / a.pool.H, args->max_q, most_keys, a.window);
-    const int64_t part = plan.ns > 1 ? plan.ns * args->n_q * args->n_q_heads : 0;
-    if (part) {
-        if (!args->work || !aligned(args->work, 16)) return KVC_ERR_ARG;
-        if (args->work_bytes < part * (a.pool.D + 2) * 4) return KVC_ERR_CAPACITY;
-        a.part_o = (float *)args->work;
-        a.part_ml = a.part_o + part * a.pool.D;
-    }
-    a.pool.codes = (uint8_t *)codes;
-    a.pool.params = (uint32_t *)params;
-    a.pool.status = dev_status;
-    a.q = (const uint16_t *)args->q;
-    a.out = (uint16_t *)args->out;
-    a.lse = args->lse;
-    a.q_ts = args->q_token_stride;
-    a.q_hs = args->q_head_stride;
-    a.o_ts = args->out_token_stride;
-    a.o_hs = args->out_head_stride;
-    a.q_vec = aligned(a.q, 16) && a.q_ts % 8 == 0 && a.q_hs % 8 == 0;
-    a.o_vec = aligned(a.out, 8) && a.o_ts % 4 == 0 && a.o_hs % 4 == 0;
-    a.table = args->page_table;
-    a.table_stride = args->table_stride;
-    a.kv_len = args->kv_len;
-    a.cu_q = args->cu_q;
-    a.n_q = args->n_q;
-    a.B = args->n_seqs;
-    a.Hq = args->n_q_heads;
-    a.R = args->n_q_heads / a.pool.H;
-    a.max_pages = args->max_pages;
-    a.max_q = args->max_q;
-    a.causal = args->causal != 0;
-    a.softcap = args->softcap;
-    a.scale = args->scale;
-    a.ns = plan.ns;
-    a.tiles = plan.tiles;
-    a.prompt = plan.prompt;
-    return launch_status(launch_kv4_attention(a, args->dtype == KVC_BF16, (hipStream_t)stream));
+    return kv4_attend(desc, args, false, nullptr, codes, params, dev_status, stream);
+}
+
+int64_t kvc_kv4_tree_work_bytes(const kvc_kv4_desc *desc, int64_t n_q, int32_t n_seqs, int32_t n_q_heads,
+                                int32_t max_pages, int32_t max_q)
+{
+    if (max_q > kTreeMost) return KVC_ERR_ARG;
+    return kv4_work(desc, kv4_tree_plan, n_q, n_seqs, n_q_heads, max_pages, max_q);
+}
+
+int kvc_kv4_tree_attention(const kvc_kv4_desc *desc, const kvc_kv4_attn *args, const int32_t *parents,
+                           const uint8_t *codes, const uint16_t *params, int32_t *dev_status, void *stream)
+{
+    return kv4_attend(desc, args, true, parents, codes, params, dev_status, stream);
 }
 
 }  // extern "C"

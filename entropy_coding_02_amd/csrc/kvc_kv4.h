@@ -47,12 +47,43 @@ struct Kv4Attn {
     bool prompt;                // which kernel: tiles of 128 rows rather than 16
     float *part_o;              // [ns][n_q * Hq][D]
     float *part_ml;             // [ns][n_q * Hq][2]
+    const int32_t *parents;     // of a tree's tokens (kvc_kv4_tree_attention), or NULL
+};
+
+// The rotation of a call of kvc_kv4_append_rotated, and its q.
+struct Kv4Turn {
+    const float *table;         // [n_positions][rot]: cosines, then sines
+    const int64_t *positions;
+    int64_t n_positions;
+    int32_t rot;
+    bool interleaved;
+    Kv4Rows q;                  // src NULL: none; dst lies at the strides below
+    int64_t out_token_stride, out_head_stride;
+    bool out_vec;
+    int32_t Hq;
 };
 
 hipError_t launch_kv4_append(const Kv4Pool &pool, const Kv4Rows &k, const Kv4Rows &v, int64_t n_tokens,
                              int dtype, const int64_t *slots, hipStream_t stream);
 hipError_t launch_kv4_read(const Kv4Pool &pool, const Kv4Rows &k, const Kv4Rows &v, int64_t n_tokens,
                            int dtype, const int64_t *slots, hipStream_t stream);
+hipError_t launch_kv4_append_rotated(const Kv4Pool &pool, const Kv4Rows &k, const Kv4Rows &v, const Kv4Turn &turn,
+                                     int64_t n_tokens, int dtype, const int64_t *slots, hipStream_t stream);
+
+// Pools that one launch of kvc_kv4_keep moves tokens in: their addresses are kernel arguments.
+constexpr int kKeepPools = 64;
+
+struct Kv4Keep {
+    Kv4Pool pool;               // the geometry
+    kvc_kv4_pool pools[kKeepPools];
+    int32_t n_pools;
+    const int32_t *table;
+    int64_t table_stride;
+    const int32_t *base, *path, *n_keep;
+    int64_t path_stride;
+    int32_t B, max_path, max_pages;
+};
+hipError_t launch_kv4_keep(const Kv4Keep &a, hipStream_t stream);
 
 // Tiles of query rows and splits of the keys for a call (the launch and the
 // workspace size both follow them).
@@ -63,3 +94,8 @@ struct Kv4Plan {
 };
 Kv4Plan kv4_plan(const Kv4Pool &p, int64_t n_seqs, int R, int64_t max_q, int64_t max_keys, int64_t window);
 hipError_t launch_kv4_attention(const Kv4Attn &a, bool bf16, hipStream_t stream);
+
+// The same of kvc_kv4_tree_attention.
+constexpr int32_t kTreeMost = 1024;  // tokens of a tree: a block holds their parents
+Kv4Plan kv4_tree_plan(const Kv4Pool &p, int64_t n_seqs, int R, int64_t max_q, int64_t max_keys, int64_t window);
+hipError_t launch_kv4_tree(const Kv4Attn &a, bool bf16, hipStream_t stream);

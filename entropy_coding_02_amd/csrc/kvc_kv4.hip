@@ -160,6 +160,35 @@ __device__ __forceinline__ uint32_t v_pieces(uint32_t codes, int i)
     return c & 2 ? b : a;
 }
 
+// Channels 8i .. 8i + 7 of a row, quantised with the rest of their groups, which
+// the neighbouring lanes have, into their slot.
+template <int D, int G, bool V, bool WIDE>
+__device__ __forceinline__ void write_piece(const Kv4Pool &p, const float (&x)[8], int64_t slot, int head, int i)
+{
+    Extremes e;
+    for (int j = 0; j < 8; ++j) e.take(x[j]);
+    e.close();
+    const GroupScale g = group_scale(run_max<G / 8>(e.hi), run_max<G / 8>(e.nlo));
+    uint32_t w = 0;
+    for (int j = 0; j < 8; ++j) w |= code4<WIDE>(x[j], g) << (4 * j);
+    const int P = 1 << p.pshift, off = (int)(slot & (P - 1));
+    const int64_t blk = kv4_block(p, slot >> p.pshift, V, head);
+    uint8_t *dst = p.codes + blk * (P * (D / 2));
+    if (V) {
+        const uint32_t two = v_pieces(w, i);
+        const int piece = 8 * (i % 2) + 2 * (i / 2 % 4);  // the first one's n
+        uint16_t *at = (uint16_t *)(dst + (off / 4) * (2 * D) + piece * (D / 8) + i / 8 * 8 + (off % 4) * 2);
+        at[0] = (uint16_t)two;
+        at[D / 16] = (uint16_t)(two >> 16);
+    } else {
+        *(uint32_t *)(dst + off * (D / 2) + 4 * ((i % 4) * (D / 32) + i / 4)) = w;
+    }
+    if (i % (G / 8) == 0) {
+        p.params[(blk * (D / G) + i / (G / 8)) * P + off] = g.bits;
+        if (g.bad) kvc_flag(p.status, KVC_DEV_NONFINITE);
+    }
+}
+
 // A lane quantises 8 contiguous channels of one token: one K dword, or two V
 // pieces; a group is G/8 neighbouring lanes.  Both halves read alike, 16 bytes
 // a lane (a V half that read each piece's own channels, 2 bytes at a time, was
@@ -191,28 +220,9 @@ __device__ __forceinline__ void append_rows(const Kv4Pool &p, const Kv4Rows &r, 
             if (slot[u] >= 0 && i == 0) kvc_flag(p.status, KVC_DEV_BAD_INDEX);
             continue;
         }
-        Extremes e;
-        for (int j = 0; j < 8; ++j) e.take(x[u].at(j));
-        e.close();
-        const GroupScale g = group_scale(run_max<G / 8>(e.hi), run_max<G / 8>(e.nlo));
-        uint32_t w = 0;
-        for (int j = 0; j < 8; ++j) w |= code4<DT != KVC_F16>(x[u].at(j), g) << (4 * j);
-        const int P = 1 << p.pshift, off = (int)(slot[u] & (P - 1));
-        const int64_t blk = kv4_block(p, slot[u] >> p.pshift, V, head[u]);
-        uint8_t *dst = p.codes + blk * (P * (D / 2));
-        if (V) {
-            const uint32_t two = v_pieces(w, i);
-            const int piece = 8 * (i % 2) + 2 * (i / 2 % 4);  // the first one's n
-            uint16_t *at = (uint16_t *)(dst + (off / 4) * (2 * D) + piece * (D / 8) + i / 8 * 8 + (off % 4) * 2);
-            at[0] = (uint16_t)two;
-            at[D / 16] = (uint16_t)(two >> 16);
-        } else {
-            *(uint32_t *)(dst + off * (D / 2) + 4 * ((i % 4) * (D / 32) + i / 4)) = w;
-        }
-        if (i % (G / 8) == 0) {
-            p.params[(blk * (D / G) + i / (G / 8)) * P + off] = g.bits;
-            if (g.bad) kvc_flag(p.status, KVC_DEV_NONFINITE);
-        }
+        float y[8];
+        for (int j = 0; j < 8; ++j) y[j] = x[u].at(j);
+        write_piece<D, G, V, DT != KVC_F16>(p, y, slot[u], head[u], i);
     }
 }
 
@@ -359,6 +369,169 @@ __global__ __launch_bounds__(256) void k_kv4_read(Kv4Pool p, Kv4Rows k, Kv4Rows 
         read_v<D, G, DT>(p, v, n, slots, (uint32_t)xcd_block(blockIdx.x - k_blocks, gridDim.x - k_blocks) * 256 + threadIdx.x);
 }
 
+// ------------------------------------------------------ rotated on the way
+
+// A lane's 8 channels (8i ..) and what they are paired with: the next 8 of the
+// other half, or their own neighbours.
+template <int DT>
+__device__ __forceinline__ void rotate8(const Kv4Turn &r, int64_t pos, int i, const Eight<DT> &own, const Eight<DT> &other, float *y)
+{
+    const int half = r.rot / 2;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = own.at(j);
+    if (8 * i >= r.rot) return;
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+    if (r.interleaved) {
+        const float *cs = r.table + pos * r.rot + 4 * i;
+        const f32x4 c = *(const f32x4 *)cs, sn = *(const f32x4 *)(cs + half);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float a = y[2 * j], b = y[2 * j + 1];
+            y[2 * j] = a * c[j] - b * sn[j];
+            y[2 * j + 1] = b * c[j] + a * sn[j];
+        }
+        return;
+    }
+    const bool second = 8 * i >= half;
+    const float *cs = r.table + pos * r.rot + (second ? 8 * i - half : 8 * i);
+    f32x4 c[2], sn[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) c[k] = *(const f32x4 *)(cs + 4 * k), sn[k] = *(const f32x4 *)(cs + half + 4 * k);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        // b cos + a sin, or a cos - b sin: the sign is exact
+        const float t = other.at(j) * sn[j / 4][j % 4];
+        y[j] = y[j] * c[j / 4][j % 4] + (second ? t : -t);
+    }
+}
+
+// Eight channels of a rotated row, rounded to its type.
+template <int DT>
+__device__ __forceinline__ void store_turned(void *dst, int64_t i, bool vec, const float (&y)[8])
+{
+    if (DT == KVC_F32) {
+        typedef float f32x4 __attribute__((ext_vector_type(4)));
+        float *d = (float *)dst + i;
+        if (vec) {
+            *(f32x4 *)d = f32x4{y[0], y[1], y[2], y[3]};
+            *(f32x4 *)(d + 4) = f32x4{y[4], y[5], y[6], y[7]};
+        } else {
+            for (int j = 0; j < 8; ++j) d[j] = y[j];
+        }
+        return;
+    }
+    u32x4 w;
+    for (int j = 0; j < 4; ++j)
+        w[j] = DT == KVC_F16 ? kvc_f2h2(y[2 * j], y[2 * j + 1])
+                             : (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)y[2 * j]) |
+                                   (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)y[2 * j + 1]) << 16;
+    uint16_t *d = (uint16_t *)dst + i;
+    if (vec) {
+        *(u32x4 *)d = w;
+    } else {
+        for (int j = 0; j < 8; ++j) d[j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+    }
+}
+
+// The piece that a lane's channels are paired with (its own where they are not with another's).
+__device__ __forceinline__ int other_piece(const Kv4Turn &r, int i)
+{
+    const int half = r.rot / 16;
+    return r.interleaved || i >= 2 * half ? i : i < half ? i + half : i - half;
+}
+
+// K or V rows, as append_rows; a token without a position has no slot.
+template <int D, int G, int DT, int ITEMS, bool V>
+__device__ __forceinline__ void append_turned(const Kv4Pool &p, const Kv4Rows &r, const Kv4Turn &turn, int64_t n,
+                                              const int64_t *slots, uint32_t block)
+{
+    Eight<DT> x[ITEMS], other[ITEMS];
+    int64_t slot[ITEMS], pos[ITEMS];
+    int head[ITEMS];
+    const int64_t end = p.n_pages << p.pshift;
+    const int i = threadIdx.x % (D / 8), oi = V ? i : other_piece(turn, i);
+#pragma unroll
+    for (int u = 0; u < ITEMS; ++u) {
+        const uint32_t item = (block * ITEMS + u) * 256 + threadIdx.x;
+        const uint32_t qh = item / (D / 2);
+        head[u] = qh % p.H;
+        const int64_t t = (int64_t)(qh / p.H) * 4 + item / (D / 8) % 4;
+        slot[u] = pos[u] = -1;
+        if (t >= n) continue;
+        slot[u] = slots[t];
+        pos[u] = turn.positions[t];
+        const int64_t at = t * r.token_stride + head[u] * r.head_stride;
+        x[u].load(r.src, at + 8 * i, r.vec);
+        if (!V) other[u].load(r.src, at + 8 * oi, r.vec);
+    }
+#pragma unroll
+    for (int u = 0; u < ITEMS; ++u) {
+        // the D/8 lanes of a token skip it together
+        const bool bad = slot[u] >= end || pos[u] >= turn.n_positions;
+        if (slot[u] < 0 || pos[u] < 0 || bad) {
+            if (bad && slot[u] >= 0 && pos[u] >= 0 && i == 0) kvc_flag(p.status, KVC_DEV_BAD_INDEX);
+            continue;
+        }
+        float y[8];
+        if (V)
+            for (int j = 0; j < 8; ++j) y[j] = x[u].at(j);
+        else
+            rotate8<DT>(turn, pos[u], i, x[u], other[u], y);
+        write_piece<D, G, V, !V || DT != KVC_F16>(p, y, slot[u], head[u], i);  // a turned fp16 pair may pass its range
+    }
+}
+
+// HEADS rows of a token's q a lane, so that its angles are loaded once for them.
+// In place: a row lies within one wave, which has loaded it before it stores.
+template <int D, int DT, int HEADS>
+__device__ __forceinline__ void turn_queries(const Kv4Pool &p, const Kv4Turn &turn, int64_t n, uint32_t block)
+{
+    const int i = threadIdx.x % (D / 8);
+    const uint32_t per = (uint32_t)(turn.Hq + HEADS - 1) / HEADS;
+    const uint32_t row = block * (256 / (D / 8)) + threadIdx.x / (D / 8);
+    const int64_t t = row / per;
+    if (t >= n) return;
+    const int64_t pos = turn.positions[t];
+    if (pos < 0) return;
+    if (pos >= turn.n_positions) {
+        if (i == 0) kvc_flag(p.status, KVC_DEV_BAD_INDEX);
+        return;
+    }
+    const Kv4Rows &q = turn.q;
+    const int oi = other_piece(turn, i);
+    Eight<DT> x[HEADS], other[HEADS];
+#pragma unroll
+    for (int u = 0; u < HEADS; ++u) {
+        const uint32_t head = row % per + u * per;
+        if (head >= (uint32_t)turn.Hq) break;
+        const int64_t at = t * q.token_stride + head * q.head_stride;
+        x[u].load(q.src, at + 8 * i, q.vec);
+        other[u].load(q.src, at + 8 * oi, q.vec);
+    }
+#pragma unroll
+    for (int u = 0; u < HEADS; ++u) {
+        const uint32_t head = row % per + u * per;
+        if (head >= (uint32_t)turn.Hq) break;
+        float y[8];
+        rotate8<DT>(turn, pos, i, x[u], other[u], y);
+        store_turned<DT>(q.dst, t * turn.out_token_stride + head * turn.out_head_stride + 8 * i, turn.out_vec, y);
+    }
+}
+
+// Blocks of K rows, of V rows, of q's.
+template <int D, int G, int DT, int ITEMS, int HEADS>
+__global__ __launch_bounds__(256) void k_kv4_append_rotated(Kv4Pool p, Kv4Rows k, Kv4Rows v, Kv4Turn turn, int64_t n,
+                                                             const int64_t *slots, uint32_t kv_blocks)
+{
+    const uint32_t b = blockIdx.x;
+    if (b < kv_blocks)
+        append_turned<D, G, DT, ITEMS, false>(p, k, turn, n, slots, (uint32_t)xcd_block(b, kv_blocks));
+    else if (b < 2 * kv_blocks)
+        append_turned<D, G, DT, ITEMS, true>(p, v, turn, n, slots, (uint32_t)xcd_block(b - kv_blocks, kv_blocks));
+    else
+        turn_queries<D, DT, HEADS>(p, turn, n, b - 2 * kv_blocks);
+}
+
 template <int D, int G>
 hipError_t move_rows(bool append, const Kv4Pool &p, const Kv4Rows &k, const Kv4Rows &v, int64_t n, int dt,
                      const int64_t *slots, hipStream_t s)
@@ -408,6 +581,47 @@ Kv4Rows rows_from(Kv4Rows r, int64_t t, int dt)
     return r;
 }
 
+template <int D, int G, int DT>
+hipError_t rotate_rows(const Kv4Pool &p, const Kv4Rows &k, const Kv4Rows &v, const Kv4Turn &turn, int64_t n, const int64_t *slots,
+                       hipStream_t s)
+{
+    const uint32_t lanes = (uint32_t)((n + 3) / 4 * p.H) * (D / 2);
+    const bool full = lanes > 256u * 2048u;  // as move_rows
+    const uint32_t kvb = (lanes + (full ? 511 : 255)) / (full ? 512 : 256);
+    const int heads = n * turn.Hq * (D / 8) > 256 * 2048 ? 4 : 1;
+    const int64_t rows = turn.q.src ? n * ((turn.Hq + heads - 1) / heads) : 0;
+    const dim3 grid(2 * kvb + (uint32_t)((rows * (D / 8) + 255) / 256)), block(256);
+    if (full && heads == 4) k_kv4_append_rotated<D, G, DT, 2, 4><<<grid, block, 0, s>>>(p, k, v, turn, n, slots, kvb);
+    else if (full) k_kv4_append_rotated<D, G, DT, 2, 1><<<grid, block, 0, s>>>(p, k, v, turn, n, slots, kvb);
+    else if (heads == 4) k_kv4_append_rotated<D, G, DT, 1, 4><<<grid, block, 0, s>>>(p, k, v, turn, n, slots, kvb);
+    else k_kv4_append_rotated<D, G, DT, 1, 1><<<grid, block, 0, s>>>(p, k, v, turn, n, slots, kvb);
+    return hipGetLastError();
+}
+
+template <int D, int G>
+hipError_t rotate_dt(const Kv4Pool &p, const Kv4Rows &k, const Kv4Rows &v, const Kv4Turn &turn, int64_t n, int dt, const int64_t *slots,
+                     hipStream_t s)
+{
+    if (dt == KVC_F16) return rotate_rows<D, G, KVC_F16>(p, k, v, turn, n, slots, s);
+    if (dt == KVC_BF16) return rotate_rows<D, G, KVC_BF16>(p, k, v, turn, n, slots, s);
+    return rotate_rows<D, G, KVC_F32>(p, k, v, turn, n, slots, s);
+}
+
+hipError_t rotate_piece(const Kv4Pool &p, const Kv4Rows &k, const Kv4Rows &v, const Kv4Turn &turn, int64_t n, int dt,
+                        const int64_t *slots, hipStream_t s)
+{
+    switch (p.D * 1000 + p.G) {
+    case 64032: return rotate_dt<64, 32>(p, k, v, turn, n, dt, slots, s);
+    case 64064: return rotate_dt<64, 64>(p, k, v, turn, n, dt, slots, s);
+    case 128032: return rotate_dt<128, 32>(p, k, v, turn, n, dt, slots, s);
+    case 128064: return rotate_dt<128, 64>(p, k, v, turn, n, dt, slots, s);
+    case 128128: return rotate_dt<128, 128>(p, k, v, turn, n, dt, slots, s);
+    case 256032: return rotate_dt<256, 32>(p, k, v, turn, n, dt, slots, s);
+    case 256064: return rotate_dt<256, 64>(p, k, v, turn, n, dt, slots, s);
+    default: return rotate_dt<256, 128>(p, k, v, turn, n, dt, slots, s);
+    }
+}
+
 // A launch holds fewer than 2^32 threads, n/4 * H * D/2 for K and as many for V;
 // more tokens than that take several.
 hipError_t move_any(bool append, const Kv4Pool &p, const Kv4Rows &k, const Kv4Rows &v, int64_t n, int dt,
@@ -434,4 +648,21 @@ hipError_t launch_kv4_read(const Kv4Pool &pool, const Kv4Rows &k, const Kv4Rows 
                            int dtype, const int64_t *slots, hipStream_t stream)
 {
     return move_any(false, pool, k, v, n_tokens, dtype, slots, stream);
+}
+
+hipError_t launch_kv4_append_rotated(const Kv4Pool &pool, const Kv4Rows &k, const Kv4Rows &v, const Kv4Turn &turn,
+                                     int64_t n_tokens, int dtype, const int64_t *slots, hipStream_t stream)
+{
+    // a launch holds fewer than 2^32 threads: H * D/8 lanes a token for K, as many for V, Hq * D/8 for q
+    const int64_t most = ((int64_t)1 << 31) / ((int64_t)(2 * pool.H + (turn.q.src ? turn.Hq : 0)) * (pool.D / 8)) / 4 * 4;
+    for (int64_t t = 0; t < n_tokens; t += most) {
+        Kv4Turn from = turn;
+        from.q = rows_from(turn.q, t, dtype);
+        if (from.q.dst) from.q.dst = (char *)turn.q.dst + t * turn.out_token_stride * (dtype == KVC_F32 ? 4 : 2);
+        from.positions += t;
+        const hipError_t e = rotate_piece(pool, rows_from(k, t, dtype), rows_from(v, t, dtype), from,
+                                          n_tokens - t < most ? n_tokens - t : most, dtype, slots + t, stream);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }

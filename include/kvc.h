@@ -536,6 +536,89 @@ int64_t kvc_kv4_work_bytes(const kvc_kv4_desc *desc, int64_t n_q, int32_t n_seqs
 int kvc_kv4_attention(const kvc_kv4_desc *desc, const kvc_kv4_attn *args, const uint8_t *codes,
                       const uint16_t *params, int32_t *dev_status, void *stream);
 
+/*
+ * Speculative decoding from the resident cache.  A step drafts a tree of
+ * tokens after each sequence, writes them behind its cached ones (their keys at
+ * the positions of their depth in the tree, not of their slots:
+ * kvc_kv4_append_rotated), attends from all of them at once
+ * (kvc_kv4_tree_attention), and keeps the path that is accepted (kvc_kv4_keep).
+ */
+
+/*
+ * Write tokens as kvc_kv4_append does, with the rotation of their positions
+ * applied to k on the way, and to q.  The first `rot` channels of a head are
+ * rot/2 pairs: (i, i + rot/2), or (2i, 2i + 1) where interleaved.  With the
+ * row of `table` at the token's position, rot/2 cosines and then as many sines,
+ * a pair (a, b) becomes
+ *   a' = a cos_i - b sin_i,   b' = b cos_i + a sin_i,
+ * in fp32, every operation rounded on its own.  k' is quantised as it is (a
+ * group that holds Inf or NaN once rotated is stored as NaN), v as it came,
+ * and q' is rounded to its type.
+ */
+typedef struct kvc_kv4_rotated {
+    const void *k, *v;        /* [n_tokens][H][D] of dtype, as kvc_kv4_append */
+    const void *q;            /* NULL, or [n_tokens][n_q_heads][D] of dtype, channels contiguous */
+    void *q_out;              /* with q: as it (written); may be q itself with q's strides, else must
+                                 not overlap it, nor its rows each other */
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride; /* elements */
+    int64_t q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride;
+    const int64_t *slots;     /* [n_tokens], as kvc_kv4_append; where k and v are skipped q is rotated all the same */
+    const int64_t *positions; /* [n_tokens]; a negative one skips its token, q_out's rows too (padding of a
+                                 captured batch); one past the table does so and sets KVC_DEV_BAD_INDEX */
+    const float *table;       /* [n_positions][rot], 16-byte aligned */
+    int64_t n_tokens, n_positions;
+    int32_t n_q_heads;        /* 1..65536 with q */
+    int32_t rot;              /* a multiple of 16, 16..D */
+    int32_t interleaved, dtype;
+} kvc_kv4_rotated;
+
+int kvc_kv4_append_rotated(const kvc_kv4_desc *desc, const kvc_kv4_rotated *args, uint8_t *codes,
+                           uint16_t *params, int32_t *dev_status, void *stream);
+
+/*
+ * Attention of drafted tokens over the cache and over their own tree.  As
+ * kvc_kv4_attention with these differences: the nq_b queries of sequence b are
+ * the drafted tokens whose keys are its last nq_b cached ones, so that
+ * base = kv_len[b] - nq_b keys lie before the tree, and parents[cu_q[b] + i] is the
+ * drafted token that token i follows, as an index within the sequence's own,
+ * less than i, or -1 for the last token before the tree.  Token i, n_i steps
+ * from there (1 with parent -1), stands at position base + n_i - 1.  It sees the
+ * keys j < base, and the drafted ones that are itself and its ancestors; if
+ * window > 0 only those at positions > its own - window.  (Keys below 0, of a
+ * sequence with fewer keys than queries, do not exist.)  args->causal must be
+ * 1, and max_q at most 1024.
+ * A parent that is no earlier token sets KVC_DEV_BAD_INDEX and is taken as -1.
+ */
+int64_t kvc_kv4_tree_work_bytes(const kvc_kv4_desc *desc, int64_t n_q, int32_t n_seqs, int32_t n_q_heads,
+                                int32_t max_pages, int32_t max_q);
+int kvc_kv4_tree_attention(const kvc_kv4_desc *desc, const kvc_kv4_attn *args, const int32_t *parents,
+                           const uint8_t *codes, const uint16_t *params, int32_t *dev_status, void *stream);
+
+/*
+ * Keep the accepted path of each sequence's tree: in every pool, token
+ * base[b] + i becomes what token base[b] + path[b][i] was before the call, for
+ * i < n_keep[b] (codes and parameters are moved as they are).  The sequence then
+ * holds base[b] + n_keep[b] tokens; what lies behind them is left over.
+ *   pools       HOST array of n_pools pools of one geometry: the layers' caches, which share the page table
+ *   page_table, table_stride, max_pages   as kvc_kv4_attention
+ *   base        int32 [n_seqs] (device, read): tokens before the tree
+ *   path        int32 [n_seqs][max_path], rows path_stride entries apart (device, read): rising, none below 0
+ *   n_keep      int32 [n_seqs] (device, read); below 1 nothing is moved
+ * Sequences must not share the pages that they keep tokens in.  A sequence
+ * whose base is negative, whose n_keep passes max_path, whose path does not
+ * rise or leaves the table, or that has a page outside the pool there, is left as it was and sets
+ * KVC_DEV_BAD_INDEX.
+ */
+typedef struct kvc_kv4_pool {
+    uint8_t *codes;
+    uint16_t *params;
+} kvc_kv4_pool;
+
+int kvc_kv4_keep(const kvc_kv4_desc *desc, const kvc_kv4_pool *pools, int32_t n_pools,
+                 const int32_t *page_table, int64_t table_stride, int32_t max_pages, const int32_t *base,
+                 const int32_t *path, int64_t path_stride, int32_t max_path, const int32_t *n_keep,
+                 int32_t n_seqs, int32_t *dev_status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
