@@ -309,6 +309,7 @@ int kv4_attend(const kvc_kv4_desc *desc, const kvc_kv4_attn *args, bool tree, co
     a.tiles = plan.tiles;
     a.prompt = plan.prompt;
     a.parents = parents;
+    a.rows = plan.rows;
     const auto launch = tree ? launch_kv4_tree : launch_kv4_attention;
     return launch_status(launch(a, args->dtype == KVC_BF16, (hipStream_t)stream));
 }

@@ -48,6 +48,7 @@ struct Kv4Attn {
     float *part_o;              // [ns][n_q * Hq][D]
     float *part_ml;             // [ns][n_q * Hq][2]
     const int32_t *parents;     // of a tree's tokens (kvc_kv4_tree_attention), or NULL
+    int32_t rows;               // of a tree's tile
 };
 
 // The rotation of a call of kvc_kv4_append_rotated, and its q.
@@ -91,6 +92,7 @@ struct Kv4Plan {
     int32_t tiles, ns;
     int32_t most_ns;  // with window = 0: the most that any window makes it
     bool prompt;      // which kernel
+    int32_t rows;     // of a tile of kvc_kv4_tree_attention, which goes by it
 };
 Kv4Plan kv4_plan(const Kv4Pool &p, int64_t n_seqs, int R, int64_t max_q, int64_t max_keys, int64_t window);
 hipError_t launch_kv4_attention(const Kv4Attn &a, bool bf16, hipStream_t stream);

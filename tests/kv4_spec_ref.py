@@ -66,6 +66,24 @@ def attention(q, k, v, ok, softcap, scale):
     return out, lse
 
 
+def spread(q, k, v, ok, softcap, scale):
+    """sum_j p_j |v_j - out|, p normalised, of attention's rows: what one rounding of every p moves out by, for each
+    unit of its relative size."""
+    n, R, D = q.shape
+    out = np.zeros((n, R, D))
+    for i in range(n):
+        if not ok[i].any():
+            continue
+        x = q[i] @ k[ok[i]].T * scale
+        if softcap:
+            x = softcap * np.tanh(x / softcap)
+        p = np.exp(x - x.max(-1, keepdims=True))
+        p /= p.sum(-1, keepdims=True)
+        for r in range(R):
+            out[i, r] = p[r] @ np.abs(v[ok[i]] - p[r] @ v[ok[i]])
+    return out
+
+
 def random_tree(n, rng, shape="bushy"):
     if shape == "chain":
         return list(range(-1, n - 1))
