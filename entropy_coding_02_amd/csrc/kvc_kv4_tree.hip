@@ -354,85 +354,99 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv4_tree(Kv4A
 
 // ------------------------------------------------------------- many rows
 
-// Blocks of 32 RG rows for trees of more than 32.  A block's four waves are RG groups of 32
-// rows times KG = 4/RG of keys; a turn of 32 KG keys is unpacked once, by all of them, into
-// matrix operands in LDS.
+// Blocks of 128 rows where that many can be had (kv4_tree_plan): four waves of 32 rows share 32 keys a turn,
+// which they unpack together, once, into matrix operands in LDS while they work on the turn before.
+// Bound by the vector and matrix units' issue: with D = 128 G = 64 a wave's turn is some 300 vector, 54 matrix and 50 LDS
+// instructions, of two waves a SIMD.  60 tokens of 8 heads a KV head, 80000 keys, 8 KV heads, bf16: 358 us, 0.44 PFLOP/s of
+// products (tiles of 32 rows 433 us).  Tried and not better: blocks of 64 rows and two times 32 keys (210 us, these
+// 125, of 16 sequences of up to 8192 keys), waves of 64 rows (130 to 380 registers spilled, 855 us).
 //
 // Here V's s is in its operand: v - mid = s (n - 7.5) is 15 bits, two fp16 terms, so that p
 // is one operand for all groups instead of p s two for each (19 vector instructions a
-// probability with two groups, here 11):
+// probability with two groups, here 7):
 //   o_c = sum_j p_j (hi + lo)_jc,   and one more product with the rows mid_g (two terms each) and
 //   "1" gives sum_j p_j mid_jg and sum_j p_j.
-// A key's rows are scaled by f_j, a power of two that takes its largest value to 2^8, and p_j
-// by 1 / f_j: its terms then keep what fp16 has below 2^9, 33 bits, whatever the others' sizes.
+// The rows of 16 keys are scaled by f, a power of two that takes their largest value to 2^8, and
+// their p by 1 / f: the terms then keep what fp16 has below 2^9, 33 bits of those keys' largest value,
+// whatever other keys' sizes.
 // bf16 outputs: p in one fp16 term, the sum that divides included, so that they are exact
 // averages whose weights are off by 2^-11 of themselves at most: 2^-11 sum_j p_j |v_j - out| / sum_j p_j,
 // an eighth of a bf16 rounding of what is averaged.  fp16 outputs: two terms, 22 bits.
 // lse is from unrounded p either way (two terms are as good).
-template <int D, int G, int KG>
-struct Turn {
-    static constexpr int NW = D / 32, NG = D / G, NT = D / 16, NP = (NG + 3) / 4;
-    static constexpr int NZ = (2 * NG + 1 + 15) / 16;  // products of the rows mid and 1
-    u32x4 k[KG][2][NW][64];
-    u32x2 v[KG][NT][2][2][64];      // V's hi and lo, of either tile of 16 keys
-    uint16_t z[KG][NZ][64][8];      // an operand: row 2g, 2g + 1: mid_g's terms, then the scale f itself
-    uint16_t nan[KG][64][8];        // an operand: row g is 1 where a key's group is NaN; only where any_nan is its tile's
-    float ks[KG][2][NG][16];        // K's s
-    uint32_t kp[KG][2][NP][64];     // K's parameters as loaded, for lo_operand
-    float e[KG][2][16], f[KG][2][16];  // -log2 f, f
-    uint32_t any_nan[KG][2];
-};
+constexpr int kTreeRows = 128;
 
-template <int D, int G, bool BF, int RG>
+// Over a row of 16 lanes: neighbours and pairs, then mirrored halves, whose quads already agree.
+template <int CTRL>
+__device__ __forceinline__ float dpp_max(float v)
+{
+    return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true)));
+}
+__device__ __forceinline__ float max16(float v) { return dpp_max<0x140>(dpp_max<0x141>(dpp_max<0x4E>(dpp_max<0xB1>(v)))); }
+
+// What a turn's 32 keys are to the matrix unit.
+template <int D, int G>
+struct Turn {
+    static constexpr int NW = D / 32, NT = D / 16;
+    u32x4 k[2][NW][64];
+    u32x2 v[NT][2][2][64];     // V's hi and lo, of either tile of 16 keys
+};
+// What goes with them, known a turn earlier.
+template <int D, int G>
+struct Keys {
+    static constexpr int NG = D / G, NP = (NG + 3) / 4, NZ = (2 * NG + 1 + 15) / 16;  // products of the rows mid and 1
+    uint16_t z[NZ][64][8];     // an operand: row 2g, 2g + 1: mid_g's terms, then the scale f itself
+    uint16_t nan[64][8];       // an operand: row g is 1 where a key's group is NaN
+    u32x2 klo[NP][2][64];      // lo_operand of K: groups 0..3, 4..7; zero where there is none
+    float ks[2][NG][16];       // K's s
+    uint16_t s[2][NG][16];     // V's s, scaled
+    float e[2], f[2];          // of the tiles: -log2 f, f
+    uint32_t any_nan[2], pad[2];
+};
+constexpr int kAhead = 3;      // turns' Keys: one read, one read to unpack V by, one written
+
+template <int D, int G, bool BF>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_tree_wide(Kv4Attn a)
 {
-    constexpr int NW = D / 32, NG = D / G, NT = D / 16, NP = (NG + 3) / 4, ROWS = 32 * RG, KG = 4 / RG;
-    constexpr int BUFS = RG == 4 ? 2 : 1;
+    constexpr int NW = D / 32, NG = D / G, NT = D / 16, NP = (NG + 3) / 4, ND = NW / 2;
     constexpr bool TWO = !BF;                          // terms of p
-    constexpr int SHARE = RG == 4 ? 2 : 1;             // waves that unpack one tile, a part of its dwords each
-    constexpr int ND = NW / SHARE;
-    typedef Turn<D, G, KG> T;
-    constexpr int NZ = T::NZ;
+    typedef Turn<D, G> T;
+    typedef Keys<D, G> K;
+    constexpr int NZ = K::NZ;
     extern __shared__ __align__(16) uint8_t lds_raw[];
     T *const turns = (T *)lds_raw;
+    K *const keys = (K *)(lds_raw + 2 * sizeof(T));
     // what the largest tree of the call takes
-    int16_t *const lds_steps = (int16_t *)(lds_raw + BUFS * sizeof(T)), *const lds_parent = lds_steps + ROWS;
+    int16_t *const lds_steps = (int16_t *)(lds_raw + 2 * sizeof(T) + kAhead * sizeof(K)), *const lds_parent = lds_steps + kTreeRows;
     uint32_t *const lds_bits = (uint32_t *)(lds_parent + (a.max_q + 1) / 2 * 2);
-    __shared__ __align__(8) uint16_t lds_s[kWaves][NG][16];  // a tile's s of V, scaled, for the lanes that unpack it
-    __shared__ u32x4 lds_sums[2 * RG][64];                   // sum_operand of the rows
-    __shared__ uint32_t lds_nan[ROWS];                       // a row's groups in which it met NaN
+    __shared__ u32x4 lds_sums[kTreeRows / 16][64];     // sum_operand of the rows
+    __shared__ uint32_t lds_nan[kTreeRows];            // a row's groups in which it met NaN
     Job j;
-    if (!make_job<ROWS, true>(a, j)) return;
+    if (!make_job<kTreeRows, true>(a, j)) return;
     int lane = threadIdx.x & 63, col = lane & 15, h = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // where a tile has fewer rows than groups of them the same waves would idle in every block
-    const int rg = (wave + (int)blockIdx.x) % RG, kg = RG == 4 ? 0 : (wave + (int)blockIdx.x) / RG % KG;
-    const int tile = RG == 4 ? wave & 1 : wave;        // of a turn, unpacked by this wave: its dwords d0 ..
-    const int d0 = RG == 4 ? (wave >> 1) * ND : 0;
-    const int t_end = (min(j.u1 * 4, (j.kend + 31) / 32) + KG - 1) / KG;
-    int turn = j.u0 * 4 / KG;
+    // where a tile has fewer rows the same waves would idle in every block
+    const int rg = (wave + (int)blockIdx.x) & 3;
+    const int tile = wave & 1, d0 = (wave >> 1) * ND;  // this wave's part in unpacking: a tile's dwords d0 ..
+    const int t_end = min(j.u1 * 4, (j.kend + 31) / 32);
+    int turn = j.u0 * 4;
     const WaveAt<D, G> wat(a, j);
 
-    const int last_row = min(j.row0 + ROWS, j.rows) - 1;
+    const int last_row = min(j.row0 + kTreeRows, j.rows) - 1;
     const int tok0 = j.row0 / a.R, tok1 = last_row / a.R;
     Paths paths;
     paths.bits = lds_bits;
     paths.base = j.pos0;
     paths.first = max(j.pos0, 0) >> 5;
     paths.words = max(((j.kend + 31) >> 5) - paths.first, 0);
-    const bool walks = t_end * KG > paths.first || a.window;
+    const bool walks = t_end > paths.first || a.window;
     if (walks) {
         stage_parents(a, j, tok1, lds_parent);
         lds_barrier();
         walk(a, paths, lds_parent, tok0, tok1, lds_steps);
     }
     // rows of the operands that no group has
-    for (int i = threadIdx.x; i < BUFS * KG * (NZ + 1) * 64; i += 256) {
-        const int buf = i / (KG * (NZ + 1) * 64), k = i / ((NZ + 1) * 64) % KG, z = i / 64 % (NZ + 1);
-        u32x4 *const to = (u32x4 *)(z < NZ ? &turns[buf].z[k][z][i % 64][0] : &turns[buf].nan[k][i % 64][0]);
-        *to = u32x4{0, 0, 0, 0};
-    }
-    if (threadIdx.x < ROWS) lds_nan[threadIdx.x] = 0;
+    for (int i = threadIdx.x; i < (int)(kAhead * sizeof(K)) / 16; i += 256) ((u32x4 *)keys)[i] = u32x4{0, 0, 0, 0};
+    if (threadIdx.x < kTreeRows) lds_nan[threadIdx.x] = 0;
     lds_barrier();
 
     const int row_w = j.row0 + 32 * rg;
@@ -455,7 +469,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_tree_wide(Kv4Attn
             for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) c = mfma(ones, q[ct][s], c);
             qs[g] = c[0] * 0x1p-9f;
         }
-        if (kg == 0) lds_sums[2 * rg + ct][lane] = sum_operand<NG>(qs, h);
+        lds_sums[2 * rg + ct][lane] = sum_operand<NG>(qs, h);  // read by this wave alone
         toks |= (uint32_t)(min(row, last_row) / a.R - tok0) << (16 * ct);
     }
     // keys that some row of the wave sees, and that every row does
@@ -474,46 +488,60 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_tree_wide(Kv4Attn
         ref[ct] = -__builtin_inff();
         l[ct] = 0.0f;
     }
-    bool bad_page = false;
 
-    // this wave's part of a turn: loaded, then laid out in LDS
-    uint32_t kw[ND], vw[ND], kp[NP], vp[NP];
-    int32_t page = 0;
-    const auto tile_of = [&](int t) { return min(max(t * (2 * KG) + tile, wat.t_lo), wat.t_hi); };
-    const auto look_up = [&](int t) { page = wat.table[tile_of(t) >> wat.shift]; };
-    const auto fetch = [&](int t) {
-        const uint32_t entry = (uint32_t)__builtin_amdgcn_readfirstlane(page);
+    // ---- unpacking.  In turn t the operands of t + 1 are laid out, a part of a tile by each wave, by what the first of a
+    // tile's waves found out about its keys in turn t - 1 (Keys).
+    bool bad_page = false;
+    uint32_t pages = 0;                    // of this wave's tiles of 64 turns, a lane each
+    uint32_t kw[ND], vw[ND], kw2[ND], vw2[ND], kp[NP], vp[NP];  // codes of t + 1, and of t + 2 on their way with the parameters
+    const auto tile_of = [&](int t) { return min(max(t * 2 + tile, wat.t_lo), wat.t_hi); };
+    const auto look_up = [&](int t) {
+        const uint32_t entry = (uint32_t)wat.table[tile_of(t + lane) >> wat.shift];
         bad_page |= entry >= wat.n_pages;
-        const uint32_t pg = entry < wat.n_pages ? entry : 0;
-        const uint32_t in = (uint32_t)(tile_of(t) & wat.mask);
-        const uint8_t *codes = wat.codes + (uint64_t)pg * wat.page_codes + in * (8 * D);
-        const uint8_t *params = wat.params + (uint64_t)pg * wat.page_params + in * 64;
-        const LaneAt<D, G> at(lane, a.pool);
-        const uint32_t k_at = at.k + 4 * d0, v_at = at.v + 4 * d0;
+        pages = entry < wat.n_pages ? entry : 0;
+    };
+    // a lane has the parameters of key `col`, group g_l (and g_l + 4)
+    const auto group_l = [&](int h) { return NG == 1 ? 0 : NG == 2 ? h & 1 : h; };
+    const uint32_t k_at = col * (D / 2) + h * (D / 8) + 4 * d0;
+    const uint32_t v_at = h * (2 * D) + col * (D / 8) + ((uint32_t)a.pool.H << a.pool.pshift) * (D / 2) + 4 * d0;
+    const uint32_t p_at = (((uint32_t)group_l(h) << a.pool.pshift) + col) * 4, to_v = ((uint32_t)(a.pool.H * NG) << a.pool.pshift) * 4;
+    const int turn0 = turn;
+    const auto fetch = [&](int t) {
+        const int i = t - turn0;
+        if ((i & 63) == 0) look_up(t);
+        const uint32_t page = (uint32_t)__builtin_amdgcn_readlane((int)pages, i & 63), in = (uint32_t)(tile_of(t) & wat.mask);
+        const uint8_t *codes = wat.codes + (uint64_t)page * wat.page_codes + in * (8 * D);
+        const uint8_t *params = wat.params + (uint64_t)page * wat.page_params + in * 64;
 #pragma unroll
         for (int i = 0; i < ND; ++i) {
-            kw[i] = ((const uint32_t *)(codes + k_at))[i];
-            vw[i] = ((const uint32_t *)(codes + v_at))[i];
+            kw2[i] = ((const uint32_t *)(codes + k_at))[i];
+            vw2[i] = ((const uint32_t *)(codes + v_at))[i];
         }
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            kp[i] = *(const uint32_t *)(params + at.kp[i]);
-            vp[i] = *(const uint32_t *)(params + at.vp[i]);
+            const uint32_t g = p_at + ((uint32_t)(4 * i) << a.pool.pshift) * 4;
+            kp[i] = *(const uint32_t *)(params + g);
+            vp[i] = *(const uint32_t *)(params + (g + to_v));
         }
     };
-    const auto lay_params = [&](int t, T &to) {
-        const int kgt = tile >> 1, half = tile & 1;
-        const int key = t * (32 * KG) + 16 * tile + col;
+    const auto fetched = [&]() {
+#pragma unroll
+        for (int i = 0; i < ND; ++i) kw[i] = kw2[i], vw[i] = vw2[i];
+    };
+    const auto lay_keys = [&](int t, K &to) {
+        const int key = t * 32 + 16 * tile + col, at = 4 * tile + col % 4;
         const bool in = key >= j.kbeg && key < j.kend;  // what lies at keys that no row sees may be anything
-        // of key `col`, groups h and h + 4
         float mid[NP], s[NP], top = 0.0f;
         bool is_nan[NP], some = false;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            kp[i] = in ? kp[i] : 0;
-            const uint32_t w = in ? vp[i] : 0;
-            s[i] = s_of(w);
-            mid[i] = mid_of(w);
+            const int g = group_l(h) + 4 * i;
+            const uint32_t w = in ? kp[i] : 0, lo = w >> 16;
+            to.ks[tile][g][col] = s_of(w);
+            to.klo[i][tile][col + 16 * group_l(h)] = u32x2{lo | lo << 16, lo};
+            const uint32_t x = in ? vp[i] : 0;
+            s[i] = s_of(x);
+            mid[i] = mid_of(x);
             is_nan[i] = !(mid[i] == mid[i]);
             some |= is_nan[i];
             mid[i] = is_nan[i] ? 0.0f : mid[i];
@@ -532,45 +560,33 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_tree_wide(Kv4Attn
             const uint32_t x0 = x[0], x1 = x[1];
             top = fmaxf(__builtin_bit_cast(float, x0), __builtin_bit_cast(float, x1));
         }
+        top = max16(top);
         // f = 2^(8 - e) for a largest of 2^e (at most 2^17), and at most 2^15
         const int e = max((int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127, -7);
         const float f = __builtin_bit_cast(float, (uint32_t)(127 + 8 - e) << 23);
-        const bool one = __any(some);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            const int g = h + 4 * i;
-            if (g < NG) lds_s[wave][g][col] = (uint16_t)kvc_f2h(s[i] * f * 512.0f);
+            const int g = group_l(h) + 4 * i;
+            to.s[tile][g][col] = (uint16_t)kvc_f2h(s[i] * f * 512.0f);
+            const float m = mid[i] * f;
+            const uint32_t hi = kvc_f2h(m);
+            uint16_t *const row = &to.z[g / 8][2 * g % 16 + 16 * (col / 4)][at];
+            row[0] = (uint16_t)hi;
+            row[8] = (uint16_t)kvc_f2h(m - kvc_h2f(hi));
+            to.nan[g + 16 * (col / 4)][at] = is_nan[i] ? 0x3C00 : 0;
         }
-        if (d0 == 0) {  // the first of a tile's waves writes what is its keys'
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                const int g = h + 4 * i;
-                if (g < NG) {
-                    to.ks[kgt][half][g][col] = s_of(kp[i]);
-                    const float m = mid[i] * f;
-                    const uint32_t hi = kvc_f2h(m);
-                    uint16_t *const row = &to.z[kgt][g / 8][2 * g % 16 + 16 * (col / 4)][4 * half + col % 4];
-                    row[0] = (uint16_t)hi;
-                    row[8] = (uint16_t)kvc_f2h(m - kvc_h2f(hi));
-                    if (one) to.nan[kgt][g + 16 * (col / 4)][4 * half + col % 4] = is_nan[i] ? 0x3C00 : 0;
-                }
-                to.kp[kgt][half][i][lane] = kp[i];
-            }
-            if (h == 0) {
-                to.z[kgt][NZ - 1][2 * NG % 16 + 16 * (col / 4)][4 * half + col % 4] = (uint16_t)kvc_f2h(f);
-                to.e[kgt][half][col] = (float)(e - 8);
-                to.f[kgt][half][col] = f;
-            }
-            if (lane == 0) to.any_nan[kgt][half] = one;
-        }
+        // the same from every group
+        to.z[NZ - 1][2 * NG % 16 + 16 * (col / 4)][at] = (uint16_t)kvc_f2h(f);
+        to.e[tile] = (float)(e - 8);
+        to.f[tile] = f;
+        to.any_nan[tile] = __ballot(some) != 0;
     };
-    // Part `part` of `parts` of the operands themselves, after lay_params.
+    // Part `part` of `parts` of the operands of turn t.
     constexpr int VN = ND > 1 ? 2 : 1, V_ITEMS = ND / VN * 4;  // dwords of V at once
-    const auto lay_operands = [&](T &to, int part, int parts) {
-        const int kgt = tile >> 1, half = tile & 1;
+    const auto lay_operands = [&](T &to, const K &by, int part, int parts) {
 #pragma unroll
         for (int i = 0; i < ND; ++i)
-            if (i * parts / ND == part) to.k[kgt][half][d0 + i][lane] = code_octet(kw[i]);
+            if (i * parts / ND == part) to.k[tile][d0 + i][lane] = code_octet(kw[i]);
         // V with s of this lane's four keys
 #pragma unroll
         for (int item = 0; item < V_ITEMS; ++item) {
@@ -579,30 +595,27 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_tree_wide(Kv4Attn
             u32x2 hi, lo;
 #pragma unroll
             for (int k = 0; k < VN; ++k) {
-                const u16x2 sp = *(const u16x2 *)&lds_s[wave][16 * c / G][4 * h + 2 * ((d0 + i + k) & 1)];
+                const u16x2 sp = *(const u16x2 *)&by.s[tile][16 * c / G][4 * h + 2 * ((d0 + i + k) & 1)];
                 const f16x2 t2 = __builtin_bit_cast(f16x2, centred_pair(vw[i + k], n)), s2 = __builtin_bit_cast(f16x2, sp);
                 const f16x2 first = t2 * s2;
                 hi[k] = __builtin_bit_cast(uint32_t, first);
                 lo[k] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(t2, s2, -first));
             }
             if (VN > 1) {
-                to.v[kgt][c][0][half][lane] = hi;
-                to.v[kgt][c][1][half][lane] = lo;
+                to.v[c][0][tile][lane] = hi;
+                to.v[c][1][tile][lane] = lo;
             } else {
-                ((uint32_t *)&to.v[kgt][c][0][half][lane])[d0 & 1] = hi[0];
-                ((uint32_t *)&to.v[kgt][c][1][half][lane])[d0 & 1] = lo[0];
+                ((uint32_t *)&to.v[c][0][tile][lane])[d0 & 1] = hi[0];
+                ((uint32_t *)&to.v[c][1][tile][lane])[d0 & 1] = lo[0];
             }
         }
     };
-    const auto lay_out = [&](int t, T &to) {
-        lay_params(t, to);
-        lay_operands(to, 0, 1);
-    };
+
+    // ---- the work
     // which rows of a column tile see how many of which groups' NaN: a product of its own
-    const auto meet_nan = [&](const T &now, int ct, uint32_t see) {
-        u32x4 is = *(const u32x4 *)&now.nan[kg][lane][0], sees;
-        if (!now.any_nan[kg][0]) is[0] = is[1] = 0;
-        if (!now.any_nan[kg][1]) is[2] = is[3] = 0;
+    const auto meet_nan = [&](const K &by, int ct, uint32_t see) {
+        const u32x4 is = *(const u32x4 *)&by.nan[lane][0];
+        u32x4 sees;
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
             const int at = 16 * (i / 4) + i % 4;
@@ -612,9 +625,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_tree_wide(Kv4Attn
         uint32_t met = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) met |= n[i] > 0.0f ? 1u << i : 0;
-        if (met) atomicOr(&lds_nan[32 * rg + 16 * ct + col], met << (4 * h));
+        if (met) atomicOr(&lds_nan[16 * (2 * rg + ct) + col], met << (4 * h));
     };
-    // rows of which some p passes the largest so far by 2^8
+    // rows of which some p passes the largest so far by 2^8: what their sums were multiplied by, and p is relative to now
     const auto pass_on = [&](int ct, float top) {
         float pass = ref[ct] + 15.0f, mu;  // as rescale leaves it
         const float by = rescale(top, pass, ref[ct], mu);
@@ -623,93 +636,181 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_tree_wide(Kv4Attn
         for (int i = 0; i < NZ; ++i) z[ct][i] *= by;
 #pragma unroll
         for (int c = 0; c < NT; ++c) o[ct][c] *= by;
+        return mu;
     };
     const auto load_v = [&](const T &now, int c, u32x4 *v) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const u32x2 a0 = now.v[kg][c][k][0][lane], a1 = now.v[kg][c][k][1][lane];
+            const u32x2 a0 = now.v[c][k][0][lane], a1 = now.v[c][k][1][lane];
             v[k] = u32x4{a0[0], a0[1], a1[0], a1[1]};
         }
     };
-    // A turn that every row of the wave sees whole, without a cap, and what the next one needs laid out
-    // meanwhile: the matrix unit takes 16 cycles an instruction, of which a wave's vector instructions can have 12.
-    const auto both = [&](int t, const T &now, T &to) {
-        u32x4 k[2][NW];
-        uint32_t prm[2][NP];
-        const u32x4 sums[2] = {lds_sums[2 * rg][lane], lds_sums[2 * rg + 1][lane]};
+    const auto load_klo = [&](const K &by, int tt) {
+        const u32x2 a0 = by.klo[0][tt][lane], a1 = NP > 1 ? by.klo[NP - 1][tt][lane] : u32x2{0, 0};
+        return u32x4{a0[0], a0[1], a1[0], a1[1]};
+    };
+    // p of a column tile as operands, and its sum; at[tile]: e less what p is relative to
+    const auto weigh = [&](const f32x4 *x, float mul, const float *at, const float *f, int ct, u32x4 &hi, u32x4 &lo) {
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) {
+            float sum = 0.0f;
 #pragma unroll
-            for (int s = 0; s < NW; ++s) k[tt][s] = now.k[kg][tt][s][lane];
-#pragma unroll
-            for (int i = 0; i < NP; ++i) prm[tt][i] = now.kp[kg][tt][i][lane];
+            for (int i = 0; i < 4; i += 2) {
+                const f32x2 p = {exp2_fast(__builtin_fmaf(x[tt][i], mul, at[tt])), exp2_fast(__builtin_fmaf(x[tt][i + 1], mul, at[tt]))};
+                const f16x2 t2 = __builtin_convertvector(p, f16x2);
+                hi[2 * tt + i / 2] = __builtin_bit_cast(uint32_t, t2);
+                if (TWO) {
+                    const f32x2 r = {p[0] - (float)t2[0], p[1] - (float)t2[1]};
+                    lo[2 * tt + i / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(r, f16x2));
+                } else {
+                    sum = i ? sum + p[0] : p[0];
+                    sum += p[1];
+                }
+            }
+            if (!TWO) l[ct] = __builtin_fmaf(sum, f[tt], l[ct]);
         }
-        const uint32_t some_nan = now.any_nan[kg][0] | now.any_nan[kg][1];
-        __builtin_amdgcn_sched_barrier(0);
-        float y[2][8], top[2];
+    };
+    const auto largest = [&](const f32x4 *x, float mul, const float *e) {
+        float m[2];
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) m[tt] = __builtin_fmaf(fmaxf(fmaxf(x[tt][0], x[tt][1]), fmaxf(x[tt][2], x[tt][3])), mul, e[tt]);
+        return fmaxf(m[0], m[1]);
+    };
+    // A turn with masks, a cap, or the first.
+    const auto work = [&](int t, const T &now, const K &by) {
+        const int key0 = t * 32;
+        if (key0 >= any_hi || key0 + 32 <= any_lo) return;
+        const bool partial = key0 + 32 > j.pos0 || key0 < all_lo;
+        f32x4 x[2][2];
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) {
-            f32x4 x[2], c[2][NG], ks[NG];
+            const u32x4 klo = load_klo(by, tt);
 #pragma unroll
-            for (int g = 0; g < NG; ++g) ks[g] = *(const f32x4 *)&now.ks[kg][tt][g][4 * h];
-            const f32x4 e = *(const f32x4 *)&now.e[kg][tt][4 * h];
+            for (int ct = 0; ct < 2; ++ct) x[ct][tt] = mfma(klo, lds_sums[2 * rg + ct][lane], f32x4{0, 0, 0, 0});
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                f32x4 c[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+                for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) {
+                    const u32x4 k = now.k[tt][s][lane];
+                    c[0] = mfma(k, q[0][s], c[0]);
+                    c[1] = mfma(k, q[1][s], c[1]);
+                }
+                const f32x4 ks = *(const f32x4 *)&by.ks[tt][g][4 * h];
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[ct][tt][i] = __builtin_fmaf(ks[i], c[ct][i], x[ct][tt][i]);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        const float e[2] = {by.e[0], by.e[1]}, f[2] = {by.f[0], by.f[1]};
+        u32x4 hi[2], lo[2];
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct) {
+            float mul = up[ct];
+            if (a.softcap > 0.0f) {
+                float cap = a.softcap;
+                __asm__ volatile("" : "+s"(cap), "+v"(mul));  // or what the cap makes of them is kept in registers
+                cap_logits(cap, x[ct], mul);
+            }
+            uint32_t see = ~0u;  // the lane's keys that its row sees
+            if (partial) {
+                // keys before the tree from k_lo on, and the path's
+                const int tok = toks >> (16 * ct) & 0xFFFF;
+                const int k_lo = a.window ? max(0, j.pos0 + lds_steps[tok] - a.window) : 0;
+                const int n = min(max(j.pos0 - key0, 0), 32), m = min(max(k_lo - key0, 0), 32);
+                see = (uint32_t)((1ull << n) - 1) & ~(uint32_t)((1ull << m) - 1);
+                if (t >= paths.first) see |= lds_bits[tok * paths.words + t - paths.first];
+                see >>= 4 * h;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (!(see >> (16 * (i / 4) + i % 4) & 1)) x[ct][i / 4][i % 4] = -__builtin_inff();
+            }
+            const float top = largest(x[ct], mul, e);
+            float mu = ref[ct] == -__builtin_inff() ? 0.0f : ref[ct];
+            if (__any(top > ref[ct] + 15.0f)) mu = pass_on(ct, top);
+            const float at[2] = {e[0] - mu, e[1] - mu};
+            weigh(x[ct], mul, at, f, ct, hi[ct], lo[ct]);
+            if (by.any_nan[0] | by.any_nan[1]) meet_nan(by, ct, see);
+        }
+#pragma unroll
+        for (int i = 0; i < NZ; ++i) {
+            const u32x4 zo = *(const u32x4 *)&by.z[i][lane][0];
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) {
+                z[ct][i] = mfma(zo, hi[ct], z[ct][i]);
+                if (TWO) z[ct][i] = mfma(zo, lo[ct], z[ct][i]);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+            if (c % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+            u32x4 v[2];
+            load_v(now, c, v);
+#pragma unroll
+            for (int term = 0; term < (TWO ? 3 : 2); ++term)
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct) o[ct][c] = mfma(v[term == 1], term == 2 ? lo[ct] : hi[ct], o[ct][c]);
+        }
+    };
+    // A turn that every row of the wave sees whole, after another and without a cap, and the next one's operands laid out
+    // meanwhile: the matrix unit takes 16 cycles an instruction, of which a wave's vector instructions can have 12.
+    const auto both = [&](const T &now, const K &by, T &to, const K &to_by) {
+        u32x4 k[2][NW];
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+            for (int s = 0; s < NW; ++s) k[tt][s] = now.k[tt][s][lane];
+        const uint32_t some_nan = by.any_nan[0] | by.any_nan[1];
+        const float e[2] = {by.e[0], by.e[1]}, f[2] = {by.f[0], by.f[1]};
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4 x[2][2], c[2][NG], ks[NG];
+        const auto products = [&](int tt) {
 #pragma unroll
             for (int g = 0; g < NG; ++g)
 #pragma unroll
                 for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s)
 #pragma unroll
                     for (int ct = 0; ct < 2; ++ct) c[ct][g] = mfma(k[tt][s], q[ct][s], s == g * (G / 32) ? f32x4{0, 0, 0, 0} : c[ct][g]);
+            const u32x4 klo = load_klo(by, tt);
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct) {
-                x[ct] = mfma(lo_operand<NG>(prm[tt], h), sums[ct], f32x4{0, 0, 0, 0});
+            for (int g = 0; g < NG; ++g) ks[g] = *(const f32x4 *)&by.ks[tt][g][4 * h];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+            for (int ct = 0; ct < 2; ++ct) x[ct][tt] = mfma(klo, lds_sums[2 * rg + ct][lane], f32x4{0, 0, 0, 0});
+        };
+        const auto scaled = [&](int tt) {
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) x[ct][i] = __builtin_fmaf(ks[g][i], c[ct][g][i], x[ct][i]);
-                    y[ct][4 * tt + i] = __builtin_fmaf(x[ct][i], up[ct], e[i]);
-                    top[ct] = tt + i == 0 ? y[ct][0] : fmaxf(top[ct], y[ct][4 * tt + i]);
-                }
-            }
-        }
-        // the first tile's vector work among the second's products
-        __builtin_amdgcn_sched_group_barrier(0x8, 2 * (NW + 1), 0);
+            for (int ct = 0; ct < 2; ++ct)
 #pragma unroll
-        for (int i = 0; i < 2 * (NW + 1); ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x2, 3, 0);
-        }
-        lay_params(t + 1, to);
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) x[ct][tt][i] = __builtin_fmaf(ks[g][i], c[ct][g][i], x[ct][tt][i]);
+        };
+        products(0);
+        __builtin_amdgcn_sched_barrier(0);
+        scaled(0);
+        products(1);
+        __builtin_amdgcn_sched_barrier(0);
+        scaled(1);
+        const float top[2] = {largest(x[0], up[0], e), largest(x[1], up[1], e)};
         if (__any(top[0] > ref[0] + 15.0f || top[1] > ref[1] + 15.0f || some_nan)) {
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) {
                 pass_on(ct, top[ct]);
-                if (some_nan) meet_nan(now, ct, ~0u);
+                if (some_nan) meet_nan(by, ct, ~0u);
             }
         }
-        f32x4 f[2];
-        if (!TWO) f[0] = *(const f32x4 *)&now.f[kg][0][4 * h], f[1] = *(const f32x4 *)&now.f[kg][1][4 * h];
         u32x4 va[2][2][2], zo[NZ], hi[2], lo[2];
 #pragma unroll
-        for (int i = 0; i < NZ; ++i) zo[i] = *(const u32x4 *)&now.z[kg][i][lane][0];
+        for (int i = 0; i < NZ; ++i) zo[i] = *(const u32x4 *)&by.z[i][lane][0];
         load_v(now, 0, va[0][0]);
         load_v(now, 1, va[0][1]);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int ct = 0; ct < 2; ++ct) {
-            const float mu = ref[ct] == -__builtin_inff() ? 0.0f : ref[ct];
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                const f32x2 p = {exp2_fast(y[ct][i] - mu), exp2_fast(y[ct][i + 1] - mu)};
-                const f16x2 t2 = __builtin_convertvector(p, f16x2);
-                hi[ct][i / 2] = __builtin_bit_cast(uint32_t, t2);
-                if (TWO) {
-                    const f32x2 r = {p[0] - (float)t2[0], p[1] - (float)t2[1]};
-                    lo[ct][i / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(r, f16x2));
-                } else {
-                    l[ct] = __builtin_fmaf(p[0], f[i / 4][i % 4], l[ct]);
-                    l[ct] = __builtin_fmaf(p[1], f[i / 4][i % 4 + 1], l[ct]);
-                }
-            }
+            const float mu = ref[ct] == -__builtin_inff() ? 0.0f : ref[ct], at[2] = {e[0] - mu, e[1] - mu};
+            weigh(x[ct], up[ct], at, f, ct, hi[ct], lo[ct]);
         }
         __builtin_amdgcn_sched_barrier(0);
         constexpr int PAIRS = NT / 2, EACH = TWO ? 6 : 4;  // of channel tiles, and a pair's products
@@ -717,7 +818,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_tree_wide(Kv4Attn
         for (int p = 0; p < PAIRS; ++p) {
             // a pair's operands are on their way since the one before
             if (p + 1 < PAIRS) load_v(now, 2 * p + 2, va[(p + 1) & 1][0]), load_v(now, 2 * p + 3, va[(p + 1) & 1][1]);
-            lay_operands(to, p, PAIRS);
+            lay_operands(to, to_by, p, PAIRS);
             if (p == 0)
 #pragma unroll
                 for (int ct = 0; ct < 2; ++ct)
@@ -741,275 +842,134 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_tree_wide(Kv4Attn
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    const auto work = [&](int t, const T &now) {
-        const int blk = t * KG + kg, key0 = blk * 32;
-        if (key0 >= any_hi || key0 + 32 <= any_lo) return;
-        const bool partial = key0 + 32 > j.pos0 || key0 < all_lo;
-        // K's operands: a tile's are on their way while the other's are worked on
-        f32x4 x[2][2];
-        u32x4 k[2][NW];
-        const u32x4 sums[2] = {lds_sums[2 * rg][lane], lds_sums[2 * rg + 1][lane]};
-#pragma unroll
-        for (int s = 0; s < NW; ++s) k[0][s] = now.k[kg][0][s][lane];
-#pragma unroll
-        for (int tt = 0; tt < 2; ++tt) {
-            uint32_t prm[NP];
-            f32x4 ks[NG];
-#pragma unroll
-            for (int i = 0; i < NP; ++i) prm[i] = now.kp[kg][tt][i][lane];
-#pragma unroll
-            for (int g = 0; g < NG; ++g) ks[g] = *(const f32x4 *)&now.ks[kg][tt][g][4 * h];
-            if (tt == 0)
-#pragma unroll
-                for (int s = 0; s < NW; ++s) k[1][s] = now.k[kg][1][s][lane];
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                f32x4 c[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-#pragma unroll
-                for (int s = g * (G / 32); s < (g + 1) * (G / 32); ++s) {
-                    c[0] = mfma(k[tt][s], q[0][s], c[0]);
-                    c[1] = mfma(k[tt][s], q[1][s], c[1]);
-                }
-                if (g == 0) {
-                    const u32x4 klo = lo_operand<NG>(prm, h);
-#pragma unroll
-                    for (int ct = 0; ct < 2; ++ct) x[ct][tt] = mfma(klo, sums[ct], f32x4{0, 0, 0, 0});
-                }
-#pragma unroll
-                for (int ct = 0; ct < 2; ++ct)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[ct][tt][i] = __builtin_fmaf(ks[g][i], c[ct][i], x[ct][tt][i]);
-            }
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        const f32x4 e[2] = {*(const f32x4 *)&now.e[kg][0][4 * h], *(const f32x4 *)&now.e[kg][1][4 * h]};
-        f32x4 f[2];
-        if (!TWO) f[0] = *(const f32x4 *)&now.f[kg][0][4 * h], f[1] = *(const f32x4 *)&now.f[kg][1][4 * h];
-        // V's operands are on their way while the ones before are worked on
-        u32x4 va[2][2][2];
-        load_v(now, 0, va[0][0]);
-        load_v(now, 1, va[0][1]);
-        u32x4 hi[2], lo[2];
-        uint32_t see[2];  // the keys that the lane's row sees, of its own
-#pragma unroll
-        for (int ct = 0; ct < 2; ++ct) {
-            float mul = up[ct], y[8], top = -__builtin_inff();
-            if (a.softcap > 0.0f) {
-                float cap = a.softcap;
-                __asm__ volatile("" : "+s"(cap), "+v"(mul));  // or what the cap makes of them is kept in registers
-                cap_logits(cap, x[ct], mul);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = __builtin_fmaf(x[ct][i / 4][i % 4], mul, e[i / 4][i % 4]);
-            see[ct] = ~0u;
-            if (partial) {
-                // keys before the tree from k_lo on, and the path's
-                const int tok = toks >> (16 * ct) & 0xFFFF;
-                const int k_lo = a.window ? max(0, j.pos0 + lds_steps[tok] - a.window) : 0;
-                const int n = min(max(j.pos0 - key0, 0), 32), m = min(max(k_lo - key0, 0), 32);
-                uint32_t ok = (uint32_t)((1ull << n) - 1) & ~(uint32_t)((1ull << m) - 1);
-                if (blk >= paths.first) ok |= lds_bits[tok * paths.words + blk - paths.first];
-                see[ct] = ok >>= 4 * h;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = ok >> (16 * (i / 4) + i % 4) & 1 ? y[i] : -__builtin_inff();
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, y[i]);
-            if (__any(top > ref[ct] + 15.0f)) pass_on(ct, top);
-            const float mu = ref[ct] == -__builtin_inff() ? 0.0f : ref[ct];
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                const float p0 = exp2_fast(y[i] - mu), p1 = exp2_fast(y[i + 1] - mu);
-                const f32x2 p = {p0, p1};
-                const f16x2 t = __builtin_convertvector(p, f16x2);
-                hi[ct][i / 2] = __builtin_bit_cast(uint32_t, t);
-                if (TWO) {
-                    const f32x2 r = {p0 - (float)t[0], p1 - (float)t[1]};
-                    lo[ct][i / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(r, f16x2));
-                } else {
-                    l[ct] = __builtin_fmaf(p0, f[i / 4][i % 4], l[ct]);
-                    l[ct] = __builtin_fmaf(p1, f[i / 4][i % 4 + 1], l[ct]);
-                }
-            }
-        }
-        if (now.any_nan[kg][0] | now.any_nan[kg][1]) {
-            meet_nan(now, 0, see[0]);
-            meet_nan(now, 1, see[1]);
-        }
-#pragma unroll
-        for (int i = 0; i < NZ; ++i) {
-            const u32x4 zo = *(const u32x4 *)&now.z[kg][i][lane][0];
-#pragma unroll
-            for (int ct = 0; ct < 2; ++ct) {
-                z[ct][i] = mfma(zo, hi[ct], z[ct][i]);
-                if (TWO) z[ct][i] = mfma(zo, lo[ct], z[ct][i]);
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < NT; c += 2) {
-            const int now_v = c / 2 & 1;
-            if (c + 2 < NT) {
-                load_v(now, c + 2, va[now_v ^ 1][0]);
-                load_v(now, c + 3, va[now_v ^ 1][1]);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int term = 0; term < (TWO ? 3 : 2); ++term)
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int ct = 0; ct < 2; ++ct)
-                        o[ct][c + k] = mfma(va[now_v][k][term == 1], term == 2 ? lo[ct] : hi[ct], o[ct][c + k]);
-        }
-    };
+
+    // where the turn's, the next one's and the one's after lie, passed on from turn to turn
+    T *now = turns, *to = turns + 1;
+    K *by = keys, *to_by = keys + 1, *ahead = keys + 2;
     if (turn < t_end) {
-        look_up(turn);
+        // as if the two turns before had been worked on
         fetch(turn);
-        look_up(turn + 1);
-        if (BUFS == 2) lay_out(turn, turns[0]);
+        lay_keys(turn, *by);
+        fetched();
+        fetch(turn + 1);
+        lay_keys(turn + 1, *to_by);
+        lds_barrier();
+        lay_operands(*now, *by, 0, 1);
+        fetched();
     }
-    // what follows from the lane is worked out in each turn: kept, it takes the queries' registers
+    // What follows from the lane is worked out in each turn: kept, it takes the queries' registers.
     const auto begin = [&]() {
         __asm__ volatile("" : "+v"(lane));
         col = lane & 15, h = lane >> 4;
         lds_barrier();
+        fetch(turn + 2);
     };
-    // turns that every row sees whole, without a cap: a loop of their own, in which the sums stay where they are
-    const int from = max(turn, (max(all_lo, 0) + 32 * KG - 1) / (32 * KG));
-    const int to = BUFS == 2 && a.softcap == 0.0f ? min(t_end, max(j.pos0, 0) / (32 * KG)) : 0;
-    int side = 0;
+    const auto end = [&]() {
+        fetched();
+        ++turn;
+        T *const t0 = now;
+        now = to, to = t0;
+        K *const k0 = by;
+        by = to_by, to_by = ahead, ahead = k0;
+    };
+    // Turns that every row sees whole, without a cap: a loop of their own, in which the sums stay where they are.
+    const int from = max(turn + 1, (max(all_lo, 0) + 31) / 32);
+    const int until = a.softcap == 0.0f ? min(t_end, max(j.pos0, 0) / 32) : 0;
     while (turn < t_end) {
-        if (turn >= from && turn < to) {
+        if (turn >= from && turn < until) {
+            // a wave without rows unpacks only
             if (row_w < j.rows) {
-                for (; turn < to; ++turn, side ^= 1) {
+                while (turn < until) {
                     begin();
-                    fetch(turn + 1);
-                    look_up(turn + 2);
-                    both(turn, turns[side], turns[side ^ 1]);
+                    both(*now, *by, *to, *to_by);
+                    if (d0 == 0) lay_keys(turn + 2, *ahead);
+                    end();
                 }
             } else {
-                for (; turn < to; ++turn, side ^= 1) {
+                while (turn < until) {
                     begin();
-                    fetch(turn + 1);
-                    look_up(turn + 2);
-                    lay_out(turn + 1, turns[side ^ 1]);
+                    lay_operands(*to, *to_by, 0, 1);
+                    if (d0 == 0) lay_keys(turn + 2, *ahead);
+                    end();
                 }
             }
             continue;
         }
         begin();
-        if (BUFS == 1) {
-            lay_out(turn, turns[0]);
-            lds_barrier();
-        }
-        fetch(turn + 1);  // past the end: the last tile again
-        look_up(turn + 2);
-        work(turn, turns[side]);
+        work(turn, *now, *by);
         // the other side: nobody reads it before the next barrier, nor since the last
-        if (BUFS == 2) lay_out(turn + 1, turns[side ^ 1]);
-        ++turn, side ^= BUFS - 1;
+        lay_operands(*to, *to_by, 0, 1);
+        if (d0 == 0) lay_keys(turn + 2, *ahead);
+        end();
     }
-    if (bad_page && lane == 0) kvc_flag(a.pool.status, KVC_DEV_BAD_INDEX);
+    if (bad_page) kvc_flag(a.pool.status, KVC_DEV_BAD_INDEX);
 
-    // a row's sums, in the lanes that hold its channels
-    lds_barrier();
-    float L[2];
 #pragma unroll
     for (int ct = 0; ct < 2; ++ct) {
+        // a row's sums, in the lanes that hold its channels
         const int at_l = 2 * NG % 16;
         const float lhat = __shfl(z[ct][NZ - 1][at_l % 4], col + 16 * (at_l / 4), 64);
-        L[ct] = TWO ? lhat : row_sum(l[ct]);
-        // p's one term: an average with the weights as they were rounded, times the sum of those that were not
-        const float fix = TWO || lhat == 0.0f ? 1.0f : L[ct] / lhat;
-        const uint32_t met = lds_nan[32 * rg + 16 * ct + col];
+        const float L = TWO ? lhat : row_sum(l[ct]);
+        const uint32_t met = lds_nan[16 * (2 * rg + ct) + col];  // by this wave alone
+        const int row = row_w + 16 * ct + col;
+        const int head = j.h * a.R + row % a.R;
+        const int64_t tok = j.q0 + row / a.R, grow = tok * a.Hq + head;
+        const int64_t prow = (int64_t)j.split * a.n_q * a.Hq + grow;
+        // p's one term: an average with the weights as they were rounded; for a join, times the sum of those that were not
+        const float inv = a.ns > 1 ? (TWO || lhat == 0.0f ? 1.0f : L / lhat) : (lhat == 0.0f ? 0.0f : 1.0f / lhat);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             const f32x4 zg = z[ct][g / 8];
             float mid = __shfl(g & 1 ? zg[2] + zg[3] : zg[0] + zg[1], col + 16 * (g % 8 / 2), 64);
             if (met >> g & 1) mid = __builtin_nanf("");
 #pragma unroll
-            for (int c = g * (G / 16); c < (g + 1) * (G / 16); ++c)
+            for (int c = g * (G / 16); c < (g + 1) * (G / 16); ++c) {
+                f32x4 y;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[ct][c][i] = (o[ct][c][i] + mid) * fix;
+                for (int i = 0; i < 4; ++i) y[i] = (o[ct][c][i] + mid) * inv;
+                if (row >= j.rows) continue;
+                if (a.ns > 1)
+                    *(f32x4 *)(a.part_o + prow * D + 16 * c + 4 * h) = y;
+                else
+                    store_out<BF>(a, tok, head, 16 * c + 4 * h, y);
+            }
         }
-    }
-    // the groups of keys joined: the others hand theirs to the first
-    if constexpr (KG > 1) {
-        static_assert(KG == 2, "one hands over");
-        f32x4 *const part = (f32x4 *)lds_raw + rg * (2 * NT + 1) * 64;
-        static_assert(RG * (2 * NT + 1) * 64 * 16 <= sizeof(T), "the parts fit where the operands were");
-        lds_barrier();
-        if (kg == 1) {
-#pragma unroll
-            for (int ct = 0; ct < 2; ++ct)
-#pragma unroll
-                for (int c = 0; c < NT; ++c) part[(ct * NT + c) * 64 + lane] = o[ct][c];
-            part[2 * NT * 64 + lane] = f32x4{ref[0], L[0], ref[1], L[1]};
-        }
-        lds_barrier();
-        if (kg == 1) return;
-        const f32x4 ml = part[2 * NT * 64 + lane];
-#pragma unroll
-        for (int ct = 0; ct < 2; ++ct) {
-            const float M = fmaxf(ref[ct], ml[2 * ct]);
-            const float w0 = ref[ct] == -__builtin_inff() ? 0.0f : exp2_fast(ref[ct] - M);
-            const float w1 = ml[2 * ct] == -__builtin_inff() ? 0.0f : exp2_fast(ml[2 * ct] - M);
-#pragma unroll
-            for (int c = 0; c < NT; ++c) o[ct][c] = w0 * o[ct][c] + w1 * part[(ct * NT + c) * 64 + lane];
-            L[ct] = w0 * L[ct] + w1 * ml[2 * ct + 1];
-            ref[ct] = M;
-        }
-    }
-#pragma unroll
-    for (int ct = 0; ct < 2; ++ct) {
-        const int row = row_w + 16 * ct + col;
-        if (row >= j.rows) continue;
-        const int head = j.h * a.R + row % a.R;
-        const int64_t tok = j.q0 + row / a.R, grow = tok * a.Hq + head;
-        const int64_t prow = (int64_t)j.split * a.n_q * a.Hq + grow;
-        const float inv = a.ns > 1 ? 1.0f : (L[ct] == 0.0f ? 0.0f : 1.0f / L[ct]);
-#pragma unroll
-        for (int c = 0; c < NT; ++c) {
-            const f32x4 y = o[ct][c] * inv;
-            if (a.ns > 1)
-                *(f32x4 *)(a.part_o + prow * D + 16 * c + 4 * h) = y;
-            else
-                store_out<BF>(a, tok, head, 16 * c + 4 * h, y);
-        }
-        if (h == 0) {
+        if (h == 0 && row < j.rows) {
             if (a.ns > 1) {
                 a.part_ml[prow * 2] = ref[ct];
-                a.part_ml[prow * 2 + 1] = L[ct];
+                a.part_ml[prow * 2 + 1] = L;
             } else if (a.lse) {
-                a.lse[grow] = lse_of(ref[ct], L[ct]);
+                a.lse[grow] = lse_of(ref[ct], L);
             }
         }
     }
 }
 
-template <int D, int G, bool BF, int RG>
+template <int D, int G, bool BF>
 hipError_t attend_wide(const Kv4Attn &a, dim3 grid, hipStream_t s)
 {
-    constexpr int rows = 32 * RG, turns = sizeof(Turn<D, G, 4 / RG>) * (RG == 4 ? 2 : 1);
-    const int lds = turns + 2 * rows + (a.max_q + 1) / 2 * 4 + 4 * rows * ((a.max_q + 62) / 32);
+    const int lds = 2 * sizeof(Turn<D, G>) + kAhead * sizeof(Keys<D, G>) + 2 * kTreeRows + (a.max_q + 1) / 2 * 4 +
+                    4 * kTreeRows * ((a.max_q + 62) / 32);
     // above 64 KB LDS has to be asked for; the attribute is per device, and cheap
-    const hipError_t e = hipFuncSetAttribute((const void *)k_kv4_tree_wide<D, G, BF, RG>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    const hipError_t e = hipFuncSetAttribute((const void *)k_kv4_tree_wide<D, G, BF>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
-    k_kv4_tree_wide<D, G, BF, RG><<<grid, dim3(256), lds, s>>>(a);
+    k_kv4_tree_wide<D, G, BF><<<grid, dim3(256), lds, s>>>(a);
     return hipGetLastError();
 }
+
+// Which shapes the wide blocks are faster for, measured over 16 sequences of up to 8192 keys, 8 KV heads, trees of 128
+// rows (8 sequences with D = 256): D = 128 G = 32, 64, 128: 133, 121, 118 us, tiles of 32 rows 180, 149, 129; G = 32 with
+// D = 64: 97, 120, with D = 256: 341, 419.  The others: D = 64 G = 64: 92, 88; D = 256 G = 64, 128: 228, 200 and 214, 174.
+constexpr bool has_wide(int D, int G) { return D == 128 || G == 32; }
 
 template <int D, int G, bool BF>
 hipError_t attend(const Kv4Attn &a, hipStream_t s)
 {
     const dim3 grid((uint32_t)((int64_t)a.ns * a.pool.H * a.B * a.tiles)), block(64 * kWaves);
-    hipError_t e;
-    if (a.rows == 128)
-        e = attend_wide<D, G, BF, 4>(a, grid, s);
-    else if (a.rows == 64)
-        e = attend_wide<D, G, BF, 2>(a, grid, s);
-    else {
+    hipError_t e = hipErrorInvalidValue;
+    if (a.rows == kTreeRows) {
+        if constexpr (has_wide(D, G)) e = attend_wide<D, G, BF>(a, grid, s);
+    } else {
         if (a.rows == 32)
             k_kv4_tree<D, G, BF, 2><<<grid, block, 0, s>>>(a);
         else
@@ -1033,12 +993,22 @@ hipError_t attend_dt(const Kv4Attn &a, bool bf16, hipStream_t s)
     return bf16 ? attend<D, G, true>(a, s) : attend<D, G, false>(a, s);
 }
 
-int64_t splits(const Kv4Pool &p, int64_t blocks, int64_t keys)
+// As many parts of the keys as fill the chip, for each level (blocks, keys of a part at the nearest): a part costs its share
+// of the join and of what a block does once.
+//   Tiles of up to 32 rows.  {256, 256}: 24 blocks of 2048 keys 20 us in 8 parts, 23 in 4.  {512, 512}: 64 of 4096 31 in 8,
+// 31 in 4, 43 in 2.  {1536, 2048}, since blocks' lengths differ: 384 of 8192 120 in 4, 122 in 2, 139 in 8; 512 of 8192
+// 149 in 3, 180 in 8, 191 in 1; 396 of a window of 2060 59 in 1, 64 in 2; 120 of 80000 433 in 8, 439 in 4, 454 in 16.
+//   Blocks of 128 rows.  {512, 512}: 128 of 8192 121 in 4, 168 in 3, 131 in 8; 32 of 80000 358 in 16, 501 in 8.
+// {1024, 2048} for sequences of several lengths: 128 of 16000 259 in 8, 311 in 4; of a single one 64 of 30000
+// 267 in 8, 285 in 16.
+int64_t splits(bool wide, bool several, int64_t blocks, int64_t keys)
 {
+    typedef std::pair<int64_t, int64_t> Level;
+    const Level last = wide ? several ? Level{1024, 2048} : Level{512, 512} : Level{1536, 2048};
     int64_t ns = 1;
     if (keys > 512)
-        for (const auto &l : {std::pair<int64_t, int64_t>{256, 256}, {512, 512}})
-            ns = std::max(ns, std::min(l.first / blocks, (keys + l.second - 1) / l.second));
+        for (const Level &l : {Level{256, 256}, Level{512, 512}, last})
+            ns = std::max(ns, std::min(l.first / blocks, (keys + l.second / 2) / l.second));
     return std::min<int64_t>(ns, 128);
 }
 
@@ -1047,15 +1017,19 @@ int64_t splits(const Kv4Pool &p, int64_t blocks, int64_t keys)
 Kv4Plan kv4_tree_plan(const Kv4Pool &p, int64_t n_seqs, int R, int64_t max_q, int64_t max_keys, int64_t window)
 {
     Kv4Plan plan = {};
-    const int64_t most = max_q * R;
-    const int rows = most > 64 ? 128 : most > 32 ? 64 : most > 16 ? 32 : 16;
-    plan.rows = rows;
-    plan.tiles = (int32_t)((max_q * R + rows - 1) / rows);
-    const int64_t blocks = std::max<int64_t>(n_seqs * p.H * plan.tiles, 1);
+    const int64_t most = std::max<int64_t>(max_q * R, 1), narrow = most > 16 ? 32 : 16, heads = std::max<int64_t>(n_seqs, 1) * p.H;
+    const int64_t tiles = (most + narrow - 1) / narrow, wide_tiles = (most + kTreeRows - 1) / kTreeRows;
     // a window reaches back from the tree's first token, and its keys go on to the last
     const int64_t keys = window ? std::min(max_keys, window + max_q) : max_keys;
-    plan.ns = (int32_t)splits(p, blocks, keys);
-    plan.most_ns = (int32_t)splits(p, blocks, max_keys);
+    // blocks of 128 rows where at least 7/8 of their waves have rows (three of four: 115 us for 120, and 201 for 167 with
+    // D = 256) and the keys fill the chip (8 heads of 2 sequences of 2000 keys: 26 us for 21)
+    const bool wide = has_wide(p.D, p.G) && tiles * 8 >= wide_tiles * 28 && heads * wide_tiles * ((keys + 511) / 512) >= 512;
+    plan.rows = wide ? kTreeRows : (int32_t)narrow;
+    plan.tiles = (int32_t)(wide ? wide_tiles : tiles);
+    plan.ns = (int32_t)splits(wide, n_seqs > 1, heads * plan.tiles, keys);
+    // a shorter window may make the blocks narrow
+    plan.most_ns = (int32_t)splits(false, n_seqs > 1, heads * tiles, max_keys);
+    if (wide) plan.most_ns = (int32_t)std::max<int64_t>(plan.most_ns, splits(true, n_seqs > 1, heads * wide_tiles, max_keys));
     return plan;
 }
 

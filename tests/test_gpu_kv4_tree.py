@@ -1,8 +1,8 @@
 """kvc_kv4_tree_attention on the GPU against 64 bits, over trees of every kind.
 
 Tolerance: that of test_gpu_kv4.py, whose derivation holds for these kernels (the logits are the same; p s, or p, enters as
-two fp16 terms, nearer than the bf16 ones counted there), and one more for bf16 outputs of trees of more than 32 rows, where p
-is one fp16 term: with p_j (1 + d_j), |d_j| <= 2^-11 (fp16's half step), in the sum that divides too,
+two fp16 terms, nearer than the bf16 ones counted there), and one more for bf16 outputs of trees of more than 32 rows, whose p
+may be one fp16 term: with p_j (1 + d_j), |d_j| <= 2^-11 (fp16's half step), in the sum that divides too,
     out' - out = sum_j p_j d_j (v_j - out) / sum_j p_j (1 + d_j),
 at most 2^-11 / (1 - 2^-11) of sum_j p_j |v_j - out|, p normalised."""
 import math
