@@ -1,10 +1,12 @@
 """kvc_kv4_tree_attention on the GPU against 64 bits, over trees of every kind.
 
-Tolerance: that of test_gpu_kv4.py, whose derivation holds for these kernels (the logits are the same; p s, or p, enters as
-two fp16 terms, nearer than the bf16 ones counted there), and one more for bf16 outputs of trees of more than 32 rows, whose p
-may be one fp16 term: with p_j (1 + d_j), |d_j| <= 2^-11 (fp16's half step), in the sum that divides too,
-    out' - out = sum_j p_j d_j (v_j - out) / sum_j p_j (1 + d_j),
-at most 2^-11 / (1 - 2^-11) of sum_j p_j |v_j - out|, p normalised."""
+Tolerance: that of test_gpu_kv4.py, whose derivation holds for these kernels (the logits are the same; for fp16 outputs p s, or
+p, enters as two fp16 terms, nearer than the bf16 ones counted there), and one more for bf16 outputs, where p s, or p, is one
+fp16 term, off by d_j, |d_j| <= 2^-11 (fp16's half step):
+of p s in tiles of up to 32 rows, p normalised and v_j = mid_j + s_j (n_j - 7.5),
+    out' - out = sum_j p_j s_j d_j (n_j - 7.5), at most 2^-11 * 7.5 max s;
+of p in blocks of 128 rows, in the sum that divides too,
+    out' - out = sum_j p_j d_j (v_j - out) / sum_j p_j (1 + d_j), at most 2^-11 / (1 - 2^-11) of sum_j p_j |v_j - out|."""
 import math
 
 import numpy as np
@@ -66,8 +68,11 @@ def compare(out, lse, q, ref, slots, lens, pars, R, dt, window, softcap, scale):
             smax, vmax = ref.s[1, slots[b], h].astype(np.float64).max(), np.abs(v).max()
             steps = (l / 32 + 64) * 2.0 ** -24
             tol = EPS[dt] / 2 * np.abs(wo) + (2 * delta * vmax + 31 * 2.0 ** -18 * smax + steps * (vmax + 31 * smax))[..., None]
-            if dt == "bf16" and max(len(p) for p in pars) * R > 32:
-                tol += 2.0 ** -11 / (1 - 2.0 ** -11) * spec.spread(q64[a:a + n, hs], k, v, ok, softcap, scale)
+            if dt == "bf16":
+                off = 7.5 * smax
+                if max(len(p) for p in pars) * R > 32:
+                    off = np.maximum(off, spec.spread(q64[a:a + n, hs], k, v, ok, softcap, scale))
+                tol += 2.0 ** -11 / (1 - 2.0 ** -11) * off
             assert (np.abs(got - wo) <= tol)[~empty].all(), (b, h, np.abs(got - wo).max(), tol.min())
             assert (np.abs(gl[~empty] - wl[~empty]) <= (delta + steps * (np.abs(np.where(empty, 0, wl)) + 1))[~empty]).all(), (b, h)
         a += n
@@ -154,7 +159,7 @@ def test_long_keys_are_split(dt, lens, nqs):
 @pytest.mark.parametrize("D,G", [(64, 32), (128, 128), (256, 64)])
 def test_a_chain_is_causal_attention(D, G):
     """The outputs of kv4_attention: both near the same value, a step of the type apart at most where it lies between two,
-    and what p in one term may move it by (above)."""
+    and what one term of p s or of p may move it by (above)."""
     import torch
     lens, nq = [500, 129, 64], 20
     cache, ref, table, slots = build(2, D, G, 32, lens, "bf16", 19)
@@ -169,7 +174,8 @@ def test_a_chain_is_causal_attention(D, G):
                 at, hs = slice(i * nq, (i + 1) * nq), slice(4 * hd, 4 * hd + 4)
                 k, v = ref.value(0, slots[i])[:, hd], ref.value(1, slots[i])[:, hd]
                 ok = spec.sees(list(range(-1, nq - 1)), l, kw.get("window", 0))
-                moved[at, hs] = torch.from_numpy(spec.spread(q[at, hs].double().cpu().numpy(), k, v, ok, kw.get("softcap", 0.0), D ** -0.5))
+                spread = spec.spread(q[at, hs].double().cpu().numpy(), k, v, ok, kw.get("softcap", 0.0), D ** -0.5)
+                moved[at, hs] = torch.from_numpy(np.maximum(spread, 7.5 * float(ref.s[1, slots[i], hd].max())))
         moved = moved.cuda() * (2.0 ** -11 / (1 - 2.0 ** -11))
         assert ((a.double() - b.double()).abs() <= 2.0 ** -7 * b.double().abs() + 1e-6 + moved).all()
         assert ((la - lb).abs() <= 2.0 ** -20 * (lb.abs() + 1)).all()
@@ -297,7 +303,9 @@ def test_tiny_and_huge_values(dt):
 
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 def test_sums_over_many_keys_keep_every_key(dt):
-    """Near enough to 64 bits that a lost key among thousands shows (kv4_close)."""
+    """Near enough to 64 bits that a lost key among thousands shows (kv4_close).  bf16's one term: roundings of 2^-11 at most,
+    to either side, of shares sum_j p_j^2 <= 1/1000 of which moves an output by some 2^-12 * 0.5 / sqrt(1000) = 2^-18, well below
+    what kv4_close allows in the mean."""
     import kv4_close
     import torch
     from test_gpu_kv4 import f32
