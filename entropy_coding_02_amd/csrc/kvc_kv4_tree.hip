@@ -2,8 +2,8 @@
 // 4-bit cache.
 //
 // The arithmetic is that of kvc_kv4_attn.hip (codes as matrix operands, s and lo
-// outside of them, p s as two fp16 terms, for bf16 outputs one); what differs is which
-// keys a row sees and how many rows there are: a tree's tokens times the heads of a group,
+// outside of them, p s as two fp16 terms); what differs is which keys a row sees
+// and how many rows there are: a tree's tokens times the heads of a group,
 // typically 32 to 512, all over the same keys.  A wave therefore works on
 // CT tiles of 16 rows at once and unpacks a block of 32 keys once for all of them.
 //
@@ -69,9 +69,6 @@ template <int D, int G, bool BF, int CT>
 __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv4_tree(Kv4Attn a)
 {
     constexpr int NW = D / 32, NG = D / G, NT = D / 16, NP = Stage<D, G>::NP, TILE = 64 * NP, ROWS = 16 * CT;
-    // Terms of p s.  One is off by 2^-11 of itself at most: out by 2^-11 sum_j p_j |v_j - mid_j|, an eighth of a bf16 rounding
-    // of what is summed; sum_j p_j mid_j and the sum that divides are fp32.
-    constexpr bool TWO = !BF;
     // Each wave's results, a tile of rows at a time; while it runs, its parameters (as in
     // k_kv4_attn).
     __shared__ __align__(16) float lds_o[kWaves][16][D];
@@ -278,7 +275,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv4_tree(Kv4A
                         const f32x2 a2 = {p0 * s0, p1 * s1};
                         const f16x2 t = __builtin_convertvector(a2, f16x2);
                         hi[ct][i / 2] = __builtin_bit_cast(uint32_t, t);
-                        if (TWO) lo[ct][i / 2] = rest_of(a2, t);
+                        lo[ct][i / 2] = rest_of(a2, t);
                     }
                 }
 #pragma unroll
@@ -296,7 +293,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv4_tree(Kv4A
                         o[ct][c + 1] = mfma(va[1], hi[ct], o[ct][c + 1]);
                     }
 #pragma unroll
-                    for (int ct = 0; ct < (TWO ? CT : 0); ++ct) {
+                    for (int ct = 0; ct < CT; ++ct) {
                         o[ct][c] = mfma(va[0], lo[ct], o[ct][c]);
                         o[ct][c + 1] = mfma(va[1], lo[ct], o[ct][c + 1]);
                     }
@@ -305,9 +302,9 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv4_tree(Kv4A
             blk += kWaves;
         };
         // Blocks that every row sees whole in a loop of their own, two at a time: sums and keys then stay in their registers.
-        // Where registers are short already the second loop costs more: 16 sequences of up to 8192 keys, 8 KV heads, 128 rows,
-        // D = 128 G = 64 128 us (without 137), G = 32 225 (180); 8 sequences with D = 256, G = 32 551 (419), G = 64 236 (200);
-        // 64 sequences of 16 rows, which lose a third wave a SIMD, 141 (129).
+        // Where registers are short already the second loop costs more: 16 sequences of up to 8192 keys, 8 KV heads, trees of
+        // 96 rows, D = 128 G = 64 119 us (without 123); of 128 rows G = 32 225 (180); 8 sequences with D = 256, G = 32 551 (419),
+        // G = 64 236 (200); 64 sequences of 16 rows, which lose a third wave a SIMD, 141 (129).
         constexpr bool APART = CT > 1 && D <= 128 && 64 * D <= 128 * G;
         const int from = (max(all_lo, 0) + 31) / 32, until = min(b_end, max(j.pos0, 0) / 32);
         while (blk < b_end) {
@@ -384,15 +381,15 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv4_tree(Kv4A
 
 // ------------------------------------------------------------- many rows
 
-// Blocks of 128 rows where that many can be had and groups are small (kv4_tree_plan): four waves of 32 rows share 32 keys
-// a turn, which they unpack together, once, into matrix operands in LDS while they work on the turn before.
-// Bound by the vector and matrix units' issue: with D = 128 a wave's turn is some 300 vector, 54 matrix and 50 LDS
-// instructions, of two waves a SIMD.  60 tokens of 8 heads a KV head, 80000 keys, 8 KV heads, D = 128, bf16: 393 us,
-// 0.40 PFLOP/s of products (tiles of 32 rows 481 us).  Tried and not better: blocks of 64 rows and two times 32 keys (210 us,
-// these 125, of 16 sequences of up to 8192 keys, G = 64), waves of 64 rows (130 to 380 registers spilled, 855 us).
+// Blocks of 128 rows where that many can be had (kv4_tree_plan): four waves of 32 rows share 32 keys a turn,
+// which they unpack together, once, into matrix operands in LDS while they work on the turn before.
+// Bound by the vector and matrix units' issue: with D = 128 G = 64 a wave's turn is some 300 vector, 54 matrix and 50 LDS
+// instructions, of two waves a SIMD.  60 tokens of 8 heads a KV head, 80000 keys, 8 KV heads, bf16: 357 us, 0.44 PFLOP/s of
+// products (tiles of 32 rows 403 us).  Tried and not better: blocks of 64 rows and two times 32 keys (210 us, these
+// 125, of 16 sequences of up to 8192 keys), waves of 64 rows (130 to 380 registers spilled, 855 us).
 //
 // Here V's s is in its operand: v - mid = s (n - 7.5) is 15 bits, two fp16 terms, so that p is one operand
-// for all groups instead of p s and a sum of p mid for each, of bf16 2.5 vector instructions a probability and group:
+// for all groups instead of p s and a sum of p mid for each (4 vector instructions a probability and group):
 //   o_c = sum_j p_j (hi + lo)_jc,   and one more product with the rows mid_g (two terms each) and
 //   "1" gives sum_j p_j mid_jg and sum_j p_j.
 // The rows of 16 keys are scaled by f, a power of two that takes their largest value to 2^8, and
@@ -400,7 +397,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv4_tree(Kv4A
 // whatever other keys' sizes.
 // bf16 outputs: p in one fp16 term, the sum that divides included, so that they are exact
 // averages whose weights are off by 2^-11 of themselves at most: 2^-11 sum_j p_j |v_j - out| / sum_j p_j,
-// an eighth of a bf16 rounding of what is averaged.  fp16 outputs: two terms, 22 bits.
+// an eighth of a bf16 rounding of what is averaged, channel by channel (one term of p s would be off by a share
+// of s, which one outlying channel makes large for its whole group).  fp16 outputs: two terms, 22 bits.
 // lse is from unrounded p either way (two terms are as good).
 constexpr int kTreeRows = 128;
 
@@ -436,7 +434,7 @@ constexpr int kAhead = 3;      // turns' Keys: one read, one read to unpack V by
 template <int D, int G, bool BF>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_tree_wide(Kv4Attn a)
 {
-    static_assert(D >= 128 && D / G >= 4, "a wave unpacks whole pairs of V's dwords, and lanes have groups of their own");
+    static_assert(D >= 128, "a wave unpacks whole pairs of V's dwords");
     constexpr int NW = D / 32, NG = D / G, NT = D / 16, NP = (NG + 3) / 4, ND = NW / 2;
     constexpr bool TWO = !BF;                          // terms of p
     typedef Turn<D, G> T;
@@ -530,10 +528,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_tree_wide(Kv4Attn
         bad_page |= entry >= wat.n_pages;
         pages = entry < wat.n_pages ? entry : 0;
     };
-    // a lane has the parameters of key `col`, group h (and h + 4)
+    // a lane has the parameters of key `col`, group g_l (and g_l + 4)
+    const auto group_l = [&](int h) { return NG == 1 ? 0 : NG == 2 ? h & 1 : h; };
     const uint32_t k_at = col * (D / 2) + h * (D / 8) + 4 * d0;
     const uint32_t v_at = h * (2 * D) + col * (D / 8) + ((uint32_t)a.pool.H << a.pool.pshift) * (D / 2) + 4 * d0;
-    const uint32_t p_at = (((uint32_t)h << a.pool.pshift) + col) * 4, to_v = ((uint32_t)(a.pool.H * NG) << a.pool.pshift) * 4;
+    const uint32_t p_at = (((uint32_t)group_l(h) << a.pool.pshift) + col) * 4, to_v = ((uint32_t)(a.pool.H * NG) << a.pool.pshift) * 4;
     const int turn0 = turn;
     const auto fetch = [&](int t) {
         const int i = t - turn0;
@@ -564,10 +563,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_tree_wide(Kv4Attn
         bool is_nan[NP], some = false;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            const int g = h + 4 * i;
+            const int g = group_l(h) + 4 * i;
             const uint32_t w = in ? kp[i] : 0, lo = w >> 16;
             to.ks[tile][g][col] = s_of(w);
-            to.klo[i][tile][col + 16 * h] = u32x2{lo | lo << 16, lo};
+            to.klo[i][tile][col + 16 * group_l(h)] = u32x2{lo | lo << 16, lo};
             const uint32_t x = in ? vp[i] : 0;
             s[i] = s_of(x);
             mid[i] = mid_of(x);
@@ -577,13 +576,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_tree_wide(Kv4Attn
             s[i] = is_nan[i] ? 0.0f : s[i];
             top = fmaxf(top, __builtin_fmaf(7.5f, s[i], __builtin_fabsf(mid[i])));
         }
-        {
+        if (NG > 1) {
             const uint32_t b = __builtin_bit_cast(uint32_t, top);
             const auto x = __builtin_amdgcn_permlane16_swap(b, b, false, false);
             const uint32_t x0 = x[0], x1 = x[1];
             top = fmaxf(__builtin_bit_cast(float, x0), __builtin_bit_cast(float, x1));
         }
-        {
+        if (NG > 2) {
             const uint32_t b = __builtin_bit_cast(uint32_t, top);
             const auto x = __builtin_amdgcn_permlane32_swap(b, b, false, false);
             const uint32_t x0 = x[0], x1 = x[1];
@@ -595,7 +594,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_tree_wide(Kv4Attn
         const float f = __builtin_bit_cast(float, (uint32_t)(127 + 8 - e) << 23);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            const int g = h + 4 * i;
+            const int g = group_l(h) + 4 * i;
             to.s[tile][g][col] = (uint16_t)kvc_f2h(s[i] * f * 512.0f);
             const float m = mid[i] * f;
             const uint32_t hi = kvc_f2h(m);
@@ -980,11 +979,10 @@ hipError_t attend_wide(const Kv4Attn &a, dim3 grid, hipStream_t s)
     return hipGetLastError();
 }
 
-// Which shapes the wide blocks are faster for: many groups, for each of which the tiles weigh p anew.  16 sequences of up to
-// 8192 keys, 8 KV heads, trees of 128 rows (8 sequences with D = 256): D = 128 G = 32 133 us, tiles of 32 rows 169; D = 256
-// G = 32 341, 376.  The others: D = 64 G = 32, 64: 97, 93 and 93, 80; D = 128 G = 64, 128: 121, 126 and 117, 108, and of a
-// single sequence of 30000 keys 253, 228; D = 256 G = 64: 228, 180.
-constexpr bool has_wide(int D, int G) { return G == 32 && D >= 128; }
+// Which shapes the wide blocks are faster for (16 sequences of up to 8192 keys, 8 KV heads, trees of 128 rows; 8 sequences
+// with D = 256): D = 128 G = 32, 64, 128: 133, 121, 118 us, tiles of 32 rows 180, 140, 124; D = 256 G = 32 341, 419.
+// The others: D = 64 G = 32, 64: 97, 100 and 93, 86; D = 256 G = 64: 228, 200.
+constexpr bool has_wide(int D, int G) { return D == 128 || (D == 256 && G == 32); }
 
 template <int D, int G, bool BF>
 hipError_t attend(const Kv4Attn &a, hipStream_t s)
@@ -1022,9 +1020,9 @@ hipError_t attend_dt(const Kv4Attn &a, bool bf16, hipStream_t s)
 //   Tiles of up to 32 rows.  {256, 256}: 24 blocks of 2048 keys 22 us in 8 parts, 23 in 4, 28 in 2; 16 of 32768 40 in 32,
 // 49 in 12.  {512, 512}: 64 of 8192 40 in 8, 61 in 2, 54 in 16.  {1536, 2048}, since blocks' lengths differ: 256 of 8192
 // 79 in 4, 85 in 2, 108 in 8; 512 of 8192 128 in 3, 144 in 1, 178 in 8; 396 of a window of 2060 55 in 1, 60 in 2.
-//   Blocks of 128 rows.  {512, 512}: 128 of 8192 133 in 4, 183 in 3, 145 in 8; 32 of 80000 393 in 16, 532 in 8.
-// {1024, 2048} for sequences of several lengths (G = 64: 128 of 16000 259 in 8, 312 in 4); of a single one 64 of 30000
-// 294 in 8, 310 in 16.
+//   Blocks of 128 rows.  {512, 512}: 128 of 8192 121 in 4, 166 in 3, 132 in 8; 32 of 80000 358 in 16, 498 in 8.
+// {1024, 2048} for sequences of several lengths: 128 of 16000 259 in 8, 312 in 4; of a single one 64 of 30000
+// 267 in 8, 284 in 16.
 int64_t splits(bool wide, bool several, int64_t blocks, int64_t keys)
 {
     typedef std::pair<int64_t, int64_t> Level;
@@ -1045,8 +1043,8 @@ Kv4Plan kv4_tree_plan(const Kv4Pool &p, int64_t n_seqs, int R, int64_t max_q, in
     const int64_t tiles = (most + narrow - 1) / narrow, wide_tiles = (most + kTreeRows - 1) / kTreeRows;
     // a window reaches back from the tree's first token, and its keys go on to the last
     const int64_t keys = window ? std::min(max_keys, window + max_q) : max_keys;
-    // blocks of 128 rows where at least 7/8 of their waves have rows (three of four: 123 us for 140, but 323 for 316 with
-    // D = 256) and the keys fill the chip (8 heads of 2 sequences of 2000 keys: 26 us for 23)
+    // blocks of 128 rows where the longest tree gives at least 7/8 of their waves rows (three of four: trees of up to 96 rows
+    // 137 us for 124, since most are smaller) and the keys fill the chip (8 heads of 2 sequences of 2000 keys: 26 us for 23)
     const bool wide = has_wide(p.D, p.G) && tiles * 8 >= wide_tiles * 28 && heads * wide_tiles * ((keys + 511) / 512) >= 512;
     plan.rows = wide ? kTreeRows : (int32_t)narrow;
     plan.tiles = (int32_t)(wide ? wide_tiles : tiles);

@@ -1,5 +1,5 @@
-"""kvc_kv4_tree_attention on the GPU with trees of many rows: blocks of 128 rows, which the kernel takes with groups of 32 where at least
-7/8 of their waves have rows and the tables' keys fill the chip, here by tables far wider than the sequences are long.
+"""kvc_kv4_tree_attention on the GPU with trees of many rows: blocks of 128 rows, which the kernel takes where 7/8 of
+their waves have rows and the tables' keys fill the chip, here by tables far wider than the sequences are long.
 
 Tolerance: test_gpu_kv4_tree.py's, which counts p's one term for bf16."""
 import math
@@ -11,7 +11,7 @@ import entropy_coding_02_amd as kvc
 import kv4_spec_ref as spec
 from gpu_util import say
 from test_gpu_kv4 import build, draw, f32, fresh, status, tdt
-from test_gpu_kv4_tree import call, check, compare, ints, trees
+from test_gpu_kv4_tree import call, check, compare, ints, outlying, trees
 
 pytestmark = pytest.mark.gpu
 
@@ -26,7 +26,7 @@ def roomy(table, H, P, rows):
     return wide
 
 
-@pytest.mark.parametrize("H,D,G,P", [(2, 128, 32, 16), (1, 128, 32, 64), (3, 128, 32, 32), (1, 256, 32, 16), (2, 256, 32, 128)])
+@pytest.mark.parametrize("H,D,G,P", [(2, 128, 32, 16), (1, 128, 64, 64), (3, 128, 128, 32), (2, 256, 32, 128), (1, 256, 32, 16)])
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 def test_lengths_and_sizes(H, D, G, P, dt):
     lens, nqs = [1, 9, 33, 64, 65, 200, 131, 300, 1030], [1, 9, 2, 1, 32, 30, 7, 31, 3]
@@ -39,7 +39,7 @@ def test_lengths_and_sizes(H, D, G, P, dt):
 def test_head_ratios(R, nq):
     lens, nqs = [70, 259, 400], [16, nq, 5]
     say(f"[gpu] kv4 tree of many rows R={R} n={nq}")
-    cache, ref, table, slots = build(2, 128, 32, 32, lens, "f16", 32)
+    cache, ref, table, slots = build(2, 128, 64, 32, lens, "f16", 32)
     check(cache, ref, roomy(table, 2, 32, nq * R), slots, lens, trees(nqs, 32), R, "f16")
 
 
@@ -57,14 +57,14 @@ def test_the_largest_tree(D, R):
 def test_more_tokens_than_keys(dt):
     lens, nqs = [3, 0, 20, -5, 1, 41], [9, 4, 40, 3, 2, 42]
     say(f"[gpu] kv4 tree of many rows, few keys, {dt}")
-    cache, ref, table, slots = build(2, 128, 32, 16, lens, dt, 35)
+    cache, ref, table, slots = build(2, 128, 64, 16, lens, dt, 35)
     for shape in ("bushy", "chain", "flat"):
         for window in (0, 2):
             check(cache, ref, roomy(table, 2, 16, 126), slots, lens, trees(nqs, 35, shape), 3, dt, window=window)
 
 
 @pytest.mark.parametrize("window", [1, 3, 31, 128, 30000])
-@pytest.mark.parametrize("D,G", [(128, 32), (256, 32)])
+@pytest.mark.parametrize("D,G", [(256, 32), (128, 64)])
 def test_window(window, D, G):
     """A short window leaves too few keys for such blocks: both kinds from one workspace's size."""
     lens, nqs = [300, 37, 160, 9, 400], [40, 1, 13, 9, 64]
@@ -88,34 +88,34 @@ def test_a_window_within_long_sequences():
 def test_softcap_and_scale(softcap, scale, dt):
     lens, nqs = [300, 33], [32, 20]
     say(f"[gpu] kv4 tree of many rows, softcap={softcap} scale={scale} {dt}")
-    cache, ref, table, slots = build(2, 128, 32, 16, lens, dt, 38)
+    cache, ref, table, slots = build(2, 128, 64, 16, lens, dt, 38)
     check(cache, ref, roomy(table, 2, 16, 128), slots, lens, trees(nqs, 38), 4, dt, softcap=softcap, scale=scale)
 
 
 @pytest.mark.parametrize("dt,lens,nqs", [("bf16", [5000], [57]), ("f16", [9001, 137], [64, 37]), ("bf16", [2049, 0, 4096], [3, 2, 60])])
 def test_long_keys_are_split(dt, lens, nqs):
     say(f"[gpu] kv4 tree of many rows, split {lens}")
-    cache, ref, table, slots = build(2, 128, 32, 64, lens, dt, 39)
+    cache, ref, table, slots = build(2, 128, 64, 64, lens, dt, 39)
     table = roomy(table, 2, 64, max(nqs) * 4)
     check(cache, ref, table, slots, lens, trees(nqs, 39), 4, dt)
     check(cache, ref, table, slots, lens, trees(nqs, 39), 4, dt, window=70000)
 
 
-@pytest.mark.parametrize("D", [128, 256])
-def test_what_a_token_does_not_see_does_not_reach_it(D):
+@pytest.mark.parametrize("G", [32, 64, 128])
+def test_what_a_token_does_not_see_does_not_reach_it(G):
     """NaN in a sibling's keys and values, and in one that all see."""
     import torch
-    n0, nq, R, G = 170, 32, 4, 32
+    n0, nq, R = 170, 32, 4
     lens, pars = [n0 + nq], trees([nq], 40)
-    cache, ref, table, slots = build(1, D, G, 16, lens, "bf16", 40)
+    cache, ref, table, slots = build(1, 128, G, 16, lens, "bf16", 40)
     table = roomy(table, 1, 16, nq * R)
-    q = draw((nq, R, D), "bf16", 72)
+    q = draw((nq, R, 128), "bf16", 72)
     good, _ = call(cache, q, table, lens, pars)
     for key in (n0 + 1, 75):
         seen = spec.sees(pars[0], lens[0], 0)[:, key]
         assert seen.any()
         for side in (0, 1):
-            x = torch.zeros((2, 1, 1, D), dtype=torch.bfloat16, device="cuda")
+            x = torch.zeros((2, 1, 1, 128), dtype=torch.bfloat16, device="cuda")
             x[side, 0, 0, 100] = math.nan
             kvc.kv4_append(cache, x[0], x[1], torch.from_numpy(slots[0][key:key + 1]).cuda())
             assert status(cache) == kvc.KVC_DEV_NONFINITE
@@ -125,7 +125,7 @@ def test_what_a_token_does_not_see_does_not_reach_it(D):
             assert torch.equal(out[torch.from_numpy(~seen).cuda()], good[torch.from_numpy(~seen).cuda()])
             if side:  # V's: the groups of that channel alone
                 only = torch.isnan(out).any(0).any(0).cpu().numpy()
-                assert np.array_equal(only, np.arange(D) // G == 100 // G)
+                assert np.array_equal(only, np.arange(128) // G == 100 // G)
     assert status(cache) == 0
 
 
@@ -156,7 +156,7 @@ def test_bad_parents_and_pages_are_flagged():
 def test_strides_and_rows_of_no_sequence():
     import torch
     lens, pars, R, H, D = [400, 40], trees([32, 5], 42), 4, 2, 128
-    cache, ref, table, slots = build(H, D, 32, 16, lens, "f16", 42)
+    cache, ref, table, slots = build(H, D, 64, 16, lens, "f16", 42)
     table = roomy(table, H, 16, 128)
     n_q = 41  # two before the first sequence's, two behind the last's
     big = torch.full((n_q, 3, H * R, D + 1), 7.0, dtype=torch.float16, device="cuda")
@@ -177,7 +177,7 @@ def test_strides_and_rows_of_no_sequence():
 def test_repeats_give_the_same():
     import torch
     lens, nqs = [9001, 20, 333], [32, 20, 7]
-    cache, ref, table, slots = build(2, 128, 32, 16, lens, "bf16", 43)
+    cache, ref, table, slots = build(2, 128, 64, 16, lens, "bf16", 43)
     table, pars, q = roomy(table, 2, 16, 128), trees(nqs, 43), draw((59, 8, 128), "bf16", 75)
     want, wl = call(cache, q, table, lens, pars)
     for _ in range(3):
@@ -190,7 +190,7 @@ def test_repeats_give_the_same():
 def test_tiny_and_huge_values(dt):
     """V's terms are scaled by 16 keys' largest value: of one size, and of very different ones side by side."""
     import torch
-    H, D, G, P, T, n = 1, 128, 32, 16, 200, 32
+    H, D, G, P, T, n = 1, 128, 64, 16, 200, 32
     pars = trees([n], 44)
     for kmul, vmul, qmul, uneven in ((1.0, 1e-3, 1.0, 0), (1.0, 6000.0, 1.0, 0), (1000.0, 1.0, 1e-4, 0), (1e-3, 1.0, 3e4, 0), (1.0, 30.0, 1.0, 1)):
         cache, ref = fresh(H, D, G, P, 14)
@@ -213,7 +213,7 @@ def test_sums_over_many_keys_keep_every_key(dt):
     import kv4_close
     import kv4_ref
     import torch
-    H, D, G, P, R, T, n = 2, 128, 32, 64, 4, 6000, 32
+    H, D, G, P, R, T, n = 2, 128, 64, 64, 4, 6000, 32
     pages = -(-T // P)
     cache, ref = kvc.Kv4Cache(H, D, pages, page_tokens=P, group=G), kv4_ref.Pool(H, D, G, P, pages)
     k, v, q = kv4_close.inputs((T, H, D), (n, H * R, D), dt, 60)
@@ -229,3 +229,9 @@ def test_sums_over_many_keys_keep_every_key(dt):
         wo, wl = spec.attention(q[:, hs].double().numpy(), ref.value(0, slots)[:, h], ref.value(1, slots)[:, h], ok, 0.0, D ** -0.5)
         assert kv4_close.lse_off(lse[:, hs].double().cpu().numpy(), wl) <= 1.0
         assert kv4_close.out_off(out[:, hs].double().cpu().numpy(), wo, dt) <= 1.0
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("D,G", [(128, 64), (256, 32)])
+def test_outlying_channels(D, G, dt):
+    outlying(2, D, G, 16, 4, 70, 32, dt, lambda t: roomy(t, 2, 16, 128))
