@@ -913,16 +913,20 @@ int kvc_kv4_keep(const kvc_kv4_desc *desc, const kvc_kv4_pool *pools, int32_t n_
     const int rc = make_pool(desc, a.pool);
     if (rc != KVC_OK) return rc;
     const int64_t rows = (int64_t)n_seqs * a.pool.H;  // a wave each in every pool
-    if (n_pools < 0 || n_seqs < 0 || rows >= (1 << 24) || max_pages < 0 || max_path < 0 ||
+    if (n_pools < 0 || n_pools > 4096 || n_seqs < 0 || rows >= (1 << 24) || max_pages < 0 || max_path < 0 ||
         ((int64_t)max_pages << a.pool.pshift) > ((int64_t)1 << 30) || max_path > (1 << 30))
         return KVC_ERR_ARG;
     if (n_pools == 0 || n_seqs == 0) return KVC_OK;
     if (!pools || !base || !n_keep || (!path && max_path) || (!page_table && max_pages) || !aligned(base, 4) ||
         !aligned(n_keep, 4) || !aligned(path, 4) || !aligned(page_table, 4) || (dev_status && !aligned(dev_status, 4)))
         return KVC_ERR_ARG;
-    for (int i = 0; i < n_pools; ++i)
+    for (int i = 0; i < n_pools; ++i) {
         if (!pools[i].codes || !pools[i].params || !aligned(pools[i].codes, 16) || !aligned(pools[i].params, 16))
             return KVC_ERR_ARG;
+        // two waves would move the same path, one what the other has moved
+        for (int j = 0; j < i; ++j)
+            if (pools[i].codes == pools[j].codes || pools[i].params == pools[j].params) return KVC_ERR_ARG;
+    }
     a.pool.status = dev_status;
     a.table = page_table;
     a.table_stride = table_stride;

@@ -970,10 +970,15 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_tree_wide(Kv4Attn
 template <int D, int G, bool BF>
 hipError_t attend_wide(const Kv4Attn &a, dim3 grid, hipStream_t s)
 {
-    const int lds = 2 * sizeof(Turn<D, G>) + kAhead * sizeof(Keys<D, G>) + 2 * kTreeRows + (a.max_q + 1) / 2 * 4 +
-                    4 * kTreeRows * ((a.max_q + 62) / 32);
-    // above 64 KB LDS has to be asked for; the attribute is per device, and cheap
-    const hipError_t e = hipFuncSetAttribute((const void *)k_kv4_tree_wide<D, G, BF>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    const auto lds_of = [](int max_q) {
+        return (int)(2 * sizeof(Turn<D, G>) + kAhead * sizeof(Keys<D, G>)) + 2 * kTreeRows + (max_q + 1) / 2 * 4 +
+               4 * kTreeRows * ((max_q + 62) / 32);
+    };
+    const int lds = lds_of(a.max_q);
+    // above 64 KB LDS has to be asked for; the attribute is per device, and cheap.  What the largest tree takes, always: calls of
+    // several threads must not lower it for each other.
+    const hipError_t e = hipFuncSetAttribute((const void *)k_kv4_tree_wide<D, G, BF>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                             lds_of(kTreeMost));
     if (e != hipSuccess) return e;
     k_kv4_tree_wide<D, G, BF><<<grid, dim3(256), lds, s>>>(a);
     return hipGetLastError();

@@ -599,7 +599,8 @@ int kvc_kv4_tree_attention(const kvc_kv4_desc *desc, const kvc_kv4_attn *args, c
  * base[b] + i becomes what token base[b] + path[b][i] was before the call, for
  * i < n_keep[b] (codes and parameters are moved as they are).  The sequence then
  * holds base[b] + n_keep[b] tokens; what lies behind them is left over.
- *   pools       HOST array of n_pools pools of one geometry: the layers' caches, which share the page table
+ *   pools       HOST array of n_pools (at most 4096) pools of one geometry, none of them twice: the layers'
+ *               caches, which share the page table
  *   page_table, table_stride, max_pages   as kvc_kv4_attention
  *   base        int32 [n_seqs] (device, read): tokens before the tree
  *   path        int32 [n_seqs][max_path], rows path_stride entries apart (device, read): rising, none below 0

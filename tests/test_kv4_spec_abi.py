@@ -96,6 +96,11 @@ def test_tree_workspace_covers_every_window(D, G):
                         work=OK if need else None, work_bytes=need) == kvc.KVC_ERR_HIP
 
 
+def test_keep_refuses_a_pool_given_twice():
+    assert keep(pools=(OK, OK, OK, OK + 64)) == keep(pools=(OK, OK, OK + 64, OK)) == kvc.KVC_ERR_ARG
+    assert keep(n_pools=4097) == kvc.KVC_ERR_ARG
+
+
 def test_keep_refusals():
     for kw in (dict(pools=None), dict(pools=(OK, None)), dict(pools=(None, OK)), dict(pools=(OK, OK, OK + 8, OK)),
                dict(pools=(OK, OK + 4, OK, OK)), dict(n_pools=-1), dict(table=None), dict(table=OK + 2), dict(max_pages=-1),
