@@ -518,7 +518,8 @@ __device__ __forceinline__ void turn_queries(const Kv4Pool &p, const Kv4Turn &tu
     }
 }
 
-// Blocks of K rows, of V rows, of q's.
+// Blocks of K rows, of V rows, of q's.  Bound by memory: 32768 tokens of 8 KV and 32 query heads of 128, fp16 and all of them
+// turned, 156 us, 4.7 TB/s (vector units 70% busy); 64 tokens 3.2 us, the launch and the loads' chain.
 template <int D, int G, int DT, int ITEMS, int HEADS>
 __global__ __launch_bounds__(256) void k_kv4_append_rotated(Kv4Pool p, Kv4Rows k, Kv4Rows v, Kv4Turn turn, int64_t n,
                                                              const int64_t *slots, uint32_t kv_blocks)
