@@ -235,3 +235,43 @@ def test_sums_over_many_keys_keep_every_key(dt):
 @pytest.mark.parametrize("D,G", [(128, 64), (256, 32)])
 def test_outlying_channels(D, G, dt):
     outlying(2, D, G, 16, 4, 70, 32, dt, lambda t: roomy(t, 2, 16, 128))
+
+
+def test_captured_and_on_two_streams():
+    """Replays follow what lengths, queries and parents hold then; calls on two streams at once keep to their own."""
+    import torch
+    lens, nqs, H, R = [700, 45], [32, 20], 2, 4
+    cache, ref, table, slots = build(H, 128, 64, 16, lens, "bf16", 45)
+    pars = [trees(nqs, 45 + i) for i in range(3)]
+    qs = [draw((52, H * R, 128), "bf16", 76 + i) for i in range(3)]
+    want = [call(cache, q, roomy(table, H, 16, 128), lens, p) for q, p in zip(qs, pars)]
+    tab, ln, cu = torch.from_numpy(roomy(table, H, 16, 128)).cuda(), ints(lens), ints([0, 32, 52])
+    q, par = qs[0].cuda(), ints(sum(pars[0], []))
+    nb = kvc.kv4_tree_work_bytes(cache, 52, H * R, 2, tab.shape[1], 32)
+    out, lse = torch.empty_like(q), torch.empty((52, H * R), dtype=torch.float32, device="cuda")
+    work = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    run = lambda: kvc.kv4_tree_attention(cache, q, tab, ln, par, cu_q=cu, max_q=32, out=out, lse=lse, work=work)
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for i in (1, 2, 0, 1):
+        q.copy_(qs[i])
+        par.copy_(ints(sum(pars[i], [])))
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+        again, _ = call(cache, qs[i], roomy(table, H, 16, 128), lens, pars[i])
+        assert torch.equal(again, want[i][0])
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    dev = [(a.cuda(), ints(sum(p, []))) for a, p in zip(qs, pars)]
+    torch.cuda.synchronize()
+    for i, s in enumerate(streams * 3):
+        a, p = dev[i % 2]
+        got.append(kvc.kv4_tree_attention(cache, a, tab, ln, p, cu_q=cu, max_q=32, return_lse=True, stream=s))
+    torch.cuda.synchronize()
+    for i, (o, l) in enumerate(got):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
+    assert status(cache) == 0
