@@ -303,8 +303,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv4_tree(Kv4A
         };
         // Blocks that every row sees whole in a loop of their own, two at a time: sums and keys then stay in their registers.
         // Where registers are short already the second loop costs more: 16 sequences of up to 8192 keys, 8 KV heads, trees of
-        // 96 rows, D = 128 G = 64 119 us (without 123); of 128 rows G = 32 225 (180); 8 sequences with D = 256, G = 32 551 (419),
-        // G = 64 236 (200); 64 sequences of 16 rows, which lose a third wave a SIMD, 141 (129).
+        // 96 rows, D = 128 G = 64 119 us (without 123); of 128 rows G = 32 225 (215); 8 sequences with D = 256, G = 32 551 (399),
+        // G = 64 236 (198); 64 sequences of 16 rows, which lose a third wave a SIMD, 141 (129).
         constexpr bool APART = CT > 1 && D <= 128 && 64 * D <= 128 * G;
         const int from = (max(all_lo, 0) + 31) / 32, until = min(b_end, max(j.pos0, 0) / 32);
         while (blk < b_end) {
@@ -984,9 +984,9 @@ hipError_t attend_wide(const Kv4Attn &a, dim3 grid, hipStream_t s)
     return hipGetLastError();
 }
 
-// Which shapes the wide blocks are faster for (16 sequences of up to 8192 keys, 8 KV heads, trees of 128 rows; 8 sequences
-// with D = 256): D = 128 G = 32, 64, 128: 133, 121, 118 us, tiles of 32 rows 180, 140, 124; D = 256 G = 32 341, 419.
-// The others: D = 64 G = 32, 64: 97, 100 and 93, 86; D = 256 G = 64: 228, 200.
+// Which shapes the wide blocks are faster for (16 sequences of up to 8192 keys, 8 KV heads, trees of 128 rows, bf16; 8
+// sequences with D = 256): D = 128 G = 32, 64, 128: 133, 122, 118 us, tiles of 32 rows 215, 141, 121; D = 256 G = 32 335, 399.
+// The others: D = 64 G = 32, 64: 97, 106 (trees of 96 rows 93, 86) and 93, 89; D = 256 G = 64: 228, 198.
 constexpr bool has_wide(int D, int G) { return D == 128 || (D == 256 && G == 32); }
 
 template <int D, int G, bool BF>
@@ -1048,9 +1048,11 @@ Kv4Plan kv4_tree_plan(const Kv4Pool &p, int64_t n_seqs, int R, int64_t max_q, in
     const int64_t tiles = (most + narrow - 1) / narrow, wide_tiles = (most + kTreeRows - 1) / kTreeRows;
     // a window reaches back from the tree's first token, and its keys go on to the last
     const int64_t keys = window ? std::min(max_keys, window + max_q) : max_keys;
-    // blocks of 128 rows where the longest tree gives at least 7/8 of their waves rows (three of four: trees of up to 96 rows
-    // 137 us for 124, since most are smaller) and the keys fill the chip (8 heads of 2 sequences of 2000 keys: 26 us for 23)
-    const bool wide = has_wide(p.D, p.G) && tiles * 8 >= wide_tiles * 28 && heads * wide_tiles * ((keys + 511) / 512) >= 512;
+    // blocks of 128 rows where the longest tree gives at least 7/8 of their waves rows (three of four, trees of up to 96 rows:
+    // 137 us for 124, since most are smaller; but with groups of 32 123 for 173) and the keys fill the chip (8 heads of 2
+    // sequences of 2000 keys: 26 us for 23)
+    const int64_t full = p.G == 32 ? 24 : 28;  // of 32
+    const bool wide = has_wide(p.D, p.G) && tiles * 8 >= wide_tiles * full && heads * wide_tiles * ((keys + 511) / 512) >= 512;
     plan.rows = wide ? kTreeRows : (int32_t)narrow;
     plan.tiles = (int32_t)(wide ? wide_tiles : tiles);
     plan.ns = (int32_t)splits(wide, n_seqs > 1, heads * plan.tiles, keys);

@@ -275,3 +275,12 @@ def test_captured_and_on_two_streams():
     for i, (o, l) in enumerate(got):
         assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
     assert status(cache) == 0
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("D,R,nq", [(128, 4, 17), (128, 3, 32), (256, 2, 33)])
+def test_groups_of_32_fill_fewer(D, R, nq, dt):
+    """With groups of 32 three of four waves with rows are enough, the last of them part of one."""
+    lens, nqs, H = [300, 77, 500], [nq, 3, 9], 2
+    cache, ref, table, slots = build(H, D, 32, 16, lens, dt, 46)
+    check(cache, ref, roomy(table, H, 16, 128), slots, lens, trees(nqs, 46), R, dt)
