@@ -469,7 +469,8 @@ __device__ __forceinline__ void append_turned(const Kv4Pool &p, const Kv4Rows &r
         // the D/8 lanes of a token skip it together
         const bool bad = slot[u] >= end || pos[u] >= turn.n_positions;
         if (slot[u] < 0 || pos[u] < 0 || bad) {
-            if (bad && slot[u] >= 0 && pos[u] >= 0 && i == 0) kvc_flag(p.status, KVC_DEV_BAD_INDEX);
+            // nothing of a token without a position is looked at; of one without a slot its position is
+            if (bad && pos[u] >= 0 && i == 0) kvc_flag(p.status, KVC_DEV_BAD_INDEX);
             continue;
         }
         float y[8];

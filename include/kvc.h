@@ -563,8 +563,9 @@ typedef struct kvc_kv4_rotated {
     int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride; /* elements */
     int64_t q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride;
     const int64_t *slots;     /* [n_tokens], as kvc_kv4_append; where k and v are skipped q is rotated all the same */
-    const int64_t *positions; /* [n_tokens]; a negative one skips its token, q_out's rows too (padding of a
-                                 captured batch); one past the table does so and sets KVC_DEV_BAD_INDEX */
+    const int64_t *positions; /* [n_tokens]; a negative one skips its token, whatever its slot, and q_out's rows too
+                                 (padding of a captured batch); one past the table does so, whatever its slot, and
+                                 sets KVC_DEV_BAD_INDEX */
     const float *table;       /* [n_positions][rot], 16-byte aligned */
     int64_t n_tokens, n_positions;
     int32_t n_q_heads;        /* 1..65536 with q */
