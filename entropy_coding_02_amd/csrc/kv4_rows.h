@@ -137,7 +137,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv4_prompt(Kv4Attn a)
         paths.base = j.pos0;
         paths.first = max(j.pos0, 0) >> 5;
         paths.words = max(((j.kend + 31) >> 5) - paths.first, 0);
-        if (t_end * 2 > paths.first || a.window) {  // the same for the whole block
+        // the same for the whole block; a tile without a key walks for its bad parents
+        if (t_end * 2 > paths.first || a.window || j.kend == 0) {
             stage_parents(a, j, last_row / a.R, lds_parent);
             lds_barrier();
             walk(a, paths, lds_parent, tok0, last_row / a.R, lds_steps);

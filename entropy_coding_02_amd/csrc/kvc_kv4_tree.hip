@@ -55,7 +55,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv4_tree(Kv4A
     paths.base = j.pos0;
     paths.first = max(j.pos0, 0) >> 5;
     paths.words = max(((j.kend + 31) >> 5) - paths.first, 0);
-    const bool walks = b_end > paths.first || a.window;  // the same for the whole block
+    // the same for the whole block; a tile without a key walks for its bad parents
+    const bool walks = b_end > paths.first || a.window || j.kend == 0;
     if (walks) stage_parents(a, j, tok1, lds_parent);
 
     int32_t first[2] = {0, 0}, pages[2] = {0, 0};
