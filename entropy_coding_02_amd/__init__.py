@@ -742,7 +742,7 @@ def kv4_append_rotated(cache: Kv4Cache, k, v, slots, positions, table, q=None, q
                        stream=None):
     """kv4_append with k turned by the rotation of its tokens' positions on the
     way, and q [T][Hq][D] too, into q_out (allocated if not given; q itself: in
-    place).  positions int64 [T] (negative: the token is skipped); table float32
+    place; not k's or v's rows).  positions int64 [T] (negative: the token is skipped); table float32
     [n_positions][rot]: rot/2 cosines, then rot/2 sines of each position's angles, usually
     position * base ** (-2 i / rot) computed in 64 bits; the first rot channels of a head
     are turned, as pairs (i, i + rot/2), or (2i, 2i + 1) if interleaved.  What is

@@ -884,9 +884,10 @@ int kvc_kv4_append_rotated(const kvc_kv4_desc *desc, const kvc_kv4_rotated *args
         if (!make_rows(turn.q, args->q, nullptr, args->q_token_stride, args->q_head_stride, dt) ||
             !make_rows(out, nullptr, args->q_out, args->q_out_token_stride, args->q_out_head_stride, dt))
             return KVC_ERR_ARG;
-        // in place or apart
+        // in place or apart; k and v are read by other blocks meanwhile
         if (args->q == args->q_out && (out.token_stride != turn.q.token_stride || out.head_stride != turn.q.head_stride))
             return KVC_ERR_ARG;
+        if (args->q_out == args->k || args->q_out == args->v) return KVC_ERR_ARG;
         turn.q.dst = args->q_out;
         turn.out_token_stride = out.token_stride;
         turn.out_head_stride = out.head_stride;

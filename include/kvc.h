@@ -559,7 +559,7 @@ typedef struct kvc_kv4_rotated {
     const void *k, *v;        /* [n_tokens][H][D] of dtype, as kvc_kv4_append */
     const void *q;            /* NULL, or [n_tokens][n_q_heads][D] of dtype, channels contiguous */
     void *q_out;              /* with q: as it (written); may be q itself with q's strides, else must
-                                 not overlap it, nor its rows each other */
+                                 not overlap it; its rows must not overlap k's, v's or each other */
     int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride; /* elements */
     int64_t q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride;
     const int64_t *slots;     /* [n_tokens], as kvc_kv4_append; where k and v are skipped q is rotated all the same */
