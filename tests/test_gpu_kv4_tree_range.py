@@ -17,9 +17,9 @@ import entropy_coding_02_amd as kvc
 import kv4_ref
 import kv4_spec_ref as spec
 from gpu_util import say
-from test_gpu_kv4 import EPS, f32, status, tdt
-from test_gpu_kv4_tree import call, check, ints, trees
-from test_gpu_kv4 import build
+from test_gpu_kv4 import EPS, build, f32, status, tdt
+from test_gpu_kv4_tree import call, check, trees
+from test_gpu_kv4_tree_rows import roomy
 
 pytestmark = pytest.mark.gpu
 
@@ -175,3 +175,13 @@ def test_a_window_within_long_sequences(D, G, dt, softcap):
     say(f"[gpu] kv4 tree of many rows, long windows D={D} G={G} {dt}")
     cache, ref, table, slots = build(H, D, G, 32, lens, dt, 37)
     check(cache, ref, table, slots, lens, trees(nqs, 37), 2, dt, window=2500, softcap=softcap)
+
+
+@pytest.mark.parametrize("D,G,heads,n,dt", [(256, 32, 2, 1024, "f16"), (256, 32, 1, 590, "bf16"), (128, 64, 8, 640, "f16"), (128, 128, 2, 128, "bf16"),
+                                            (128, 32, 1, 1024, "bf16")])
+def test_paths_that_fill_a_block(D, G, heads, n, dt):
+    """The largest trees whose paths a block of 128 rows still has room for, and one that goes to tiles."""
+    lens = [n + 333, n + 64]
+    say(f"[gpu] kv4 tree of {n}, {heads} heads of {D}, G={G} {dt}")
+    cache, ref, table, slots = build(1, D, G, 64, lens, dt, 38)
+    check(cache, ref, roomy(table, 1, 64, n * heads), slots, lens, [trees([n], 38)[0], trees([n], 39, "chain")[0]], heads, dt)
